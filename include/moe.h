@@ -523,6 +523,80 @@ moe_status_t moe_reshard_tp_to_ep_unpack(int32_t E_local, int32_t H, int32_t I, 
                                          const void *w13_chunks, const void *w2_chunks,
                                          void *w13, void *w2, moe_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The dense half of a transformer block, around the MoE layer: the residual
+ * addition with root-mean-square norm, the matrix product with an epilogue,
+ * and the gated feed-forward block, each with its gradient.
+ *
+ * The conventions above hold (device pointers, 16-byte alignment, nothing
+ * allocated or synchronised, host checks before any launch).  In addition:
+ * - Element types are MOE_DTYPE_*; sums, norms and accumulators are fp32.
+ * - A call with T = 0 is valid: it writes no rows, and gradients summed over
+ *   rows come out as zero (or unchanged when accumulating).
+ * - Strides are in elements between consecutive rows, multiples of 8 (16 for
+ *   MOE_DTYPE_E4M3 rows); 0 means dense rows.
+ * - Workspaces: one buffer of the operator's *_workspace_size(desc) bytes,
+ *   256-byte aligned, initialised once with moe_workspace_init(); read its
+ *   status word with moe_get_device_status().
+ */
+enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_FP16 = 1,
+  MOE_DTYPE_FP32 = 2,
+  MOE_DTYPE_E4M3 = 3 /* 8-bit codes with power-of-two block exponents */
+};
+
+typedef struct {
+  int32_t T, H;             /* rows, elements of a row */
+  int32_t dtype;            /* of every row tensor and the weight: BF16, FP16 or FP32 */
+  float eps;                /* added to the mean square, >= 0 */
+  int64_t x_stride;         /* rows of x (and dx) */
+  int64_t residual_stride;  /* rows of residual and residual_out (and sum, dresidual) */
+  int64_t y_stride;         /* rows of y (and dy) */
+} moe_norm_desc_t;
+
+/* Bytes of the backward call's workspace; 0 for an invalid descriptor. */
+size_t moe_norm_workspace_size(const moe_norm_desc_t *d);
+
+/*
+ * moe_add_rms_norm -- per row, s = x + residual, y = weight * s / sqrt(mean(s^2) + eps).
+ * The pre-norm in front of a layer's router and FFN, with the residual stream
+ * carried on.  s is normalised in fp32, before it is rounded to residual_out.
+ *   x, residual    [T,H] in; residual may be NULL (s = x)
+ *   weight         [H] in
+ *   residual_out   [T,H] out or NULL: s rounded to the type; may be x or residual
+ *                  itself (equal strides)
+ *   y              [T,H] out or NULL; may be x itself (equal strides)
+ *   y_q, scale_exp E4M3 codes [T,H] (dense) and int8 exponents [T, ceil(H/128)]
+ *                  out, both or neither NULL: per row and block of 128 elements
+ *                  the least e with max|y| <= 448 * 2^e (at least -126; 0 for a
+ *                  block of zeros), codes = y / 2^e rounded to nearest even;
+ *                  the activation form of moe_quantize_fp8's weight blocks
+ * At least one of y and y_q.  Limits: 0 <= T <= 2^20, 8 <= H <= 16384,
+ * H % 8 == 0 (MOE_ERR_UNSUPPORTED_SHAPE).  Needs no workspace.
+ */
+moe_status_t moe_add_rms_norm(const moe_norm_desc_t *d, const void *x, const void *residual,
+                              const void *weight, void *residual_out, void *y, void *y_q,
+                              int8_t *scale_exp, moe_stream_t stream);
+
+/*
+ * moe_add_rms_norm_backward -- with r = 1 / sqrt(mean(s^2) + eps), n = s r:
+ *   dx = dresidual + r (w dy - n mean(w dy n)),   dweight = sum over rows of dy n
+ * (dx is the gradient of x and of residual alike).
+ *   dy         [T,H] in, rows y_stride apart
+ *   dresidual  [T,H] in or NULL: the gradient of residual_out, rows residual_stride apart
+ *   sum        [T,H] in: s as the forward left it (residual_out), or x where
+ *              there was no residual; rows residual_stride apart
+ *   dx         [T,H] out, rows x_stride apart; may be dy or dresidual itself
+ *              (equal strides)
+ *   dweight    [H] fp32 out or NULL; summed in a fixed order
+ */
+moe_status_t moe_add_rms_norm_backward(const moe_norm_desc_t *d, const void *dy,
+                                       const void *dresidual, const void *sum, const void *weight,
+                                       void *dx, float *dweight, void *workspace, size_t ws_bytes,
+                                       moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

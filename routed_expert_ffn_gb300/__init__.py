@@ -35,6 +35,11 @@ MOE_PATH_KERNEL_CHAIN = 1
 MOE_PATH_PERSISTENT = 2
 MOE_PATH_CHAIN_ONE_SM = 3
 
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP16 = 1
+MOE_DTYPE_FP32 = 2
+MOE_DTYPE_E4M3 = 3
+
 MOE_STAGE_EVENTS = 7
 STAGE_NAMES = ("route", "dispatch", "gather", "gateup", "down", "combine")
 
@@ -77,6 +82,12 @@ class WorkspaceLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in _LAYOUT_FIELDS]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -111,6 +122,9 @@ def library() -> ctypes.CDLL:
         "moe_layer_forward_ex": ([D, ctypes.POINTER(LayerWeights), P, P, P, S, P, P, I32], I32),
         "moe_reshard_ep_to_tp_pack": ([I32, I32, I32, I32, P, P, P, P, P], I32),
         "moe_reshard_tp_to_ep_unpack": ([I32, I32, I32, I32, P, P, P, P, P], I32),
+        "moe_norm_workspace_size": ([ctypes.POINTER(NormDesc)], S),
+        "moe_add_rms_norm": ([ctypes.POINTER(NormDesc), P, P, P, P, P, P, P, P], I32),
+        "moe_add_rms_norm_backward": ([ctypes.POINTER(NormDesc), P, P, P, P, P, P, P, S, P], I32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -172,12 +186,17 @@ def moe_workspace_layout(d: LayerDesc) -> Dict[str, int]:
     return {n: int(getattr(out, n)) for n in _LAYOUT_FIELDS}
 
 
-def alloc_workspace(d: LayerDesc, device="cuda"):
-    """A zero-initialised workspace tensor (uint8) of moe_workspace_size(d) bytes."""
+_WORKSPACE_SIZE = {LayerDesc: "moe_workspace_size", NormDesc: "moe_norm_workspace_size"}
+
+
+def alloc_workspace(d, device="cuda"):
+    """A zero-initialised workspace tensor (uint8) for the calls made with ``d``: a layer's
+    descriptor (moe_workspace_size(d) bytes) or a dense operator's (its own *_workspace_size)."""
     import torch
-    n = moe_workspace_size(d)
+    fn = _WORKSPACE_SIZE[type(d)]
+    n = int(getattr(library(), fn)(ctypes.byref(d)))
     if n == 0:
-        raise MoeError("moe_workspace_size", MOE_ERR_UNSUPPORTED_SHAPE)
+        raise MoeError(fn, MOE_ERR_UNSUPPORTED_SHAPE)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     moe_workspace_init(ws)
     return ws
@@ -346,6 +365,61 @@ def moe_layer_forward_fp8(d: LayerDesc, w: LayerWeightsFp8, x, y, ws, stream=Non
     _check("moe_layer_forward_fp8", library().moe_layer_forward_fp8(
         ctypes.byref(d), ctypes.byref(w), _ptr(x), _ptr(y), _ptr(ws), _nbytes(ws),
         _stream(stream)))
+
+
+# ---------------------------------------------- dense operators --
+# Rows may be strided (the descriptor's *_stride, in elements); everything else is contiguous.
+
+def dtype_of(t) -> int:
+    """The MOE_DTYPE_* of a tensor (uint8 counts as E4M3 codes)."""
+    name = str(t.dtype)
+    try:
+        return {"torch.bfloat16": MOE_DTYPE_BF16, "torch.float16": MOE_DTYPE_FP16,
+                "torch.float32": MOE_DTYPE_FP32, "torch.float8_e4m3fn": MOE_DTYPE_E4M3,
+                "torch.uint8": MOE_DTYPE_E4M3}[name]
+    except KeyError:
+        raise ValueError(f"unsupported element type {name}") from None
+
+
+def _rows(t, stride: int, cols: int) -> Optional[int]:
+    """The pointer of a [T, cols] tensor whose rows are ``stride`` elements apart (0: cols)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dim() != 2 or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1) or (
+            t.shape[0] > 1 and t.stride(0) != (stride or cols)):
+        raise ValueError("expected a [T, cols] tensor with rows at the descriptor's stride")
+    return t.data_ptr()
+
+
+def norm_desc(T: int, H: int, dtype: int, eps: float = 1e-6, x_stride: int = 0,
+              residual_stride: int = 0, y_stride: int = 0) -> NormDesc:
+    return NormDesc(T, H, dtype, eps, x_stride, residual_stride, y_stride)
+
+
+def moe_norm_workspace_size(d: NormDesc) -> int:
+    return int(library().moe_norm_workspace_size(ctypes.byref(d)))
+
+
+def moe_add_rms_norm(d: NormDesc, x, residual, weight, residual_out, y, y_q=None, scale_exp=None,
+                     stream=None):
+    """s = x + residual; residual_out = s; y (and / or E4M3 codes y_q with exponents
+    scale_exp) = weight * s / sqrt(mean(s^2) + eps)."""
+    _check("moe_add_rms_norm", library().moe_add_rms_norm(
+        ctypes.byref(d), _rows(x, d.x_stride, d.H), _rows(residual, d.residual_stride, d.H),
+        _ptr(weight), _rows(residual_out, d.residual_stride, d.H), _rows(y, d.y_stride, d.H),
+        _ptr(y_q), _ptr(scale_exp), _stream(stream)))
+
+
+def moe_add_rms_norm_backward(d: NormDesc, dy, dresidual, sum, weight, dx, dweight, ws,
+                              stream=None):
+    """dx (of x and of residual) and dweight (fp32) of moe_add_rms_norm; ``sum`` is its
+    residual_out, ``dresidual`` the gradient of that (or None)."""
+    _check("moe_add_rms_norm_backward", library().moe_add_rms_norm_backward(
+        ctypes.byref(d), _rows(dy, d.y_stride, d.H), _rows(dresidual, d.residual_stride, d.H),
+        _rows(sum, d.residual_stride, d.H), _ptr(weight), _rows(dx, d.x_stride, d.H),
+        _ptr(dweight), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def workspace_view(ws, layout: Dict[str, int], name: str, dtype, shape):

@@ -99,9 +99,10 @@ constexpr uint32_t kStatusTimeoutRouter = 1u << 4;
 constexpr uint32_t kStatusRange = 1u << 5;  // a gate-weighted expert output beyond fp16 range
 constexpr uint32_t kStatusTimeoutCheck = 1u << 6;  // the bounded-wait check ran out (expected)
 constexpr uint32_t kStatusTimeoutLayer = 1u << 7;  // a wait of the persistent decode layer ran out
+constexpr uint32_t kStatusTimeoutDense = 1u << 8;  // a wait of a dense operator's GEMM ran out
 constexpr uint32_t kStatusTimeoutMask =
     kStatusTimeoutGateUp | kStatusTimeoutDown | kStatusTimeoutRouter | kStatusTimeoutCheck |
-    kStatusTimeoutLayer;
+    kStatusTimeoutLayer | kStatusTimeoutDense;
 
 // A bounded pipeline wait gives up after this long (the longest legitimate
 // wait is one tile's mainloop, well under a millisecond).
@@ -160,6 +161,8 @@ constexpr int kDecodeBarrierWord = kSplitCounterWord + 2 * kMaxSplitTiles;
 constexpr int kDecodePieceWord = kDecodeBarrierWord + 32;
 constexpr int kDecodeSegWord = kDecodePieceWord + 2 * kDecodeMaxCtas;
 constexpr size_t kStatusBlockBytes = (size_t)(kDecodeSegWord + kMaxE + 16) * 4;
+// The dense operators' workspaces: the same status block, then their buffers.
+constexpr size_t kStatusPad = (kStatusBlockBytes + 1023) / 1024 * 1024;
 
 // ------------------------------------------------------ argument checks --
 // Host-side validation shared by every entry point (api.cu, noalloc.cu):
@@ -293,8 +296,27 @@ cudaError_t launch_bounded_wait_check(uint32_t *status, cudaStream_t s);
 cudaError_t launch_reshard(int E_local, int H, int I, int P, const void *w13_src, void *w13_dst,
                            const void *w2_src, void *w2_dst, int unpack, cudaStream_t st);
 
+// Residual addition with RMS norm (norm.cu).  Strides as in the descriptor,
+// with no zeros left; T >= 1.
+cudaError_t launch_add_rms_norm(const moe_norm_desc_t &d, const void *x, const void *residual,
+                                const void *weight, void *residual_out, void *y, uint8_t *q,
+                                int8_t *scale, cudaStream_t s);
+size_t norm_bwd_part_bytes(const moe_norm_desc_t &d);  // fp32 column partials
+cudaError_t launch_add_rms_norm_backward(const moe_norm_desc_t &d, const void *dy, const void *dres,
+                                         const void *sum, const void *weight, void *dx,
+                                         float *dweight, float *part, cudaStream_t s);
+// out[c] (+)= sum over r < n of part[r * ld + c], in a fixed order (norm.cu).
+cudaError_t launch_column_sum(const float *part, int n, int cols, int64_t ld, float *out,
+                              int accumulate, cudaStream_t s);
+
 int num_sms();  // of the current device (cached)
 
+// Tensor map of any type and swizzle; dims/strides innermost first, strides in
+// bytes for dims 1..rank-1.  False if the encoder is unavailable or rejects
+// the arguments.
+bool encode_map(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle,
+                const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                const cuuint32_t *box);
 // bf16 tensor map with 128-byte swizzle; dims/strides innermost first,
 // strides in bytes for dims 1..rank-1.  False if the encoder is unavailable
 // or rejects the arguments.

@@ -597,6 +597,113 @@ moe_status_t moe_add_rms_norm_backward(const moe_norm_desc_t *d, const void *dy,
                                        void *dx, float *dweight, void *workspace, size_t ws_bytes,
                                        moe_stream_t stream);
 
+/* Activations of moe_linear. */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2)) */
+  MOE_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  MOE_ACT_SILU = 4       /* z / (1 + e^-z) */
+};
+
+typedef struct {
+  int32_t T, N, K;          /* rows, output columns, input columns */
+  int32_t dtype;            /* of x and w: BF16, FP16 or E4M3 */
+  int32_t out_dtype;        /* of y, residual and bias: dtype or FP32 (E4M3: BF16 or FP32) */
+  int32_t act;              /* MOE_ACT_* */
+  int64_t x_stride;         /* rows of x (and dx) */
+  int64_t residual_stride;  /* rows of residual */
+  int64_t y_stride;         /* rows of y (and dy) */
+} moe_linear_desc_t;
+
+/* Bytes of the workspace of both calls; 0 for an invalid descriptor. */
+size_t moe_linear_workspace_size(const moe_linear_desc_t *d);
+
+/*
+ * moe_linear -- y = act(x w^T + bias) + residual, in one kernel: the products
+ * in fp32 accumulators, everything after them in fp32 before the one rounding
+ * to y.
+ *   x         [T,K] in
+ *   w         [N,K] in, dense
+ *   x_scale, w_scale  MOE_DTYPE_E4M3 only (else NULL): int8 exponents
+ *             [T, ceil(K/128)] (moe_add_rms_norm's scale_exp) and
+ *             [ceil(N/128), ceil(K/128)] (moe_quantize_fp8's); the operand is
+ *             code * 2^e.  Exponents in [-127, 127].
+ *   bias      [N] in or NULL
+ *   residual  [T,N] in or NULL; may be y itself (equal strides)
+ *   preact    [T,N] fp32 out, dense, or NULL: x w^T + bias, which
+ *             moe_linear_backward needs where act is not MOE_ACT_NONE
+ *             (not with MOE_DTYPE_E4M3)
+ *   y         [T,N] out
+ * Limits: 0 <= T <= 2^20, 8 <= N, K <= 2^18, both multiples of 8 (K of 16
+ * for MOE_DTYPE_E4M3).
+ */
+moe_status_t moe_linear(const moe_linear_desc_t *d, const void *x, const int8_t *x_scale,
+                        const void *w, const int8_t *w_scale, const void *bias,
+                        const void *residual, float *preact, void *y, void *workspace,
+                        size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_linear_backward -- with z = preact and dz = dy act'(z):
+ *   dx = dz w,   dw = dz^T x,   dbias = sum over rows of dz
+ * (the gradient of residual is dy itself).  dz is rounded once to the 16-bit
+ * type, the tensor cores' operand; dbias sums it unrounded.
+ *   dy      [T,N] in, of type dtype, rows y_stride apart
+ *   preact  [T,N] fp32 in; NULL where act is MOE_ACT_NONE
+ *   dx      [T,K] out, of type dtype, rows x_stride apart, or NULL
+ *   dw      [N,K] out, of type dw_dtype (dtype or FP32), or NULL
+ *   dbias   [N] fp32 out or NULL, summed in a fixed order
+ *   accumulate  1: dw and dbias are added to what they hold, 0: written
+ * Not for MOE_DTYPE_E4M3 (MOE_ERR_INVALID_ARG).
+ */
+moe_status_t moe_linear_backward(const moe_linear_desc_t *d, const void *dy, const void *x,
+                                 const void *w, const float *preact, void *dx, void *dw,
+                                 int32_t dw_dtype, float *dbias, int32_t accumulate,
+                                 void *workspace, size_t ws_bytes, moe_stream_t stream);
+
+typedef struct {
+  int32_t T, H, I;  /* rows, hidden size, intermediate size */
+  int32_t dtype;    /* of every tensor but `saved`: BF16 or FP16 */
+} moe_ffn_desc_t;
+
+/* Bytes of the workspace of both calls; 0 for an invalid descriptor. */
+size_t moe_gated_ffn_workspace_size(const moe_ffn_desc_t *d);
+
+/*
+ * moe_gated_ffn -- the dense gated feed-forward block, the FFN of one expert
+ * over all rows, in two kernels:
+ *   g = x Wg^T, u = x Wu^T, h = SiLU(g) u      (both projections, the
+ *       activation and the product in one; h rounded once, the second
+ *       product's operand)
+ *   y = h W2^T + residual
+ *   x         [T,H] in
+ *   w13       [2I,H] in: rows [0,I) gate Wg, [I,2I) up Wu
+ *   w2        [H,I] in
+ *   residual  [T,H] in or NULL; may be y itself
+ *   saved     [T,2I] fp32 out or NULL: g then u, for the backward call (kept
+ *             unrounded: the gradients of all three weights go through them)
+ *   y         [T,H] out; not x
+ * Limits: 0 <= T <= 2^20, 8 <= H, I <= 2^17, both multiples of 8.
+ */
+moe_status_t moe_gated_ffn(const moe_ffn_desc_t *d, const void *x, const void *w13, const void *w2,
+                           const void *residual, float *saved, void *y, void *workspace,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_gated_ffn_backward -- from dy and the forward's `saved`, with s = sigmoid(g):
+ *   dh = dy W2,  h = g s u,  dg = dh u s (1 + g (1 - s)),  du = dh g s
+ *   dx = [dg du] w13,   dw13 = [dg du]^T x,   dw2 = dy^T h
+ * (the gradient of residual is dy itself).  h, dg and du are rounded once to
+ * the 16-bit type, the tensor cores' operand.
+ *   dx    [T,H] out or NULL; not dy, not x
+ *   dw13  [2I,H], dw2 [H,I] out of type dw_dtype (dtype or FP32), or NULL
+ *   accumulate  1: dw13 and dw2 are added to what they hold, 0: written
+ */
+moe_status_t moe_gated_ffn_backward(const moe_ffn_desc_t *d, const void *dy, const void *x,
+                                    const void *w13, const void *w2, const float *saved, void *dx,
+                                    void *dw13, void *dw2, int32_t dw_dtype, int32_t accumulate,
+                                    void *workspace, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

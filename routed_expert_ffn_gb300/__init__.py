@@ -40,6 +40,13 @@ MOE_DTYPE_FP16 = 1
 MOE_DTYPE_FP32 = 2
 MOE_DTYPE_E4M3 = 3
 
+MOE_ACT_NONE = 0
+MOE_ACT_RELU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_GELU_TANH = 3
+MOE_ACT_SILU = 4
+ACT_NAMES = ("none", "relu", "gelu", "gelu_tanh", "silu")
+
 MOE_STAGE_EVENTS = 7
 STAGE_NAMES = ("route", "dispatch", "gather", "gateup", "down", "combine")
 
@@ -88,6 +95,18 @@ class NormDesc(ctypes.Structure):
                 ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64)]
+
+
+class FfnDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -125,6 +144,14 @@ def library() -> ctypes.CDLL:
         "moe_norm_workspace_size": ([ctypes.POINTER(NormDesc)], S),
         "moe_add_rms_norm": ([ctypes.POINTER(NormDesc), P, P, P, P, P, P, P, P], I32),
         "moe_add_rms_norm_backward": ([ctypes.POINTER(NormDesc), P, P, P, P, P, P, P, S, P], I32),
+        "moe_linear_workspace_size": ([ctypes.POINTER(LinearDesc)], S),
+        "moe_linear": ([ctypes.POINTER(LinearDesc), P, P, P, P, P, P, P, P, P, S, P], I32),
+        "moe_linear_backward": ([ctypes.POINTER(LinearDesc), P, P, P, P, P, P, I32, P, I32, P, S,
+                                 P], I32),
+        "moe_gated_ffn_workspace_size": ([ctypes.POINTER(FfnDesc)], S),
+        "moe_gated_ffn": ([ctypes.POINTER(FfnDesc), P, P, P, P, P, P, P, S, P], I32),
+        "moe_gated_ffn_backward": ([ctypes.POINTER(FfnDesc), P, P, P, P, P, P, P, P, I32, I32, P,
+                                    S, P], I32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -186,7 +213,9 @@ def moe_workspace_layout(d: LayerDesc) -> Dict[str, int]:
     return {n: int(getattr(out, n)) for n in _LAYOUT_FIELDS}
 
 
-_WORKSPACE_SIZE = {LayerDesc: "moe_workspace_size", NormDesc: "moe_norm_workspace_size"}
+_WORKSPACE_SIZE = {LayerDesc: "moe_workspace_size", NormDesc: "moe_norm_workspace_size",
+                   LinearDesc: "moe_linear_workspace_size",
+                   FfnDesc: "moe_gated_ffn_workspace_size"}
 
 
 def alloc_workspace(d, device="cuda"):
@@ -420,6 +449,73 @@ def moe_add_rms_norm_backward(d: NormDesc, dy, dresidual, sum, weight, dx, dweig
         ctypes.byref(d), _rows(dy, d.y_stride, d.H), _rows(dresidual, d.residual_stride, d.H),
         _rows(sum, d.residual_stride, d.H), _ptr(weight), _rows(dx, d.x_stride, d.H),
         _ptr(dweight), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def linear_desc(T: int, N: int, K: int, dtype: int, act="none", out_dtype: int = None,
+                x_stride: int = 0, residual_stride: int = 0, y_stride: int = 0) -> LinearDesc:
+    """``act``: a name of ACT_NAMES or MOE_ACT_*; ``out_dtype``: default ``dtype`` (bf16 for E4M3)."""
+    if isinstance(act, str):
+        act = ACT_NAMES.index(act)
+    if out_dtype is None:
+        out_dtype = MOE_DTYPE_BF16 if dtype == MOE_DTYPE_E4M3 else dtype
+    return LinearDesc(T, N, K, dtype, out_dtype, act, x_stride, residual_stride, y_stride)
+
+
+def moe_linear_workspace_size(d: LinearDesc) -> int:
+    return int(library().moe_linear_workspace_size(ctypes.byref(d)))
+
+
+def moe_linear(d: LinearDesc, x, w, bias, residual, y, ws, preact=None, x_scale=None,
+               w_scale=None, stream=None):
+    """y = act(x w^T + bias) + residual (``preact``: x w^T + bias in fp32 as well); E4M3 codes
+    come with their block exponents ``x_scale`` and ``w_scale``."""
+    _check("moe_linear", library().moe_linear(
+        ctypes.byref(d), _rows(x, d.x_stride, d.K), _ptr(x_scale), _ptr(w), _ptr(w_scale),
+        _ptr(bias), _rows(residual, d.residual_stride, d.N), _ptr(preact),
+        _rows(y, d.y_stride, d.N), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _grad_dtype(d, *grads) -> int:
+    """The element type of the weight gradients (all of one type)."""
+    kinds = {d.dtype if isinstance(g, int) else dtype_of(g) for g in grads if g is not None}
+    if len(kinds) > 1:
+        raise ValueError("weight gradients of different types")
+    return kinds.pop() if kinds else d.dtype
+
+
+def moe_linear_backward(d: LinearDesc, dy, x, w, preact, dx, dw, dbias, ws,
+                        accumulate: bool = False, stream=None):
+    """dx, dw (in the type of x or fp32) and dbias (fp32) of moe_linear; any of them may be None."""
+    _check("moe_linear_backward", library().moe_linear_backward(
+        ctypes.byref(d), _rows(dy, d.y_stride, d.N), _rows(x, d.x_stride, d.K), _ptr(w),
+        _ptr(preact) if d.act != MOE_ACT_NONE else None, _rows(dx, d.x_stride, d.K), _ptr(dw),
+        _grad_dtype(d, dw), _ptr(dbias), 1 if accumulate else 0, _ptr(ws), _nbytes(ws),
+        _stream(stream)))
+
+
+def ffn_desc(T: int, H: int, I: int, dtype: int) -> FfnDesc:
+    return FfnDesc(T, H, I, dtype)
+
+
+def moe_gated_ffn_workspace_size(d: FfnDesc) -> int:
+    return int(library().moe_gated_ffn_workspace_size(ctypes.byref(d)))
+
+
+def moe_gated_ffn(d: FfnDesc, x, w13, w2, residual, saved, y, ws, stream=None):
+    """y = (SiLU(x Wg^T) * (x Wu^T)) W2^T + residual; ``saved`` ([T,2I] fp32 or None) is what
+    moe_gated_ffn_backward needs of it."""
+    _check("moe_gated_ffn", library().moe_gated_ffn(
+        ctypes.byref(d), _ptr(x), _ptr(w13), _ptr(w2), _ptr(residual), _ptr(saved), _ptr(y),
+        _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_gated_ffn_backward(d: FfnDesc, dy, x, w13, w2, saved, dx, dw13, dw2, ws,
+                           accumulate: bool = False, stream=None):
+    """dx, dw13 and dw2 (in the type of x, or both in fp32) of moe_gated_ffn; any may be None."""
+    _check("moe_gated_ffn_backward", library().moe_gated_ffn_backward(
+        ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(saved), _ptr(dx), _ptr(dw13),
+        _ptr(dw2), _grad_dtype(d, dw13, dw2), 1 if accumulate else 0, _ptr(ws), _nbytes(ws),
+        _stream(stream)))
 
 
 def workspace_view(ws, layout: Dict[str, int], name: str, dtype, shape):

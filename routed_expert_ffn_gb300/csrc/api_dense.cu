@@ -3,7 +3,7 @@
 // argument are in include/moe.h.
 #include <stdint.h>
 
-#include "moe_internal.cuh"
+#include "dense.cuh"
 
 namespace moe {
 
@@ -37,6 +37,107 @@ moe_status_t norm_desc(const moe_norm_desc_t *in, moe_norm_desc_t *d) {
       !fix_stride(&d->y_stride, d->H, 8))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
+}
+
+moe_status_t linear_desc(const moe_linear_desc_t *in, moe_linear_desc_t *d) {
+  if (in == nullptr) return MOE_ERR_INVALID_ARG;
+  *d = *in;
+  const bool e4m3 = d->dtype == MOE_DTYPE_E4M3;
+  if (d->dtype != MOE_DTYPE_BF16 && d->dtype != MOE_DTYPE_FP16 && !e4m3) return MOE_ERR_INVALID_ARG;
+  if (d->out_dtype != (e4m3 ? (int32_t)MOE_DTYPE_BF16 : d->dtype) &&
+      d->out_dtype != MOE_DTYPE_FP32)
+    return MOE_ERR_INVALID_ARG;
+  if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_SILU) return MOE_ERR_INVALID_ARG;
+  const int32_t most = 1 << 18;
+  if (d->T < 0 || d->T > kMaxT || d->N < 8 || d->N > most || d->N % 8 != 0 || d->K < 8 ||
+      d->K > most || d->K % (e4m3 ? 16 : 8) != 0)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!fix_stride(&d->x_stride, d->K, e4m3 ? 16 : 8) || !fix_stride(&d->residual_stride, d->N, 8) ||
+      !fix_stride(&d->y_stride, d->N, 8))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+size_t pad(size_t n) { return (n + 1023) / 1024 * 1024; }
+
+// After the status block: the 16-bit operands of E4M3 products, or dz and the
+// column partials of the gradient.
+struct LinearWs {
+  size_t a, b, total;
+};
+LinearWs linear_ws(const moe_linear_desc_t &d) {
+  LinearWs w;
+  w.a = kStatusPad;
+  if (d.dtype == MOE_DTYPE_E4M3) {
+    w.b = w.a + pad((size_t)d.T * d.K * 2);
+    w.total = w.b + pad((size_t)d.N * d.K * 2);
+  } else {
+    w.b = w.a + (d.act == MOE_ACT_NONE ? 0 : pad((size_t)d.T * d.N * 2));
+    w.total = w.b + pad((size_t)act_grad_slices(d.T, d.N) * d.N * 4);
+  }
+  return w;
+}
+
+moe_status_t ffn_desc(const moe_ffn_desc_t *d) {
+  if (d == nullptr) return MOE_ERR_INVALID_ARG;
+  if (d->dtype != MOE_DTYPE_BF16 && d->dtype != MOE_DTYPE_FP16) return MOE_ERR_INVALID_ARG;
+  const int32_t most = 1 << 17;
+  if (d->T < 0 || d->T > kMaxT || d->H < 8 || d->H > most || d->H % 8 != 0 || d->I < 8 ||
+      d->I > most || d->I % 8 != 0)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+struct FfnWs {
+  size_t h, dgu, total;
+};
+FfnWs ffn_ws(const moe_ffn_desc_t &d) {
+  FfnWs w;
+  w.h = kStatusPad;
+  w.dgu = w.h + pad((size_t)d.T * d.I * 2);
+  w.total = w.dgu + pad((size_t)d.T * d.I * 4);
+  return w;
+}
+
+uint8_t *at(void *ws, size_t off) { return static_cast<uint8_t *>(ws) + off; }
+
+// D[M,N] = A B with fp32 accumulators: the fields every product shares.
+DenseGemm product(int M, int N, int K, int dtype, const void *a, int64_t lda, bool a_mn,
+                  const void *b, int64_t ldb, bool b_mn, void *d, int64_t ldd, int out_dtype,
+                  void *ws) {
+  DenseGemm g = {};
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.epi = kEpiLinear;
+  g.dtype = dtype;
+  g.out_dtype = out_dtype;
+  g.act = MOE_ACT_NONE;
+  g.a = a;
+  g.lda = lda;
+  g.a_mn = a_mn;
+  g.b = b;
+  g.ldb = ldb;
+  g.b_mn = b_mn;
+  g.d = d;
+  g.ldd = ldd;
+  g.status = static_cast<uint32_t *>(ws);
+  return g;
+}
+
+// dw[M,N] (+)= a^T b over T rows; T = 0 leaves zeros, or what is accumulated.
+cudaError_t weight_grad(int M, int N, int T, int dtype, const void *a, int64_t lda, const void *b,
+                        int64_t ldb, void *dw, int dw_dtype, int accumulate, void *ws,
+                        cudaStream_t s) {
+  if (T == 0)
+    return accumulate ? cudaSuccess
+                      : cudaMemsetAsync(dw, 0, (size_t)M * N * (dw_dtype == MOE_DTYPE_FP32 ? 4 : 2), s);
+  DenseGemm g = product(M, N, T, dtype, a, lda, true, b, ldb, true, dw, N, dw_dtype, ws);
+  if (accumulate) {
+    g.residual = dw;
+    g.ldr = N;
+  }
+  return launch_dense_pair(g, s);
 }
 
 }  // namespace
@@ -97,6 +198,168 @@ moe_status_t moe_add_rms_norm_backward(const moe_norm_desc_t *in, const void *dy
   if ((st = check_device()) != MOE_OK) return st;
   return cuda_status(launch_add_rms_norm_backward(d, dy, dresidual, sum, weight, dx, dweight, part,
                                                   (cudaStream_t)stream));
+}
+
+size_t moe_linear_workspace_size(const moe_linear_desc_t *in) {
+  moe_linear_desc_t d;
+  return linear_desc(in, &d) == MOE_OK ? linear_ws(d).total : 0;
+}
+
+moe_status_t moe_linear(const moe_linear_desc_t *in, const void *x, const int8_t *x_scale,
+                        const void *w, const int8_t *w_scale, const void *bias,
+                        const void *residual, float *preact, void *y, void *workspace,
+                        size_t ws_bytes, moe_stream_t stream) {
+  moe_linear_desc_t d;
+  moe_status_t st = linear_desc(in, &d);
+  if (st != MOE_OK) return st;
+  const LinearWs L = linear_ws(d);
+  if ((st = check_ws(workspace, ws_bytes, L.total)) != MOE_OK) return st;
+  if (d.T == 0) return MOE_OK;  // empty tensors may have no address
+  const bool e4m3 = d.dtype == MOE_DTYPE_E4M3;
+  if (!ok_ptr(x) || !ok_ptr(w) || !ok_opt(bias) || !ok_opt(residual) || !ok_opt(preact) ||
+      !ok_ptr(y))
+    return MOE_ERR_INVALID_ARG;
+  if ((x_scale != nullptr) != e4m3 || (w_scale != nullptr) != e4m3) return MOE_ERR_INVALID_ARG;
+  if (e4m3 && preact != nullptr) return MOE_ERR_INVALID_ARG;
+  if (residual == y && d.residual_stride != d.y_stride) return MOE_ERR_INVALID_ARG;
+  if (y == x || y == w) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device()) != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  DenseGemm g = product(d.T, d.N, d.K, d.dtype, x, d.x_stride, false, w, d.K, false, y, d.y_stride,
+                        d.out_dtype, workspace);
+  cudaError_t e = cudaSuccess;
+  if (e4m3) {
+    e = launch_widen_e4m3(x, d.x_stride, x_scale, 1, d.T, d.K, at(workspace, L.a), s);
+    if (e == cudaSuccess)
+      e = launch_widen_e4m3(w, d.K, w_scale, 128, d.N, d.K, at(workspace, L.b), s);
+    g.dtype = MOE_DTYPE_BF16;
+    g.a = at(workspace, L.a);
+    g.lda = d.K;
+    g.b = at(workspace, L.b);
+  }
+  g.act = d.act;
+  g.bias = bias;
+  g.residual = residual;
+  g.ldr = d.residual_stride;
+  g.preact = preact;
+  if (e == cudaSuccess) e = launch_dense_pair(g, s);
+  return cuda_status(e);
+}
+
+moe_status_t moe_linear_backward(const moe_linear_desc_t *in, const void *dy, const void *x,
+                                 const void *w, const float *preact, void *dx, void *dw,
+                                 int32_t dw_dtype, float *dbias, int32_t accumulate,
+                                 void *workspace, size_t ws_bytes, moe_stream_t stream) {
+  moe_linear_desc_t d;
+  moe_status_t st = linear_desc(in, &d);
+  if (st != MOE_OK) return st;
+  if (d.dtype == MOE_DTYPE_E4M3) return MOE_ERR_INVALID_ARG;
+  if (dw_dtype != d.dtype && dw_dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  const LinearWs L = linear_ws(d);
+  if ((st = check_ws(workspace, ws_bytes, L.total)) != MOE_OK) return st;
+  const bool act = d.act != MOE_ACT_NONE;
+  if (!ok_opt(dw) || !ok_opt(dbias)) return MOE_ERR_INVALID_ARG;
+  if (d.T > 0) {
+    if (!ok_ptr(dy) || !ok_opt(dx) || (act ? !ok_ptr(preact) : preact != nullptr))
+      return MOE_ERR_INVALID_ARG;
+    if ((dx != nullptr && !ok_ptr(w)) || (dw != nullptr && !ok_ptr(x))) return MOE_ERR_INVALID_ARG;
+    if (dx != nullptr && (dx == dy || dx == x || dx == w)) return MOE_ERR_INVALID_ARG;
+  }
+  if ((st = check_device()) != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  float *part = reinterpret_cast<float *>(at(workspace, L.b));
+  const void *dz = act ? at(workspace, L.a) : dy;
+  const int64_t ldz = act ? d.N : d.y_stride;
+  cudaError_t e = cudaSuccess;
+  if (d.T > 0 && (dbias != nullptr || (act && (dx != nullptr || dw != nullptr))))
+    e = launch_act_grad(dy, d.y_stride, preact, d.T, d.N, d.act, d.dtype,
+                        act ? at(workspace, L.a) : nullptr, dbias != nullptr ? part : nullptr, s);
+  if (e == cudaSuccess && dbias != nullptr)
+    e = launch_column_sum(part, d.T > 0 ? act_grad_slices(d.T, d.N) : 0, d.N, d.N, dbias,
+                          accumulate, s);
+  if (e == cudaSuccess && dx != nullptr && d.T > 0)
+    e = launch_dense_pair(product(d.T, d.K, d.N, d.dtype, dz, ldz, false, w, d.K, true, dx,
+                                  d.x_stride, d.dtype, workspace),
+                          s);
+  if (e == cudaSuccess && dw != nullptr)
+    e = weight_grad(d.N, d.K, d.T, d.dtype, dz, ldz, x, d.x_stride, dw, dw_dtype, accumulate,
+                    workspace, s);
+  return cuda_status(e);
+}
+
+size_t moe_gated_ffn_workspace_size(const moe_ffn_desc_t *d) {
+  return ffn_desc(d) == MOE_OK ? ffn_ws(*d).total : 0;
+}
+
+moe_status_t moe_gated_ffn(const moe_ffn_desc_t *d, const void *x, const void *w13, const void *w2,
+                           const void *residual, float *saved, void *y, void *workspace,
+                           size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = ffn_desc(d);
+  if (st != MOE_OK) return st;
+  const FfnWs L = ffn_ws(*d);
+  if ((st = check_ws(workspace, ws_bytes, L.total)) != MOE_OK) return st;
+  if (d->T == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(w13) || !ok_ptr(w2) || !ok_opt(residual) || !ok_opt(saved) ||
+      !ok_ptr(y))
+    return MOE_ERR_INVALID_ARG;
+  if (y == x || y == w13 || y == w2) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device()) != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  DenseGemm up = product(d->T, d->I, d->H, d->dtype, x, d->H, false, w13, d->H, false,
+                         at(workspace, L.h), d->I, d->dtype, workspace);
+  up.epi = kEpiGated;
+  up.saved = saved;
+  cudaError_t e = launch_dense_pair(up, s);
+  DenseGemm down = product(d->T, d->H, d->I, d->dtype, at(workspace, L.h), d->I, false, w2, d->I,
+                           false, y, d->H, d->dtype, workspace);
+  down.residual = residual;
+  down.ldr = d->H;
+  if (e == cudaSuccess) e = launch_dense_pair(down, s);
+  return cuda_status(e);
+}
+
+moe_status_t moe_gated_ffn_backward(const moe_ffn_desc_t *d, const void *dy, const void *x,
+                                    const void *w13, const void *w2, const float *saved, void *dx,
+                                    void *dw13, void *dw2, int32_t dw_dtype, int32_t accumulate,
+                                    void *workspace, size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = ffn_desc(d);
+  if (st != MOE_OK) return st;
+  if (dw_dtype != d->dtype && dw_dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  const FfnWs L = ffn_ws(*d);
+  if ((st = check_ws(workspace, ws_bytes, L.total)) != MOE_OK) return st;
+  if (!ok_opt(dw13) || !ok_opt(dw2)) return MOE_ERR_INVALID_ARG;
+  if (d->T > 0) {
+    if (!ok_ptr(dy) || !ok_ptr(w2) || !ok_ptr(saved) || !ok_opt(dx)) return MOE_ERR_INVALID_ARG;
+    if ((dx != nullptr && !ok_ptr(w13)) || (dw13 != nullptr && !ok_ptr(x)))
+      return MOE_ERR_INVALID_ARG;
+    if (dx != nullptr && (dx == dy || dx == x || dx == w13 || dx == w2)) return MOE_ERR_INVALID_ARG;
+  }
+  if ((st = check_device()) != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  void *h = at(workspace, L.h), *dgu = at(workspace, L.dgu);
+  const int T = d->T, H = d->H, I = d->I;
+  cudaError_t e = cudaSuccess;
+  if (T > 0 && (dx != nullptr || dw13 != nullptr || dw2 != nullptr)) {
+    DenseGemm g = product(T, I, H, d->dtype, dy, H, false, w2, I, true, nullptr, 0, d->dtype,
+                          workspace);
+    g.epi = kEpiGatedGrad;
+    g.saved = const_cast<float *>(saved);
+    g.dgu = dgu;
+    g.h = h;
+    e = launch_dense_pair(g, s);
+  }
+  if (e == cudaSuccess && dx != nullptr && T > 0)
+    e = launch_dense_pair(product(T, H, 2 * I, d->dtype, dgu, 2 * (int64_t)I, false, w13, H, true,
+                                  dx, H, d->dtype, workspace),
+                          s);
+  if (e == cudaSuccess && dw13 != nullptr)
+    e = weight_grad(2 * I, H, T, d->dtype, dgu, 2 * (int64_t)I, x, H, dw13, dw_dtype, accumulate,
+                    workspace, s);
+  if (e == cudaSuccess && dw2 != nullptr)
+    e = weight_grad(H, I, T, d->dtype, dy, H, h, I, dw2, dw_dtype, accumulate, workspace, s);
+  return cuda_status(e);
 }
 
 }  // extern "C"

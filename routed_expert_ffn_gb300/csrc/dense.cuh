@@ -1,0 +1,155 @@
+// Shared by the dense operators' GEMMs (dense_pair.cu, dense_small.cu): the
+// description of a launch, activations, and the packing of output elements.
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// What is done with the accumulator before it is stored.
+//   kEpiLinear  D = act(acc + bias) + residual; acc + bias to `preact` if asked
+//   kEpiGated   the accumulators g and u of a gate and an up column: h = silu(g) u;
+//               g and u to `saved` if asked
+//   kEpiGatedGrad  acc = dh with g and u from `saved`: dg, du and h
+enum { kEpiLinear = 0, kEpiGated = 1, kEpiGatedGrad = 2 };
+
+// One product D[M,N] = sum over k of A(m,k) B(n,k), row-major D.
+// An operand is K-major (rows of K elements, `ld` apart) or MN-major (its K
+// index runs over the rows, `ld` apart): gradients read the same tensors as
+// the forward product, without a transposed copy.
+struct DenseGemm {
+  int M, N, K;      // kEpiGated: N = columns of h (I)
+  int epi;
+  int dtype;        // A and B: MOE_DTYPE_BF16, FP16 or E4M3
+  int out_dtype;    // D (kEpiLinear): BF16, FP16 or FP32
+  int act;          // kEpiLinear
+  bool a_mn, b_mn;  // MN-major operands
+  const void *a, *b;
+  int64_t lda, ldb;
+  const void *bias, *residual;  // out_dtype; residual rows ldr apart; may be null
+  void *d;                      // rows ldd apart; kEpiGatedGrad: null
+  int64_t ldr, ldd;
+  float *preact;  // kEpiLinear: [M][N] fp32 or null
+  float *saved;   // [M][2N] fp32: g then u.  kEpiGated: out or null; kEpiGatedGrad: in
+  void *dgu, *h;  // kEpiGatedGrad: [M][2N] and [M][N] out
+  const int8_t *a_scale, *b_scale;  // E4M3: exponents [M][ceil(K/128)], [ceil(N/128)][ceil(K/128)]
+  uint32_t *status;
+};
+
+// Prefill and training sizes: 256-row tiles on CTA pairs (dense_pair.cu).
+cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s);
+// Up to kSmallRows rows: weight rows as the MMA's M, rows of A as its N, K
+// split over a cluster (dense_small.cu).  K-major operands, no preact/saved.
+constexpr int kSmallRows = 256;
+cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s);
+
+// dz = dy act'(z) in 16 bits (dz null: not written; z null: dz = dy) and the
+// column sums of each slice of the rows (part [slices][N], or null).
+int act_grad_slices(int T, int N);
+cudaError_t launch_act_grad(const void *dy, int64_t ldy, const float *z, int T, int N, int act,
+                            int dtype, void *dz, float *part, cudaStream_t s);
+// dst[r][c] = code * 2^e as bf16, for E4M3 codes with one exponent to each
+// block of `block_rows` rows by 128 columns; exact (4 significant bits).
+cudaError_t launch_widen_e4m3(const void *src, int64_t ld, const int8_t *scale, int block_rows,
+                              int64_t rows, int cols, void *dst, cudaStream_t s);
+
+// ------------------------------------------------------------ element types --
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Two fp32 values to a word of the 16-bit output type (round to nearest even).
+__device__ __forceinline__ uint32_t pack16(int dtype, float lo, float hi) {
+  return dtype == MOE_DTYPE_FP16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ float2 unpack16(int dtype, uint32_t w) {
+  if (dtype == MOE_DTYPE_FP16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// -------------------------------------------------------------- activations --
+
+constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluC1 = 0.044715f;
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+__device__ __forceinline__ float activate(int act, float z) {
+  switch (act) {
+    // comparisons that let a NaN through
+    case MOE_ACT_RELU: return z < 0.f ? 0.f : z;
+    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case MOE_ACT_GELU_TANH: {
+      // 1/2 (1 + tanh v) = sigmoid(2 v)
+      return z * sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
+    }
+    case MOE_ACT_SILU: return z * sigmoid(z);
+    default: return z;
+  }
+}
+
+// The activation's slope at z.
+__device__ __forceinline__ float activate_slope(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+    case MOE_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) +
+             z * __expf(-0.5f * z * z) * 0.3989422804014327f;  // 1 / sqrt(2 pi)
+    case MOE_ACT_GELU_TANH: {
+      // with p = sigmoid(2v): p + 2 z p (1 - p) dv/dz
+      const float p = sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
+      return p + 2.0f * z * p * (1.0f - p) * kGeluC0 * (1.0f + 3.0f * kGeluC1 * z * z);
+    }
+    case MOE_ACT_SILU: {
+      const float p = sigmoid(z);
+      return p * (1.0f + z * (1.0f - p));
+    }
+    default: return 1.f;
+  }
+}
+
+// ------------------------------------------------------------ MMA operands --
+
+// Instruction descriptor of kind::f16 with fp32 accumulators for either 16-bit
+// type and majorness (bits 7-9 and 10-12: 0 fp16, 1 bf16; bits 15, 16: MN-major).
+__host__ __device__ constexpr uint32_t idesc_16(int dtype, bool a_mn, bool b_mn, int M, int N) {
+  const uint32_t f = dtype == MOE_DTYPE_BF16 ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of an MN-major operand in 128-byte swizzled boxes
+// of 64 MN elements by 64 K rows (8 KB): K groups of 8 rows 1024 bytes apart
+// (stride offset), boxes of 64 MN elements 8192 bytes apart (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(8192 >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// 32 lanes x 32 consecutive 32-bit columns; thread i gets lane (base + i).
+// The wait is part of the same statement: no use can move in front of it.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&f)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+}  // namespace moe

@@ -47,3 +47,22 @@ def rms_norm(x, residual, weight, eps):
     """(s, y) in 64 bits."""
     s = x.double() + (residual.double() if residual is not None else 0.0)
     return s, s / torch.sqrt(s.square().mean(1, keepdim=True) + eps) * weight.double()
+
+
+def activation(z, act):
+    f = torch.nn.functional
+    return {"none": lambda v: v, "relu": f.relu, "gelu": f.gelu, "silu": f.silu,
+            "gelu_tanh": lambda v: f.gelu(v, approximate="tanh")}[act](z)
+
+
+def product_bound(a, b, K):
+    """What fp32 accumulation of K exact products may be off by, for a [M,K] and b [N,K] in 64
+    bits: every addition at most one step (2^-23) of the running sum, itself at most the sum of
+    the products' magnitudes; the tensor cores add 16 products (or 32) at a time."""
+    return (a.abs() @ b.abs().t()) * ((K / 8 + 8) * 2.0 ** -23)
+
+
+def rel_l2(got, want):
+    g, w = got.double(), want.double()
+    n = float(w.norm())
+    return float((g - w).norm()) / n if n else float((g - w).norm())

@@ -125,6 +125,13 @@ DenseGemm product(int M, int N, int K, int dtype, const void *a, int64_t lda, bo
   return g;
 }
 
+// The forward products by their number of rows.  preact and saved are stored
+// by the tiled kernel only.
+cudaError_t forward(const DenseGemm &g, cudaStream_t s) {
+  const bool few = g.M <= kSmallRows && g.preact == nullptr && g.saved == nullptr;
+  return few ? launch_dense_small(g, s) : launch_dense_pair(g, s);
+}
+
 // dw[M,N] (+)= a^T b over T rows; T = 0 leaves zeros, or what is accumulated.
 cudaError_t weight_grad(int M, int N, int T, int dtype, const void *a, int64_t lda, const void *b,
                         int64_t ldb, void *dw, int dw_dtype, int accumulate, void *ws,
@@ -227,8 +234,10 @@ moe_status_t moe_linear(const moe_linear_desc_t *in, const void *x, const int8_t
   cudaStream_t s = (cudaStream_t)stream;
   DenseGemm g = product(d.T, d.N, d.K, d.dtype, x, d.x_stride, false, w, d.K, false, y, d.y_stride,
                         d.out_dtype, workspace);
+  g.a_scale = x_scale;
+  g.b_scale = w_scale;
   cudaError_t e = cudaSuccess;
-  if (e4m3) {
+  if (e4m3 && d.T > kSmallRows) {
     e = launch_widen_e4m3(x, d.x_stride, x_scale, 1, d.T, d.K, at(workspace, L.a), s);
     if (e == cudaSuccess)
       e = launch_widen_e4m3(w, d.K, w_scale, 128, d.N, d.K, at(workspace, L.b), s);
@@ -242,7 +251,7 @@ moe_status_t moe_linear(const moe_linear_desc_t *in, const void *x, const int8_t
   g.residual = residual;
   g.ldr = d.residual_stride;
   g.preact = preact;
-  if (e == cudaSuccess) e = launch_dense_pair(g, s);
+  if (e == cudaSuccess) e = forward(g, s);
   return cuda_status(e);
 }
 
@@ -310,12 +319,12 @@ moe_status_t moe_gated_ffn(const moe_ffn_desc_t *d, const void *x, const void *w
                          at(workspace, L.h), d->I, d->dtype, workspace);
   up.epi = kEpiGated;
   up.saved = saved;
-  cudaError_t e = launch_dense_pair(up, s);
+  cudaError_t e = forward(up, s);
   DenseGemm down = product(d->T, d->H, d->I, d->dtype, at(workspace, L.h), d->I, false, w2, d->I,
                            false, y, d->H, d->dtype, workspace);
   down.residual = residual;
   down.ldr = d->H;
-  if (e == cudaSuccess) e = launch_dense_pair(down, s);
+  if (e == cudaSuccess) e = forward(down, s);
   return cuda_status(e);
 }
 

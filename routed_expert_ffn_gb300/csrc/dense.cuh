@@ -73,7 +73,8 @@ __device__ __forceinline__ float2 unpack16(int dtype, uint32_t w) {
 constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluC1 = 0.044715f;
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// the approximate division: 2 ulp, and 0 where 1 + e^-z overflows
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
 __device__ __forceinline__ float activate(int act, float z) {
   switch (act) {
@@ -89,6 +90,23 @@ __device__ __forceinline__ float activate(int act, float z) {
   }
 }
 
+// All of an array, the choice made once.
+template <int kAct, int kN>
+__device__ __forceinline__ void activate_as(float (&f)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) f[i] = activate(kAct, f[i]);
+}
+template <int kN>
+__device__ __forceinline__ void activate_all(int act, float (&f)[kN]) {
+  switch (act) {
+    case MOE_ACT_RELU: return activate_as<MOE_ACT_RELU>(f);
+    case MOE_ACT_GELU: return activate_as<MOE_ACT_GELU>(f);
+    case MOE_ACT_GELU_TANH: return activate_as<MOE_ACT_GELU_TANH>(f);
+    case MOE_ACT_SILU: return activate_as<MOE_ACT_SILU>(f);
+    default: return;
+  }
+}
+
 // The activation's slope at z.
 __device__ __forceinline__ float activate_slope(int act, float z) {
   switch (act) {
@@ -97,9 +115,11 @@ __device__ __forceinline__ float activate_slope(int act, float z) {
       return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) +
              z * __expf(-0.5f * z * z) * 0.3989422804014327f;  // 1 / sqrt(2 pi)
     case MOE_ACT_GELU_TANH: {
-      // with p = sigmoid(2v): p + 2 z p (1 - p) dv/dz
+      // with p = sigmoid(2v): p + 2 z p (1 - p) dv/dz; beyond |z| = 30 the
+      // second term is zero, and z^2 does not overflow
       const float p = sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
-      return p + 2.0f * z * p * (1.0f - p) * kGeluC0 * (1.0f + 3.0f * kGeluC1 * z * z);
+      const float c = fminf(fmaxf(z, -30.f), 30.f);
+      return p + 2.0f * c * p * (1.0f - p) * kGeluC0 * (1.0f + 3.0f * kGeluC1 * c * c);
     }
     case MOE_ACT_SILU: {
       const float p = sigmoid(z);
@@ -150,6 +170,102 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&f)[32]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&f)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+// ------------------------------------------------ block-scaled E4M3 products --
+
+// Instruction descriptor of kind::mxf8f6f4: E4M3 operands (types 0), both
+// K-major, scale factors UE8M0 (bit 23), scale-factor bytes 0 of both, N >> 3
+// in bits 17-22, M >> 7 in bits 27-28.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
+  return ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
+}
+
+// Scale-factor columns of a stage: 4 for 128 rows of A, 8 for 256 rows of B.
+constexpr uint32_t kSmallSfCols = 12;
+
+// A block exponent as four equal UE8M0 bytes (2^(byte - 127)).
+__device__ __forceinline__ uint32_t e8m0x4(int8_t e) {
+  return (uint32_t)((int)e + 127) * 0x01010101u;
+}
+
+// D (+)= (A * 2^sfa) (B * 2^sfb)^T, 32 of K, one CTA.
+__device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+          "r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// This warp's 32 lanes x 4 or 8 columns.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::
+                   "r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------- tensor maps --
+
+inline CUtensorMapDataType map_type(int dtype) {
+  switch (dtype) {
+    case MOE_DTYPE_BF16: return CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    case MOE_DTYPE_FP16: return CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    case MOE_DTYPE_FP32: return CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    default: return CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  }
+}
+inline int type_bytes(int dtype) {
+  return dtype == MOE_DTYPE_FP32 ? 4 : (dtype == MOE_DTYPE_E4M3 ? 1 : 2);
+}
+
+// [rows][cols] with rows `ld` elements apart, boxes of box_rows x box_cols.
+inline bool map_2d(CUtensorMap *m, int dtype, CUtensorMapSwizzle sw, const void *p, int64_t rows,
+                   int64_t cols, int64_t ld, int box_rows, int box_cols) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * type_bytes(dtype)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  return encode_map(m, map_type(dtype), sw, p, 2, dims, strides, box);
+}
+// Two matrices [rows][cols], `ld` between rows and `plane` between the two;
+// a box holds box_planes of them.
+inline bool map_two(CUtensorMap *m, int dtype, CUtensorMapSwizzle sw, const void *p, int64_t rows,
+                    int64_t cols, int64_t ld, int64_t plane, int box_rows, int box_cols,
+                    int box_planes) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * type_bytes(dtype),
+                                 (cuuint64_t)plane * type_bytes(dtype)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
+  return encode_map(m, map_type(dtype), sw, p, 3, dims, strides, box);
 }
 
 }  // namespace moe

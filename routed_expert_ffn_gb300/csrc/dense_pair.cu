@@ -16,14 +16,13 @@
 // transposed copy.  Tails of M, N and K are zeros filled in by TMA on the way
 // in and clipped by TMA on the way out.
 //
-// CTA = 6 warps, in both CTAs of the pair:
-//   warps 0-3  epilogue: 32 accumulator rows each, 32 columns at a time, from
-//              TMEM through registers to a swizzled 32 x 32 slot in shared
-//              memory and out by a TMA store of the warp's own (two slots, no
-//              barrier between warps);
-//   warp 4     TMA producer of its CTA's operands (completion counted on the
+// CTA = 10 warps, in both CTAs of the pair:
+//   warps 0-7  epilogue: 32 accumulator rows by 32 columns at a time, from
+//              TMEM through registers to a swizzled slot in shared memory and
+//              out by a TMA store of the warp's own (no barrier between warps);
+//   warp 8     TMA producer of its CTA's operands (completion counted on the
 //              even CTA's `full` barrier);
-//   warp 5     TMEM allocation; in the even CTA one thread issues the MMAs.
+//   warp 9     TMEM allocation; in the even CTA one thread issues the MMAs.
 // Every wait is bounded; on expiry the CTA latches the status bit and leaves
 // its loops, and both CTAs meet at a cluster barrier before TMEM is freed.
 #include <algorithm>
@@ -35,16 +34,18 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kStages = 6;
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;                      // the most columns of a tile
 constexpr uint32_t kABytes = kBM * kBK * 2;      // 16 KB
 constexpr uint32_t kBBytes = kTileN / 2 * kBK * 2;  // <= 16 KB
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kSlotBytes = 4096;            // 32 x 32 fp32, or 32 x 32 16-bit in half of it
+constexpr uint32_t kSlotBytes = 4096;            // an epilogue warp's: 32 x 32 fp32, or two of 16 bits
 constexpr uint32_t kTmemCols = 512;
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + 4 * 2 * kSlotBytes +
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kSlotBytes +
                          (2 * kStages + 5) * 8 + 16;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 // Row tiles of a raster group: tiles that run together share the A rows of 8
@@ -110,16 +111,28 @@ __device__ __forceinline__ Tile tile_at(int tile, const PairArgs &a) {
   return t;
 }
 
-// A warp's two output slots.
+// A warp's output buffer: two slots of 32 x 32 16-bit values, or one of fp32.
 struct Slots {
   uint8_t *base;
   uint32_t n;
-  // The next slot, once the store that last read it has done so.
-  __device__ __forceinline__ uint8_t *take(int lane) {
-    uint8_t *p = base + (n++ & 1u) * kSlotBytes;
-    if (lane == 0) bulk_wait_read<1>();
+  bool wide;  // the last store was fp32
+  // Each waits for the stores that still read what it hands out.
+  __device__ __forceinline__ uint8_t *take16(int lane) {
+    if (lane == 0) {
+      if (wide)
+        bulk_wait_read<0>();
+      else
+        bulk_wait_read<1>();
+    }
+    wide = false;
     __syncwarp();
-    return p;
+    return base + (n++ & 1u) * (kSlotBytes / 2);
+  }
+  __device__ __forceinline__ uint8_t *take32(int lane) {
+    if (lane == 0) bulk_wait_read<0>();
+    wide = true;
+    __syncwarp();
+    return base;
   }
 };
 
@@ -161,38 +174,44 @@ __device__ __forceinline__ void send_3d(const CUtensorMap *m, uint8_t *slot, int
   }
 }
 
-// f[i] += 32 consecutive values of the output type from `p` (null rows add
-// nothing); `left` of them exist (a multiple of 8).
-__device__ __forceinline__ void add_values(float (&f)[32], const void *p, int64_t off, int left,
-                                           int dtype) {
-  if (dtype == MOE_DTYPE_FP32) {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + off);
+// 32 consecutive values of the output type at `p` + off, of which `left` exist
+// (a multiple of 8; the rest zero): loaded early, added later.
+struct Values32 {
+  uint4 v[8];
+  __device__ __forceinline__ void load(const void *p, int64_t off, int left, int dtype) {
+    if (dtype == MOE_DTYPE_FP32) {
+      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + off);
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (4 * c < left) {
-        const float4 v = q[c];
-        f[4 * c] += v.x;
-        f[4 * c + 1] += v.y;
-        f[4 * c + 2] += v.z;
-        f[4 * c + 3] += v.w;
+      for (int c = 0; c < 8; ++c) v[c] = 4 * c < left ? q[c] : make_uint4(0, 0, 0, 0);
+    } else {
+      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = 8 * c < left ? q[c] : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void add_to(float (&f)[32], int dtype) const {
+    if (dtype == MOE_DTYPE_FP32) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        f[4 * c] += __uint_as_float(v[c].x);
+        f[4 * c + 1] += __uint_as_float(v[c].y);
+        f[4 * c + 2] += __uint_as_float(v[c].z);
+        f[4 * c + 3] += __uint_as_float(v[c].w);
       }
-  } else {
-    const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
-    uint4 v[4];
+    } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = 8 * c < left ? q[c] : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = unpack16(dtype, w[i]);
-        f[8 * c + 2 * i] += u.x;
-        f[8 * c + 2 * i + 1] += u.y;
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = unpack16(dtype, w[i]);
+          f[8 * c + 2 * i] += u.x;
+          f[8 * c + 2 * i + 1] += u.y;
+        }
       }
     }
   }
-}
+};
 
 // 32 consecutive fp32 values; those past `left` are zero.
 __device__ __forceinline__ void read32(float (&f)[32], const float *p, int left) {
@@ -216,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *ring = smem;
   uint8_t *slots = ring + kStages * kStageBytes;
-  uint64_t *full = reinterpret_cast<uint64_t *>(slots + 4 * 2 * kSlotBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(slots + kEpiWarps * kSlotBytes);
   uint64_t *empty = full + kStages;
   uint64_t *tfull = empty + kStages;
   uint64_t *tempty = tfull + 2;
@@ -233,17 +252,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);  // 4 epilogue warps in each CTA
+      mbar_init(&tempty[b], 2 * kEpiWarps);  // of both CTAs
     }
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.b);
     tma_prefetch_desc(&maps.d);
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int half = a.bn >> 1;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
 
-  if (warp == 4) {
+  if (warp == kTmaWarp) {
     // ------------------------------------------------------ TMA producer --
     if (lane == 0) {
       const int b_boxes = (half + 63) >> 6;
@@ -320,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- MMA issuer --
     if (rank == 0 && lane == 0) {
       constexpr uint32_t kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;  // 16 K, in 16 bytes
@@ -360,7 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue --
-    Slots slot = {slots + warp * 2 * kSlotBytes, 0};
+    // warps w and w + 4 share 32 TMEM lanes and take every other 32 columns
+    Slots slot = {slots + warp * kSlotBytes, 0, false};
+    const int quad = warp & 3, turn = (warp >> 2) * 32;
     uint32_t tl = 0;
     for (int tile = cid; tile < total; tile += ncl, ++tl) {
       const Tile t = tile_at(tile, a);
@@ -368,48 +389,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool waited = mbar_wait(&tfull[buf], use & 1u, abort_flag, a.status, kCode);
       if (!__all_sync(0xffffffffu, waited)) break;
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(warp * 32) << 16) + buf * (kTmemCols / 2);
-      const int row0 = t.m0 + (int)rank * kBM + warp * 32, row = row0 + lane;
+      const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + buf * (kTmemCols / 2);
+      const int row0 = t.m0 + (int)rank * kBM + quad * 32, row = row0 + lane;
       const int c0 = t.j * a.cols;
       const int cend = row0 < a.M ? min(a.N, c0 + a.cols) : c0;
-      for (int c = c0; c < cend; c += 32) {
+      for (int c = c0 + turn; c < cend; c += 64) {
         const int left = row < a.M ? a.N - c : 0;  // this row's columns from c on
         float v[32];
         if (kEpi == kEpiLinear) {
+          Values32 bias, res;
+          if (a.bias != nullptr) bias.load(a.bias, c, a.N - c, a.out_dtype);
+          if (a.residual != nullptr)
+            res.load(a.residual, (int64_t)row * a.ldr + c, left, a.out_dtype);
           tmem_ld32(tb + (c - c0), v);
-          if (a.bias != nullptr) add_values(v, a.bias, c, a.N - c, a.out_dtype);
+          if (a.bias != nullptr) bias.add_to(v, a.out_dtype);
           if (a.extra) {
-            uint8_t *p = slot.take(lane);
+            uint8_t *p = slot.take32(lane);
             put32(p, lane, v);
             send_2d(&maps.extra, p, lane, c, row0);
           }
-          if (a.act != MOE_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = activate(a.act, v[i]);
-          }
-          if (a.residual != nullptr && left > 0)
-            add_values(v, a.residual, (int64_t)row * a.ldr + c, left, a.out_dtype);
-          uint8_t *p = slot.take(lane);
-          if (a.out_dtype == MOE_DTYPE_FP32)
+          activate_all(a.act, v);
+          if (a.residual != nullptr) res.add_to(v, a.out_dtype);
+          uint8_t *p;
+          if (a.out_dtype == MOE_DTYPE_FP32) {
+            p = slot.take32(lane);
             put32(p, lane, v);
-          else
+          } else {
+            p = slot.take16(lane);
             put16(p, lane, a.out_dtype, v);
+          }
           send_2d(&maps.d, p, lane, c, row0);
         } else if (kEpi == kEpiGated) {
           float u[32];
           tmem_ld32(tb + (c - c0), v);
           tmem_ld32(tb + half + (c - c0), u);
           if (a.extra) {
-            uint8_t *p = slot.take(lane);
+            uint8_t *p = slot.take32(lane);
             put32(p, lane, v);
             send_3d(&maps.extra, p, lane, c, row0, 0);
-            p = slot.take(lane);
+            p = slot.take32(lane);
             put32(p, lane, u);
             send_3d(&maps.extra, p, lane, c, row0, 1);
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
-          uint8_t *p = slot.take(lane);
+          uint8_t *p = slot.take16(lane);
           put16(p, lane, a.dtype, v);
           send_2d(&maps.d, p, lane, c, row0);
         } else {
@@ -427,13 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             u[i] = v[i] * u[i] * p * (1.0f + g[i] * (1.0f - p));
             v[i] = v[i] * gp;
           }
-          uint8_t *p = slot.take(lane);
+          uint8_t *p = slot.take16(lane);
           put16(p, lane, a.dtype, o);
           send_2d(&maps.d, p, lane, c, row0);
-          p = slot.take(lane);
+          p = slot.take16(lane);
           put16(p, lane, a.dtype, u);
           send_3d(&maps.extra, p, lane, c, row0, 0);
-          p = slot.take(lane);
+          p = slot.take16(lane);
           put16(p, lane, a.dtype, v);
           send_3d(&maps.extra, p, lane, c, row0, 1);
         }
@@ -450,41 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while its peer may still signal it
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
 }
 
-CUtensorMapDataType map_type(int dtype) {
-  switch (dtype) {
-    case MOE_DTYPE_BF16: return CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    case MOE_DTYPE_FP16: return CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    case MOE_DTYPE_FP32: return CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    default: return CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  }
-}
-int type_bytes(int dtype) {
-  return dtype == MOE_DTYPE_FP32 ? 4 : (dtype == MOE_DTYPE_E4M3 ? 1 : 2);
-}
-
-// [rows][cols] with rows `ld` elements apart, boxes of box_rows x box_cols.
-bool map_2d(CUtensorMap *m, int dtype, CUtensorMapSwizzle sw, const void *p, int64_t rows,
-            int64_t cols, int64_t ld, int box_rows, int box_cols) {
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * type_bytes(dtype)};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  return encode_map(m, map_type(dtype), sw, p, 2, dims, strides, box);
-}
-// Two matrices [rows][cols], `ld` between rows and `plane` between the two.
-bool map_two(CUtensorMap *m, int dtype, CUtensorMapSwizzle sw, const void *p, int64_t rows,
-             int64_t cols, int64_t ld, int64_t plane, int box_rows, int box_cols) {
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 2};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * type_bytes(dtype),
-                                 (cuuint64_t)plane * type_bytes(dtype)};
-  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-  return encode_map(m, map_type(dtype), sw, p, 3, dims, strides, box);
-}
 CUtensorMapSwizzle out_swizzle(int dtype) {
   return dtype == MOE_DTYPE_FP32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
 }
@@ -556,7 +551,7 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
   bool ok = kAMn ? map_2d(&maps.a, g.dtype, in, g.a, g.K, g.M, g.lda, kBK, 64)
                  : map_2d(&maps.a, g.dtype, in, g.a, g.M, g.K, g.lda, kBM, kBK);
   if (kEpi == kEpiGated)
-    ok = ok && map_two(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, g.ldb * g.N, half, kBK);
+    ok = ok && map_two(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, g.ldb * g.N, half, kBK, 1);
   else
     ok = ok && (kBMn ? map_2d(&maps.b, g.dtype, in, g.b, g.K, g.N, g.ldb, kBK, 64)
                      : map_2d(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, half, kBK));
@@ -573,11 +568,11 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
     maps.extra = maps.d;
     if (a.extra)
       ok = ok && map_two(&maps.extra, MOE_DTYPE_FP32, out_swizzle(MOE_DTYPE_FP32), g.saved, g.M,
-                         g.N, 2 * (int64_t)g.N, g.N, 32, 32);
+                         g.N, 2 * (int64_t)g.N, g.N, 32, 32, 1);
   } else {
     ok = ok && map_2d(&maps.d, g.dtype, out_swizzle(g.dtype), g.h, g.M, g.N, g.N, 32, 32) &&
          map_two(&maps.extra, g.dtype, out_swizzle(g.dtype), g.dgu, g.M, g.N, 2 * (int64_t)g.N,
-                 g.N, 32, 32);
+                 g.N, 32, 32, 1);
   }
   if (!ok) return cudaErrorInvalidValue;
   const int ncl = (int)std::min<int64_t>(clusters[dev], (int64_t)a.mt * a.nt);

@@ -181,11 +181,24 @@ def _nbytes(t) -> int:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """torch's current stream; replaced on its first call by the quickest way this torch has."""
+    import torch
+    global _current_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        # 0.2 us instead of 3 for the Stream object and its handle
+        device = torch.cuda.current_device
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
 
 
 def _check(fn: str, st: int):
@@ -416,10 +429,11 @@ def _rows(t, stride: int, cols: int) -> Optional[int]:
         return t
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if t.dim() != 2 or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1) or (
-            t.shape[0] > 1 and t.stride(0) != (stride or cols)):
-        raise ValueError("expected a [T, cols] tensor with rows at the descriptor's stride")
-    return t.data_ptr()
+    s = t.stride()
+    if len(s) == 2 and t.size(1) == cols and (s[0] == (stride or cols) or t.size(0) <= 1) and (
+            s[1] == 1 or cols == 1):
+        return t.data_ptr()
+    raise ValueError("expected a [T, cols] tensor with rows at the descriptor's stride")
 
 
 def norm_desc(T: int, H: int, dtype: int, eps: float = 1e-6, x_stride: int = 0,

@@ -60,21 +60,16 @@ moe_status_t linear_desc(const moe_linear_desc_t *in, moe_linear_desc_t *d) {
 
 size_t pad(size_t n) { return (n + 1023) / 1024 * 1024; }
 
-// After the status block: the 16-bit operands of E4M3 products, or dz and the
-// column partials of the gradient.
+// After the status block: dz and the column partials of the gradient.
 struct LinearWs {
-  size_t a, b, total;
+  size_t dz, part, total;
 };
 LinearWs linear_ws(const moe_linear_desc_t &d) {
   LinearWs w;
-  w.a = kStatusPad;
-  if (d.dtype == MOE_DTYPE_E4M3) {
-    w.b = w.a + pad((size_t)d.T * d.K * 2);
-    w.total = w.b + pad((size_t)d.N * d.K * 2);
-  } else {
-    w.b = w.a + (d.act == MOE_ACT_NONE ? 0 : pad((size_t)d.T * d.N * 2));
-    w.total = w.b + pad((size_t)act_grad_slices(d.T, d.N) * d.N * 4);
-  }
+  w.dz = w.part = w.total = kStatusPad;
+  if (d.dtype == MOE_DTYPE_E4M3) return w;  // no gradient
+  w.part += d.act == MOE_ACT_NONE ? 0 : pad((size_t)d.T * d.N * 2);
+  w.total = w.part + pad((size_t)act_grad_slices(d.T, d.N) * d.N * 4);
   return w;
 }
 
@@ -125,11 +120,16 @@ DenseGemm product(int M, int N, int K, int dtype, const void *a, int64_t lda, bo
   return g;
 }
 
-// The forward products by their number of rows.  preact and saved are stored
-// by the tiled kernel only.
+// A forward product by the kernel that is estimated to take less: the one for
+// few rows reads W at the rate of HBM but X once for each 128 columns; the
+// tiled one wants 256 rows for each 64 to 256 columns.  4096 x 4096 (us, few
+// rows against tiled): 24 rows 9.6 and 23, 128 rows 15.2 and 16.8, 192 rows 20.2
+// and 16.7.  preact and saved are stored by the tiled kernel only.
 cudaError_t forward(const DenseGemm &g, cudaStream_t s) {
-  const bool few = g.M <= kSmallRows && g.preact == nullptr && g.saved == nullptr;
-  return few ? launch_dense_small(g, s) : launch_dense_pair(g, s);
+  if (g.M <= kSmallRows && g.preact == nullptr && g.saved == nullptr &&
+      dense_small_us(g) <= dense_pair_us(g))
+    return launch_dense_small(g, s);
+  return launch_dense_pair(g, s);
 }
 
 // dw[M,N] (+)= a^T b over T rows; T = 0 leaves zeros, or what is accumulated.
@@ -236,23 +236,12 @@ moe_status_t moe_linear(const moe_linear_desc_t *in, const void *x, const int8_t
                         d.out_dtype, workspace);
   g.a_scale = x_scale;
   g.b_scale = w_scale;
-  cudaError_t e = cudaSuccess;
-  if (e4m3 && d.T > kSmallRows) {
-    e = launch_widen_e4m3(x, d.x_stride, x_scale, 1, d.T, d.K, at(workspace, L.a), s);
-    if (e == cudaSuccess)
-      e = launch_widen_e4m3(w, d.K, w_scale, 128, d.N, d.K, at(workspace, L.b), s);
-    g.dtype = MOE_DTYPE_BF16;
-    g.a = at(workspace, L.a);
-    g.lda = d.K;
-    g.b = at(workspace, L.b);
-  }
   g.act = d.act;
   g.bias = bias;
   g.residual = residual;
   g.ldr = d.residual_stride;
   g.preact = preact;
-  if (e == cudaSuccess) e = forward(g, s);
-  return cuda_status(e);
+  return cuda_status(forward(g, s));
 }
 
 moe_status_t moe_linear_backward(const moe_linear_desc_t *in, const void *dy, const void *x,
@@ -277,13 +266,13 @@ moe_status_t moe_linear_backward(const moe_linear_desc_t *in, const void *dy, co
   }
   if ((st = check_device()) != MOE_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  float *part = reinterpret_cast<float *>(at(workspace, L.b));
-  const void *dz = act ? at(workspace, L.a) : dy;
+  float *part = reinterpret_cast<float *>(at(workspace, L.part));
+  const void *dz = act ? at(workspace, L.dz) : dy;
   const int64_t ldz = act ? d.N : d.y_stride;
   cudaError_t e = cudaSuccess;
   if (d.T > 0 && (dbias != nullptr || (act && (dx != nullptr || dw != nullptr))))
     e = launch_act_grad(dy, d.y_stride, preact, d.T, d.N, d.act, d.dtype,
-                        act ? at(workspace, L.a) : nullptr, dbias != nullptr ? part : nullptr, s);
+                        act ? at(workspace, L.dz) : nullptr, dbias != nullptr ? part : nullptr, s);
   if (e == cudaSuccess && dbias != nullptr)
     e = launch_column_sum(part, d.T > 0 ? act_grad_slices(d.T, d.N) : 0, d.N, d.N, dbias,
                           accumulate, s);

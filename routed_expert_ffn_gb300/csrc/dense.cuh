@@ -38,20 +38,20 @@ struct DenseGemm {
 
 // Prefill and training sizes: 256-row tiles on CTA pairs (dense_pair.cu).
 cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s);
-// Up to kSmallRows rows: weight rows as the MMA's M, rows of A as its N, K
-// split over a cluster (dense_small.cu).  K-major operands, no preact/saved.
-constexpr int kSmallRows = 256;
+// Few rows: weight rows as the MMA's M, rows of A as its N, K split over a
+// cluster (dense_small.cu).  K-major operands, no preact or saved, at most
+// kSmallRows rows.
+constexpr int kSmallRows = 1024;
 cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s);
+// What each is estimated to take, in us (0 if it cannot be told).
+float dense_pair_us(const DenseGemm &g);
+float dense_small_us(const DenseGemm &g);
 
 // dz = dy act'(z) in 16 bits (dz null: not written; z null: dz = dy) and the
 // column sums of each slice of the rows (part [slices][N], or null).
 int act_grad_slices(int T, int N);
 cudaError_t launch_act_grad(const void *dy, int64_t ldy, const float *z, int T, int N, int act,
                             int dtype, void *dz, float *part, cudaStream_t s);
-// dst[r][c] = code * 2^e as bf16, for E4M3 codes with one exponent to each
-// block of `block_rows` rows by 128 columns; exact (4 significant bits).
-cudaError_t launch_widen_e4m3(const void *src, int64_t ld, const int8_t *scale, int block_rows,
-                              int64_t rows, int cols, void *dst, cudaStream_t s);
 
 // ------------------------------------------------------------ element types --
 
@@ -139,18 +139,15 @@ __host__ __device__ constexpr uint32_t idesc_16(int dtype, bool a_mn, bool b_mn,
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Shared-memory descriptor of an MN-major operand in 128-byte swizzled boxes
-// of 64 MN elements by 64 K rows (8 KB): K groups of 8 rows 1024 bytes apart
-// (stride offset), boxes of 64 MN elements 8192 bytes apart (leading offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(8192 >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
+// Words of the shared-memory descriptors of operands in 128-byte swizzled
+// boxes, without the address (bits 0-13 of the low word, in 16-byte units).
+// Low word, from bit 16: leading offset; high word: stride offset, version 1
+// (bit 14), swizzle mode 2 (bits 29-31).
+//   K-major:  rows of 128 bytes, groups of 8 rows 1024 bytes apart (stride)
+//   MN-major: boxes of 64 MN elements by 64 K rows (8 KB): groups of 8 K rows
+//             1024 bytes apart (stride), boxes 8192 bytes apart (leading)
+constexpr uint32_t kDescLoK = 1u << 16, kDescLoMn = (8192u >> 4) << 16;
+constexpr uint32_t kDescHiK = (1024u >> 4) | (1u << 14) | (2u << 29), kDescHiMn = kDescHiK;
 
 // 32 lanes x 32 consecutive 32-bit columns; thread i gets lane (base + i).
 // The wait is part of the same statement: no use can move in front of it.
@@ -196,12 +193,28 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
   return ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
 }
 
-// Scale-factor columns of a stage: 4 for 128 rows of A, 8 for 256 rows of B.
-constexpr uint32_t kSmallSfCols = 12;
+// Which of a scale-factor word's bytes the MMA takes, for both operands.
+__host__ __device__ constexpr uint32_t idesc_sf_byte(uint32_t b) { return (b << 4) | (b << 29); }
+
+// Scale-factor columns: 4 for 128 rows of A, 8 for 256 rows of B.
+constexpr uint32_t kSfCols = 12;
 
 // A block exponent as four equal UE8M0 bytes (2^(byte - 127)).
 __device__ __forceinline__ uint32_t e8m0x4(int8_t e) {
   return (uint32_t)((int)e + 127) * 0x01010101u;
+}
+
+// Four successive block exponents as UE8M0 bytes; of those past `left` (which
+// no product takes) none is read.
+__device__ __forceinline__ uint32_t e8m0_4(const int8_t *e, int left) {
+  uint32_t w = 0x7f7f7f7fu;
+  if (left >= 4 && (reinterpret_cast<uintptr_t>(e) & 3u) == 0)
+    return __vadd4(__ldg(reinterpret_cast<const uint32_t *>(e)), w);
+  w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) w |= (uint32_t)((int)__ldg(e + i) + 127) << (8 * i);
+  return w;
 }
 
 // D (+)= (A * 2^sfa) (B * 2^sfb)^T, 32 of K, one CTA.
@@ -217,17 +230,10 @@ __device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// This warp's 32 lanes x 4 or 8 columns.
+// This warp's 32 lanes x 4 columns.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::
-                   "r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-               "r"(r[7])
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {

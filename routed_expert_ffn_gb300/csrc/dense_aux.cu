@@ -5,8 +5,6 @@
 // Bound: HBM (dy and z read, dz written).  A CTA takes 256 columns (a thread
 // 8 of them) and one slice of the rows; the slices' column sums are partials
 // that column_sum adds in a fixed order.
-#include <cuda_fp8.h>
-
 #include <algorithm>
 
 #include "dense.cuh"
@@ -67,39 +65,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One thread: 8 codes of a row.
-__global__ void __launch_bounds__(256)
-    widen_e4m3_kernel(const uint8_t *__restrict__ src, int64_t ld, const int8_t *__restrict__ scale,
-                      int block_rows, int64_t rows, int cols, uint16_t *__restrict__ dst) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int per = cols >> 3;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * per) return;
-  const int64_t r = i / per;
-  const int c = (int)(i - r * per) * 8;
-  const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src + r * ld + c));
-  const int e = scale[r / block_rows * ((cols + 127) >> 7) + (c >> 7)];
-  uint32_t out[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t two = ((j < 2 ? w.x : w.y) >> (16 * (j & 1))) & 0xffffu;
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    out[j] = pack_bf16x2(ldexpf(f.x, e), ldexpf(f.y, e));
-  }
-  *reinterpret_cast<uint4 *>(dst + r * cols + c) = make_uint4(out[0], out[1], out[2], out[3]);
-}
-
 }  // namespace
-
-cudaError_t launch_widen_e4m3(const void *src, int64_t ld, const int8_t *scale, int block_rows,
-                              int64_t rows, int cols, void *dst, cudaStream_t s) {
-  const int64_t n = rows * (cols / 8);
-  return launch_pdl(widen_e4m3_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                    static_cast<const uint8_t *>(src), ld, scale, block_rows, rows, cols,
-                    static_cast<uint16_t *>(dst));
-}
 
 // Slices of the rows: about four CTAs for each of 152 SMs, each with at least
 // 16 rows.

@@ -11,6 +11,10 @@
 // multiply-adds.  Two accumulators of 256 columns let the epilogue of a tile
 // run under the next tile's products.
 //
+// Where there are too few tiles for the SMs, two pairs (a cluster of four) take
+// the halves of K of one tile: each sends its partial sums of the other's half
+// of the columns through distributed shared memory and finishes its own half.
+//
 // Operands are K-major or MN-major, as they lie in memory: the gradient
 // products dX = dY W and dW = dY^T X read the forward tensors without a
 // transposed copy.  Tails of M, N and K are zeros filled in by TMA on the way
@@ -22,7 +26,9 @@
 //              out by a TMA store of the warp's own (no barrier between warps);
 //   warp 8     TMA producer of its CTA's operands (completion counted on the
 //              even CTA's `full` barrier);
-//   warp 9     TMEM allocation; in the even CTA one thread issues the MMAs.
+//   warp 9     TMEM allocation; in the even CTA one thread issues the MMAs;
+//   warp 10    E4M3 operands only: their block exponents, laid out as the
+//              scale factors of block-scaled MMAs (kind::mxf8f6f4).
 // Every wait is bounded; on expiry the CTA latches the status bit and leaves
 // its loops, and both CTAs meet at a cluster barrier before TMEM is freed.
 #include <algorithm>
@@ -35,19 +41,43 @@ namespace moe {
 namespace {
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kStages = 6;
+constexpr int kSfWarp = kEpiWarps + 2;           // E4M3
+// E4M3 leaves the last 64 TMEM columns to scale factors, four slots of four
+// stages each: accumulators of 224 columns.
+template <bool kE4m3>
+struct Shape {
+  static constexpr int threads = (kEpiWarps + 2 + (kE4m3 ? 1 : 0)) * 32;
+  static constexpr int stages = kE4m3 ? 5 : 6;
+  static constexpr int acc = kE4m3 ? 224 : 256;  // columns of an accumulator
+  static constexpr int kb = kE4m3 ? 128 : 64;    // K elements of a stage (128 bytes)
+  static constexpr uint32_t sf_col = 2 * acc;
+};
+static_assert(Shape<true>::sf_col + 4 * kSfCols <= 512, "TMEM columns");
+constexpr int kMaxStages = 6;
+constexpr int kSfGroup = 8;                       // stages to a hand-over of scale factors
+constexpr int kSfBufs = 3;
+constexpr uint32_t kSfBlock = 3 * 512;            // of four stages: A, twice B
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;                      // the most columns of a tile
 constexpr uint32_t kABytes = kBM * kBK * 2;      // 16 KB
 constexpr uint32_t kBBytes = kTileN / 2 * kBK * 2;  // <= 16 KB
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
+// Split-K: where a CTA's partial columns for the other pair leave, where the
+// other pair's arrive (both in the ring's place), 16 KB for 32 columns.
+constexpr uint32_t kChunkBytes = kBM * 32 * 4;
+constexpr uint32_t kRecvOff = 4 * kChunkBytes;
 constexpr uint32_t kSlotBytes = 4096;            // an epilogue warp's: 32 x 32 fp32, or two of 16 bits
 constexpr uint32_t kTmemCols = 512;
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * kSlotBytes +
-                         (2 * kStages + 5) * 8 + 16;
-static_assert(kSmem <= 232448, "shared memory per CTA");
+template <bool kE4m3>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)Shape<kE4m3>::stages * kStageBytes + kEpiWarps * kSlotBytes +
+         (2 * kMaxStages + 6 + 2 * kSfBufs) * 8 + 16 +
+         (kE4m3 ? 128 + kSfBufs * 2 * kSfBlock : 0);
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448,
+              "shared memory per CTA");
+static_assert(2 * kRecvOff <= Shape<true>::stages * kStageBytes, "exchange buffers");
 // Row tiles of a raster group: tiles that run together share the A rows of 8
 // row tiles and the B rows of ~10 column tiles, ~20 MB at K = 4096: in L2.
 constexpr int kGroupM = 8;
@@ -60,14 +90,55 @@ struct PairArgs {
   int M, N, K;
   int bn, cols;  // accumulator columns of a tile; output columns of a tile
   int mt, nt;
+  int split;     // pairs to a tile, K split between them (1 or 2)
+  int kb_part;   // stages of K to a pair
   int dtype, out_dtype, act;
   const void *bias, *residual;
   int64_t ldr;
   const float *saved;
   int extra;  // kEpiLinear: store preact; kEpiGated: store saved
+  const int8_t *a_scale, *b_scale;
   uint32_t *status;
 };
 
+// D (+)= A B^T over the pair, 16 of K; operand descriptors as low and high words.
+__device__ __forceinline__ void umma_16_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                             uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D (+)= (A * 2^sfa) (B * 2^sfb)^T over the pair, 32 of K.  Each CTA's TMEM
+// holds the scale factors of its own rows of A and of all columns.
+__device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                               uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %8, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %5, [%6], [%7], p;\n\t}" ::
+          "r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// 32 rows of 16 bytes from shared memory (both CTAs' own) to 4 columns of TMEM,
+// repeated in the four groups of 32 lanes; in order with the MMAs that follow.
+__device__ __forceinline__ void sf_copy_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+// Its source: no swizzle, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sf(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m, uint32_t bar,
                                                  int c0, int c1) {
   asm volatile(
@@ -96,6 +167,23 @@ __device__ __forceinline__ void bulk_commit() {
 template <int kLeft>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+
+// The cluster's barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// `bytes` of this CTA's shared memory to another's, counted on that CTA's barrier.
+__device__ __forceinline__ void bulk_send(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 struct Tile {
@@ -154,6 +242,17 @@ __device__ __forceinline__ void put32(uint8_t *slot, int lane, const float (&f)[
   for (int c = 0; c < 8; ++c)
     *reinterpret_cast<float4 *>(slot + lane * 128 + ((c ^ (lane & 7)) << 4)) =
         make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+}
+// Adds what put32 left.
+__device__ __forceinline__ void add32(float (&f)[32], const uint8_t *slot, int lane) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float4 v = *reinterpret_cast<const float4 *>(slot + lane * 128 + ((c ^ (lane & 7)) << 4));
+    f[4 * c] += v.x;
+    f[4 * c + 1] += v.y;
+    f[4 * c + 2] += v.z;
+    f[4 * c + 3] += v.w;
+  }
 }
 __device__ __forceinline__ void send_2d(const CUtensorMap *m, uint8_t *slot, int lane, int c0,
                                         int c1) {
@@ -226,25 +325,37 @@ __device__ __forceinline__ void read32(float (&f)[32], const float *p, int left)
   }
 }
 
-template <int kEpi, bool kAMn, bool kBMn>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kEpi, bool kAMn, bool kBMn, bool kE4m3>
+__global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
     dense_pair_kernel(const __grid_constant__ PairMaps maps, const PairArgs a) {
-  constexpr uint32_t kCode = kStatusTimeoutDense;
+  constexpr int kStages = Shape<kE4m3>::stages, kKb = Shape<kE4m3>::kb;
+  constexpr uint32_t kAcc = Shape<kE4m3>::acc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *ring = smem;
   uint8_t *slots = ring + kStages * kStageBytes;
   uint64_t *full = reinterpret_cast<uint64_t *>(slots + kEpiWarps * kSlotBytes);
-  uint64_t *empty = full + kStages;
-  uint64_t *tfull = empty + kStages;
+  uint64_t *empty = full + kMaxStages;
+  uint64_t *tfull = empty + kMaxStages;
   uint64_t *tempty = tfull + 2;
   uint64_t *fin = tempty + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
+  uint64_t *recv = fin + 1;
+  uint64_t *sf_full = recv + 1;
+  uint64_t *sf_empty = sf_full + kSfBufs;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sf_empty + kSfBufs);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+  // E4M3: [kSfBufs][2][kSfBlock], 128-byte aligned
+  uint8_t *sf_blocks = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(tmem_slot + 2) + 127) & ~static_cast<uintptr_t>(127));
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t crank = cluster_rank();
+  const uint32_t rank = crank & 1u;  // in the pair; the even CTA issues the MMAs
+  const uint32_t lead = crank & ~1u;
+  const uint16_t pair_mask = (uint16_t)(3u << lead);
+  const int kpart = (int)(crank >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -254,7 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 2 * kEpiWarps);  // of both CTAs
     }
+    for (int g = 0; g < kSfBufs; ++g) {
+      mbar_init(&sf_full[g], 2);  // a warp of each CTA
+      mbar_init(&sf_empty[g], 1);
+    }
     mbar_init(fin, 1);
+    mbar_init(recv, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -275,31 +391,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = a.mt * a.nt;
-  const int nkb = (a.K + kBK - 1) / kBK;
+  const int nkb = (a.K + kKb - 1) / kKb;
+  const int k_first = min(nkb, kpart * a.kb_part), k_end = min(nkb, k_first + a.kb_part);
   const int half = a.bn >> 1;
-  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  const int cid = blockIdx.x / (2 * a.split), ncl = gridDim.x / (2 * a.split);
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------ TMA producer --
     if (lane == 0) {
       const int b_boxes = (half + 63) >> 6;
       const uint32_t bytes =
-          kABytes + (kBMn ? (uint32_t)b_boxes * 8192u : (uint32_t)half * (kBK * 2));
+          kABytes + (kBMn ? (uint32_t)b_boxes * 8192u : (uint32_t)half * 128u);
+      const uint32_t full0 = cluster_addr(full, lead);
       uint32_t st = 0, ph = 0, issued = 0;
+      uint8_t *da = ring;
       bool ok = true;
       for (int tile = cid; ok && tile < total; tile += ncl) {
         const Tile t = tile_at(tile, a);
         const int m = t.m0 + (int)rank * kBM;
         const int n = kEpi == kEpiGated ? t.j * a.cols : t.j * a.cols + (int)rank * half;
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.status, kCode)) {
+        for (int kb = k_first; kb < k_end; ++kb) {
+          if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
             ok = false;
             break;
           }
-          const uint32_t bar = cluster_addr(&full[st], 0);
+          const uint32_t bar = full0 + st * 8;
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
-          uint8_t *da = ring + st * kStageBytes, *db = da + kABytes;
-          const int k = kb * kBK;
+          uint8_t *db = da + kABytes;
+          const int k = kb * kKb;
           if (kAMn) {
             tma_load_2d_pair(da, &maps.a, bar, m, k);
             tma_load_2d_pair(da + 8192, &maps.a, bar, m + 64, k);
@@ -316,18 +435,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_pair(db, &maps.b, bar, k, n);
           }
           ++issued;
-          if (++st == kStages) {
+          da += kStageBytes;
+          if (++st == (uint32_t)kStages) {
             st = 0;
             ph ^= 1u;
+            da = ring;
           }
         }
       }
       if (rank == 0) {
         // every copy of both CTAs completes on these barriers
-        const uint32_t n = issued < kStages ? issued : kStages;
+        const uint32_t n = min(issued, (uint32_t)kStages);
         for (uint32_t i = 0; i < n; ++i) {
           st = st == 0 ? kStages - 1 : st - 1;
-          if (st == kStages - 1) ph ^= 1u;
+          if (st == (uint32_t)kStages - 1) ph ^= 1u;
           mbar_wait_drain(&full[st], ph);
         }
       } else if (!ok) {
@@ -343,38 +464,132 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------- MMA issuer --
     if (rank == 0 && lane == 0) {
       constexpr uint32_t kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;  // 16 K, in 16 bytes
-      const uint32_t idesc = idesc_16(a.dtype, kAMn, kBMn, 2 * kBM, a.bn);
-      const uint64_t a0 = kAMn ? sdesc_mn_sw128(smem_u32(ring)) : sdesc_k_sw128(smem_u32(ring));
-      const uint64_t b0 = kBMn ? sdesc_mn_sw128(smem_u32(ring + kABytes))
-                               : sdesc_k_sw128(smem_u32(ring + kABytes));
+      const uint32_t idesc = kE4m3 ? idesc_mxf8(2 * kBM, a.bn)
+                                   : idesc_16(a.dtype, kAMn, kBMn, 2 * kBM, a.bn);
+      // operand descriptors: the high words do not change, the low ones hold the
+      // address in 16-byte units
+      constexpr uint32_t kAHi = kAMn ? kDescHiMn : kDescHiK, kBHi = kBMn ? kDescHiMn : kDescHiK;
+      const uint32_t a0 = smem_u32(ring) >> 4 | (kAMn ? kDescLoMn : kDescLoK);
+      const uint32_t b0 = smem_u32(ring + kABytes) >> 4 | (kBMn ? kDescLoMn : kDescLoK);
+      uint32_t off = 0;
       uint32_t st = 0, ph = 0, tl = 0;
+      uint32_t sg = 0, sph = 0, sslot = 0;  // E4M3: hand-over buffer, TMEM slot
       bool ok = true;
       for (int tile = cid; ok && tile < total; tile += ncl, ++tl) {
         const uint32_t buf = tl & 1u, use = tl >> 1;
-        if (!mbar_wait(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kCode)) break;
+        if (!mbar_wait(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) break;
         tc_fence_after();
-        const uint32_t d0 = tmem_base + buf * (kTmemCols / 2);
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&full[st], ph, abort_flag, a.status, kCode)) {
+        const uint32_t d0 = tmem_base + buf * kAcc;
+        for (int kb = k_first; kb < k_end; ++kb) {
+          const int ki = kb - k_first;
+          if (!mbar_wait(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
             ok = false;
             break;
           }
+          uint32_t sf = 0, id = idesc;
+          if (kE4m3) {
+            if (ki % kSfGroup == 0 &&
+                !mbar_wait(&sf_full[sg], sph, abort_flag, a.status, kStatusTimeoutDense)) {
+              ok = false;
+              break;
+            }
+            if (ki % 4 == 0) ++sslot;
+            sf = tmem_base + Shape<true>::sf_col + (sslot & 3u) * kSfCols;
+            id |= idesc_sf_byte((uint32_t)ki & 3u);
+          }
           tc_fence_after();
-          const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
+          if (kE4m3 && ki % 4 == 0) {
+            const uint64_t sd =
+                sdesc_sf(smem_u32(sf_blocks + (sg * 2 + (uint32_t)(ki >> 2 & 1)) * kSfBlock));
 #pragma unroll
-          for (uint32_t q = 0; q < 4; ++q)
-            umma_bf16_pair(d0, ad + q * kAStep, bd + q * kBStep, idesc, (kb | q) != 0 ? 1u : 0u);
-          umma_commit_pair(&empty[st], 3);
-          if (++st == kStages) {
+            for (uint32_t i = 0; i < 3; ++i) sf_copy_pair(sf + 4 * i, sd + i * (512 >> 4));
+          }
+          const uint32_t ad = a0 + off, bd = b0 + off;
+#pragma unroll
+          for (uint32_t q = 0; q < 4; ++q) {
+            const uint32_t acc = ((uint32_t)ki | q) != 0 ? 1u : 0u;
+            if (kE4m3) {
+              umma_mxf8_pair(d0, ad + 2 * q, kAHi, bd + 2 * q, kBHi, id, sf, sf + 4, acc);
+            } else {
+              umma_16_pair(d0, ad + q * kAStep, kAHi, bd + q * kBStep, kBHi, idesc, acc);
+            }
+          }
+          umma_commit_pair(&empty[st], pair_mask);
+          if (kE4m3 && (ki % kSfGroup == kSfGroup - 1 || kb == k_end - 1)) {
+            umma_commit_pair(&sf_empty[sg], pair_mask);
+            if (++sg == kSfBufs) {
+              sg = 0;
+              sph ^= 1u;
+            }
+          }
+          off += kStageBytes >> 4;
+          if (++st == (uint32_t)kStages) {
             st = 0;
             ph ^= 1u;
+            off = 0;
           }
         }
         if (!ok) break;
-        umma_commit_pair(&tfull[buf], 3);
+        umma_commit_pair(&tfull[buf], pair_mask);
       }
-      umma_commit_pair(fin, 1);
+      umma_commit_pair(fin, (uint16_t)(1u << lead));
       mbar_wait_drain(fin, 0);
+    }
+    __syncwarp();
+  } else if (kE4m3 && warp == kSfWarp) {
+    // ------------------------------------------------- scale factors --
+    // A word of TMEM's scale factors holds four bytes: here those of four
+    // successive 128-deep stages, chosen by the byte index in the MMA's
+    // descriptor.  Lane l's word j of A's 512-byte block is row 32 j + l, word
+    // j of B's block i column 128 i + 32 j + l (32 columns lie in one 128-row
+    // block of W).  The MMA thread copies the blocks to TMEM in the order of its
+    // products.  One hand-over for eight stages: it takes a release at cluster
+    // scope, which measured 0.85 us (a stage takes 0.25).
+    const int last = (a.N - 1) >> 7;
+    uint32_t g = 0, ph = 0;
+    bool ok = true;
+    for (int tile = cid; ok && tile < total; tile += ncl) {
+      const Tile t = tile_at(tile, a);
+      for (int kb = k_first; kb < k_end; kb += kSfGroup) {
+        uint32_t x[2][4], w[2][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = min(t.m0 + (int)rank * kBM + 32 * j + lane, a.M - 1);
+          const int8_t *e = a.a_scale + (int64_t)r * nkb + kb;
+          x[0][j] = e8m0_4(e, nkb - kb);
+          x[1][j] = e8m0_4(e + 4, nkb - kb - 4);
+        }
+        {
+          // lane j: the words of 32 columns
+          const int blk = min((t.j * a.cols + 32 * (lane & 7)) >> 7, last);
+          const int8_t *e = a.b_scale + (int64_t)blk * nkb + kb;
+          const uint32_t w0 = e8m0_4(e, nkb - kb), w1 = e8m0_4(e + 4, nkb - kb - 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            w[0][j] = __shfl_sync(0xffffffffu, w0, j);
+            w[1][j] = __shfl_sync(0xffffffffu, w1, j);
+          }
+        }
+        const bool free = mbar_wait(&sf_empty[g], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense);
+        if (!__all_sync(0xffffffffu, free)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint4 *to = reinterpret_cast<uint4 *>(sf_blocks + (g * 2 + i) * kSfBlock) + lane;
+          to[0] = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+          to[32] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+          to[64] = make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&sf_full[g], lead));
+        if (++g == kSfBufs) {
+          g = 0;
+          ph ^= 1u;
+        }
+      }
     }
     __syncwarp();
   } else {
@@ -383,25 +598,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     Slots slot = {slots + warp * kSlotBytes, 0, false};
     const int quad = warp & 3, turn = (warp >> 2) * 32;
     uint32_t tl = 0;
+    Values32 bias, res;  // kEpiLinear: of the next chunk
+    auto fetch = [&](int c, int row) {
+      if (kEpi != kEpiLinear) return;
+      if (a.bias != nullptr) bias.load(a.bias, c, a.N - c, a.out_dtype);
+      if (a.residual != nullptr)
+        res.load(a.residual, (int64_t)row * a.ldr + c, row < a.M ? a.N - c : 0, a.out_dtype);
+    };
     for (int tile = cid; tile < total; tile += ncl, ++tl) {
       const Tile t = tile_at(tile, a);
       const uint32_t buf = tl & 1u, use = tl >> 1;
-      const bool waited = mbar_wait(&tfull[buf], use & 1u, abort_flag, a.status, kCode);
-      if (!__all_sync(0xffffffffu, waited)) break;
-      tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + buf * (kTmemCols / 2);
       const int row0 = t.m0 + (int)rank * kBM + quad * 32, row = row0 + lane;
       const int c0 = t.j * a.cols;
-      const int cend = row0 < a.M ? min(a.N, c0 + a.cols) : c0;
-      for (int c = c0 + turn; c < cend; c += 64) {
+      int cfirst = c0, cend = c0 + a.cols;  // the columns this CTA finishes
+      // of a cluster's only tile the first pair finishes the first half of the
+      // columns, the second the rest
+      const int mid = c0 + (a.cols / 32 + 1) / 2 * 32;
+      if (a.split == 2 && kpart == 0) cend = mid;
+      if (a.split == 2 && kpart == 1) cfirst = mid;
+      fetch(cfirst + turn, row);
+      bool ok = mbar_wait(&tfull[buf], use & 1u, abort_flag, a.status, kStatusTimeoutDense);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && a.split == 1) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + buf * kAcc;
+      if (a.split == 2) {
+        // The others' partial sums go to the same CTA of the other pair, in
+        // 32-column chunks (gated: g's chunk, then u's).
+        const int ofirst = kpart == 0 ? mid : c0, oend = kpart == 0 ? c0 + a.cols : mid;
+        constexpr int kPer = kEpi == kEpiGated ? 2 : 1;
+        if (warp == 0 && lane == 0)
+          mbar_arrive_expect_tx(recv, (uint32_t)((cend - cfirst) / 32 * kPer) * kChunkBytes);
+        __syncwarp();
+        cluster_arrive();  // this CTA's ring is done
+        if (ok)
+          for (int c = ofirst + turn; c < oend; c += 64) {
+            uint8_t *p = ring + (uint32_t)((c - ofirst) / 32 * kPer) * kChunkBytes + quad * kSlotBytes;
+            float v[32];
+            tmem_ld32(tb + (c - c0), v);
+            put32(p, lane, v);
+            if (kEpi == kEpiGated) {
+              tmem_ld32(tb + half + (c - c0), v);
+              put32(p + kChunkBytes, lane, v);
+            }
+          }
+        fence_proxy_async_shared();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        cluster_wait();  // every ring is done
+        if (ok && warp == 0 && lane == 0)
+          bulk_send(cluster_addr(ring + kRecvOff, crank ^ 2u), ring,
+                    (uint32_t)((oend - ofirst) / 32 * kPer) * kChunkBytes,
+                    cluster_addr(recv, crank ^ 2u));
+        __syncwarp();
+        ok = mbar_wait(recv, 0, abort_flag, a.status, kStatusTimeoutDense) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      const uint8_t *others = ring + kRecvOff + quad * kSlotBytes;
+      const int cstart = cfirst;
+      cend = row0 < a.M ? min(a.N, cend) : cfirst;
+      for (int c = cfirst + turn; c < cend; c += 64) {
         const int left = row < a.M ? a.N - c : 0;  // this row's columns from c on
         float v[32];
         if (kEpi == kEpiLinear) {
-          Values32 bias, res;
-          if (a.bias != nullptr) bias.load(a.bias, c, a.N - c, a.out_dtype);
-          if (a.residual != nullptr)
-            res.load(a.residual, (int64_t)row * a.ldr + c, left, a.out_dtype);
           tmem_ld32(tb + (c - c0), v);
+          if (a.split == 2) add32(v, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, lane);
           if (a.bias != nullptr) bias.add_to(v, a.out_dtype);
           if (a.extra) {
             uint8_t *p = slot.take32(lane);
@@ -410,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           activate_all(a.act, v);
           if (a.residual != nullptr) res.add_to(v, a.out_dtype);
+          if (c + 64 < cend) fetch(c + 64, row);
           uint8_t *p;
           if (a.out_dtype == MOE_DTYPE_FP32) {
             p = slot.take32(lane);
@@ -423,6 +685,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           float u[32];
           tmem_ld32(tb + (c - c0), v);
           tmem_ld32(tb + half + (c - c0), u);
+          if (a.split == 2) {
+            const uint8_t *o = others + (uint32_t)((c - cstart) / 32 * 2) * kChunkBytes;
+            add32(v, o, lane);
+            add32(u, o + kChunkBytes, lane);
+          }
           if (a.extra) {
             uint8_t *p = slot.take32(lane);
             put32(p, lane, v);
@@ -443,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           read32(g, sv, left);
           read32(u, sv + a.N, left);
           tmem_ld32(tb + (c - c0), v);
+          if (a.split == 2) add32(v, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, lane);
           float o[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -464,13 +732,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[buf], lead));
     }
     // the slots outlive the copies that read them
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   }
 
+  if (a.split == 2 && warp >= kEpiWarps) {
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while its peer may still signal it
@@ -484,58 +756,111 @@ CUtensorMapSwizzle out_swizzle(int dtype) {
   return dtype == MOE_DTYPE_FP32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
 }
 
-template <int kEpi, bool kAMn, bool kBMn>
-cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
-  auto kern = dense_pair_kernel<kEpi, kAMn, kBMn>;
+// How a product is laid out over the clusters, and about how long it takes (us).
+struct PairPlan {
+  int bn, cols, mt, nt, split, kb_part;
+  int clusters;
+  float us;
+};
+
+// The plan with the least estimated time.  Fitted to the kernel on one GB300
+// over 24 to 1024 rows, N of 512 to 14336, K of 512 to 14336 (each within a few
+// per cent): a stage takes 0.26 us up to 128 columns and 0.31 at 256 (E4M3:
+// 0.37 and 0.41), a launch with its first copies 6 us, the last tile's epilogue
+// 0.02 us a column.  Splitting K in two halves a single round's stages: 4096 x
+// 14336 at 512 rows 66.6 -> 43.2 us.
+PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
+  const bool e4m3 = g.dtype == MOE_DTYPE_E4M3, gated = g.epi == kEpiGated;
+  const int kb = e4m3 ? Shape<true>::kb : Shape<false>::kb;
+  const int nkb = (g.K + kb - 1) / kb;
+  PairPlan p = {};
+  p.mt = (g.M + kTileM - 1) / kTileM;
+  const int mt = p.mt;
+  for (int split = 1; split <= 2; ++split) {
+    const int part = split == 1 ? nkb : (nkb + 15) / 16 * 8;  // E4M3: whole groups of scales
+    if (split == 2 && part >= nkb) continue;
+    for (int bn = e4m3 ? Shape<true>::acc : Shape<false>::acc; bn >= 64; bn -= gated ? 64 : 32) {
+      const int cols = gated ? bn / 2 : bn;
+      const int nt = (g.N + cols - 1) / cols;
+      const int64_t tiles = (int64_t)mt * nt;
+      if (split == 2 && (tiles > resident[1] || cols < 64)) continue;  // one tile a cluster
+      const int64_t rounds = (tiles + resident[split - 1] - 1) / resident[split - 1];
+      const float stage = (e4m3 ? 0.37f : 0.26f) + 0.0004f * (float)std::max(0, bn - 128);
+      const float us = 6.0f + 0.02f * (float)bn + (split == 2 ? 1.0f : 0.0f) +
+                       (float)(rounds * part) * stage;
+      if (p.us == 0.f || us < p.us) {
+        p.us = us;
+        p.bn = bn;
+        p.cols = cols;
+        p.nt = nt;
+        p.split = split;
+        p.kb_part = part;
+        p.clusters = (int)std::min<int64_t>(resident[split - 1], tiles);
+      }
+    }
+  }
+  return p;
+}
+
+// Clusters of one and of two pairs that can run at once (per device, queried once).
+template <int kEpi, bool kAMn, bool kBMn, bool kE4m3>
+cudaError_t resident_clusters(int (&out)[2]) {
+  auto kern = dense_pair_kernel<kEpi, kAMn, kBMn, kE4m3>;
+  static int resident[64][2] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  static int clusters[64] = {};
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  if (clusters[dev] == 0) {
+  if (resident[dev][0] == 0) {
+    constexpr size_t kBytes = smem_bytes<kE4m3>();
     cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2));
-    cfg.numAttrs = 1;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    clusters[dev] = std::min(n, num_sms() / 2);
+    for (int p = 2; p >= 1; --p) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)(2 * p);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3((unsigned)(num_sms() / (2 * p) * (2 * p)));
+      cfg.blockDim = dim3(Shape<kE4m3>::threads);
+      cfg.dynamicSmemBytes = kBytes;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      resident[dev][p - 1] = std::min(n, num_sms() / (2 * p));
+    }
+  }
+  out[0] = resident[dev][0];
+  out[1] = resident[dev][1];
+  return cudaSuccess;
+}
+
+// `us` not null: only the estimated time.
+template <int kEpi, bool kAMn, bool kBMn, bool kE4m3 = false>
+cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
+  constexpr int kKb = Shape<kE4m3>::kb;
+  int resident[2];
+  cudaError_t e = resident_clusters<kEpi, kAMn, kBMn, kE4m3>(resident);
+  if (e != cudaSuccess) return e;
+  const PairPlan plan = plan_pair(g, resident);
+  if (us != nullptr) {
+    *us = plan.us;
+    return cudaSuccess;
   }
 
   PairArgs a = {};
   a.M = g.M;
   a.N = g.N;
   a.K = g.K;
-  a.mt = (g.M + kTileM - 1) / kTileM;
-  // Tile width: the one with the least whole rounds x columns over the
-  // clusters.
-  const int step = kEpi == kEpiGated ? 64 : 32;
-  int64_t best = 0;
-  for (int bn = kTileN; bn >= 64; bn -= step) {
-    const int cols = kEpi == kEpiGated ? bn / 2 : bn;
-    const int nt = (g.N + cols - 1) / cols;
-    const int64_t rounds = ((int64_t)a.mt * nt + clusters[dev] - 1) / clusters[dev];
-    const int64_t cost = rounds * (std::max(bn, 112) + 8);
-    if (best == 0 || cost < best) {
-      best = cost;
-      a.bn = bn;
-      a.cols = cols;
-      a.nt = nt;
-    }
-  }
+  a.bn = plan.bn;
+  a.cols = plan.cols;
+  a.mt = plan.mt;
+  a.nt = plan.nt;
+  a.split = plan.split;
+  a.kb_part = plan.kb_part;
   a.dtype = g.dtype;
   a.out_dtype = g.out_dtype;
   a.act = g.act;
@@ -543,18 +868,20 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
   a.residual = g.residual;
   a.ldr = g.ldr;
   a.saved = g.saved;
+  a.a_scale = g.a_scale;
+  a.b_scale = g.b_scale;
   a.status = g.status;
   const int half = a.bn / 2;
 
   PairMaps maps;
   const CUtensorMapSwizzle in = CU_TENSOR_MAP_SWIZZLE_128B;
   bool ok = kAMn ? map_2d(&maps.a, g.dtype, in, g.a, g.K, g.M, g.lda, kBK, 64)
-                 : map_2d(&maps.a, g.dtype, in, g.a, g.M, g.K, g.lda, kBM, kBK);
+                 : map_2d(&maps.a, g.dtype, in, g.a, g.M, g.K, g.lda, kBM, kKb);
   if (kEpi == kEpiGated)
     ok = ok && map_two(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, g.ldb * g.N, half, kBK, 1);
   else
     ok = ok && (kBMn ? map_2d(&maps.b, g.dtype, in, g.b, g.K, g.N, g.ldb, kBK, 64)
-                     : map_2d(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, half, kBK));
+                     : map_2d(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, half, kKb));
   if (kEpi == kEpiLinear) {
     ok = ok && map_2d(&maps.d, g.out_dtype, out_swizzle(g.out_dtype), g.d, g.M, g.N, g.ldd, 32, 32);
     a.extra = g.preact != nullptr;
@@ -575,23 +902,44 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
                  g.N, 32, 32, 1);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const int ncl = (int)std::min<int64_t>(clusters[dev], (int64_t)a.mt * a.nt);
-  cfg.gridDim = dim3((unsigned)(2 * ncl));
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)(2 * a.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(2 * a.split * plan.clusters));
+  cfg.blockDim = dim3(Shape<kE4m3>::threads);
+  cfg.dynamicSmemBytes = smem_bytes<kE4m3>();
+  cfg.stream = s;
+  cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, maps, a);
+  return cudaLaunchKernelEx(&cfg, dense_pair_kernel<kEpi, kAMn, kBMn, kE4m3>, maps, a);
+}
+
+cudaError_t pair_call(const DenseGemm &g, cudaStream_t s, float *us) {
+  if (g.dtype == MOE_DTYPE_E4M3) return launch<kEpiLinear, false, false, true>(g, s, us);
+  switch (g.epi) {
+    case kEpiGated: return launch<kEpiGated, false, false>(g, s, us);
+    case kEpiGatedGrad: return launch<kEpiGatedGrad, false, true>(g, s, us);
+    default:
+      if (g.a_mn) return launch<kEpiLinear, true, true>(g, s, us);
+      if (g.b_mn) return launch<kEpiLinear, false, true>(g, s, us);
+      return launch<kEpiLinear, false, false>(g, s, us);
+  }
 }
 
 }  // namespace
 
+float dense_pair_us(const DenseGemm &g) {
+  float us = 0.f;
+  return pair_call(g, nullptr, &us) == cudaSuccess ? us : 0.f;
+}
+
 cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s) {
-  switch (g.epi) {
-    case kEpiGated: return launch<kEpiGated, false, false>(g, s);
-    case kEpiGatedGrad: return launch<kEpiGatedGrad, false, true>(g, s);
-    default:
-      if (g.a_mn) return launch<kEpiLinear, true, true>(g, s);
-      if (g.b_mn) return launch<kEpiLinear, false, true>(g, s);
-      return launch<kEpiLinear, false, false>(g, s);
-  }
+  return pair_call(g, s, nullptr);
 }
 
 }  // namespace moe

@@ -2,20 +2,21 @@
 // chunks): D[t, n] = epilogue( sum over k of X(t, k) W(n, k) ).
 //
 // Bound: the bytes of W from HBM.  W's rows are the MMA's M (128 a tile), the
-// rows of X its N (16 to 256), so a tile of W flows through the tensor core
+// rows of X its N (16 to 64), so a tile of W flows through the tensor core
 // once for all rows of X.  There are too few tiles of W to draw the whole
 // bandwidth, so K is split over the CTAs of a cluster: each streams its own
 // part of K through a ring of TMA stages into its TMEM accumulator, and the
-// partial tiles are added in rank order through distributed shared memory --
-// one kernel, no partials in HBM, and the same bits every time.
+// partial tiles are sent through distributed shared memory to the CTA that adds
+// them (each takes some of the rows of X) and added in rank order -- one kernel, no partials in HBM, and the same
+// bits every time.
 //
 // Gated tiles hold 64 gate and the same 64 up rows of W.  E4M3 operands are
 // multiplied as they are (kind::mxf8f6f4, block-scaled): the exponent of each
 // 128 x 128 block of W and of each row of X and 128 columns goes to TMEM as
 // the MMA's scale factors.
 //
-// CTA = 6 warps: 0-3 write the scale factors (E4M3), then move the accumulator
-// to shared memory; 4 TMA producer; 5 TMEM and MMA.  All warps add, apply the
+// CTA = 6 warps: 0-3 write the scale factors (E4M3), then send the accumulator's
+// rows; 4 TMA producer; 5 TMEM and MMA.  All warps add, apply the
 // epilogue and store.  Every wait is bounded.
 #include <algorithm>
 
@@ -27,8 +28,11 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 192;
+constexpr int kTmaWarp = 4, kMmaWarp = 5;
 constexpr int kMaxStages = 6;
+constexpr uint32_t kSmallSfCols = 8;     // scale-factor columns of a stage
 constexpr uint32_t kWBytes = 128 * 128;  // 128 rows of 128 bytes of K
+constexpr int kChunk = 64;               // the most rows of X a tile
 constexpr int kMaxSplit = 8;             // portable cluster size
 
 struct SmallMaps {
@@ -39,6 +43,9 @@ struct SmallArgs {
   int T, N, K;      // rows of X, output columns, depth
   int n;            // rows of X a tile (a multiple of 16)
   int split, stages;
+  int own;          // rows of X whose sums a CTA of the cluster adds
+  int bulk;         // how partial tiles travel: 0 single stores, 1 bulk copies
+  uint32_t part_off;  // where they arrive in shared memory
   int dtype, out_dtype, act;
   const void *bias, *residual;
   void *d;
@@ -48,24 +55,33 @@ struct SmallArgs {
   uint32_t *status;
 };
 
-// 8 consecutive values of type `dtype`, as fp32
-__device__ __forceinline__ void load8(float (&f)[8], const void *p, int64_t off, int dtype) {
-  if (dtype == MOE_DTYPE_FP32) {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + off);
-    const float4 a = q[0], b = q[1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 u = unpack16(dtype, w[i]);
-      f[2 * i] = u.x;
-      f[2 * i + 1] = u.y;
+// 8 consecutive values of type `dtype`, loaded early and converted late
+struct Values8 {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const void *p, int64_t off, int dtype) {
+    if (dtype == MOE_DTYPE_FP32) {
+      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + off);
+      lo = q[0];
+      hi = q[1];
+    } else {
+      lo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
     }
   }
-}
+  __device__ __forceinline__ void add_to(float (&f)[8], int dtype) const {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (dtype == MOE_DTYPE_FP32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] += __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = unpack16(dtype, w[i]);
+        f[2 * i] += u.x;
+        f[2 * i + 1] += u.y;
+      }
+    }
+  }
+};
 __device__ __forceinline__ void store8(const float (&f)[8], void *p, int64_t off, int dtype) {
   if (dtype == MOE_DTYPE_FP32) {
     float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + off);
@@ -77,37 +93,57 @@ __device__ __forceinline__ void store8(const float (&f)[8], void *p, int64_t off
                    pack16(dtype, f[4], f[5]), pack16(dtype, f[6], f[7]));
   }
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-// f[i] = sum over the cluster's ranks, in rank order, of 8 floats at `p`
-__device__ __forceinline__ void cluster_add8(float (&f)[8], const float *p, int split) {
+// `bytes` of this CTA's shared memory to another's, counted on that CTA's barrier.
+__device__ __forceinline__ void bulk_send(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// The cluster's barrier in two halves.  Arrivals release what was written
+// before (to any shared memory of the cluster), the wait acquires it.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// f[i] = sum over the ranks, in rank order, of 8 floats of their partial tiles
+__device__ __forceinline__ void add_parts(float (&f)[8], const float *p, int split, int stride) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = 0.f;
-#pragma unroll 4
-  for (int r = 0; r < split; ++r) {
-    const uint32_t a = cluster_addr(p, (uint32_t)r);
-    const float4 lo = ld_cluster4(a), hi = ld_cluster4(a + 16);
+  for (int r = 0; r < split; ++r, p += stride) {
+    const float4 lo = reinterpret_cast<const float4 *>(p)[0];
+    const float4 hi = reinterpret_cast<const float4 *>(p)[1];
     f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
     f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
   }
 }
 
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *m, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m), "r"(c0),
+               "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *m, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 template <bool kGated, bool kE4m3>
 __global__ void __launch_bounds__(kThreads)
     dense_small_kernel(const __grid_constant__ SmallMaps maps, const SmallArgs a) {
-  constexpr uint32_t kCode = kStatusTimeoutDense;
   constexpr int kCols = kGated ? 64 : 128;  // output columns of a tile
   constexpr int kKb = kE4m3 ? 128 : 64;     // K elements of a stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kMaxStages], tfull;
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kMaxStages], tfull, recv;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
@@ -121,23 +157,18 @@ __global__ void __launch_bounds__(kThreads)
       mbar_init(&sf_full[s], 4);
     }
     mbar_init(&tfull, 1);
+    mbar_init(&recv, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&tmem_slot, a.tmem_cols);
     tmem_relinquish();
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     tma_prefetch_desc(&maps.w);
     tma_prefetch_desc(&maps.x);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_wait();
-  pdl_launch_dependents();
-  const uint32_t tmem = tmem_slot;
   const int tile = blockIdx.x / a.split;
   const int c0 = tile * kCols;              // first output column
   const int t0 = blockIdx.y * a.n;          // first row of X
@@ -145,13 +176,51 @@ __global__ void __launch_bounds__(kThreads)
   const int nkb = (a.K + kKb - 1) / kKb;
   const int k0 = (int)((int64_t)nkb * rank / a.split);
   const int k1 = (int)((int64_t)nkb * (rank + 1) / a.split);
-  float *part = reinterpret_cast<float *>(ring);  // [n][128] once the ring is done
+  // [rank][own][128]: every rank's partial tile of this CTA's rows
+  float *part = reinterpret_cast<float *>(ring + a.part_off);
+  // Until the kernel before this one is done nothing may be read, but W's first
+  // stages may come to L2: whatever is still written to them goes there too.
+  // (One ring of them: 4096 x 4096 at one row 9.0 -> 8.3 us; all of W measured
+  // slower, 14336 x 4096 21 -> 26 us.)
+  if (warp == kTmaWarp && lane == 0)
+    for (int kb = k0; kb < min(k1, k0 + a.stages); ++kb) {
+      if (kGated)
+        tma_prefetch_3d(&maps.w, kb * kKb, c0, 0);
+      else
+        tma_prefetch_2d(&maps.w, kb * kKb, c0);
+    }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t tmem = tmem_slot;
+  // this CTA runs, so its shared memory may be written (nothing to release yet)
+  if (!a.bulk) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-  if (warp == 4) {
+  // This CTA's rows of X, 8 columns a thread.
+  constexpr int kGroups = kCols / 8;
+  const int first = (int)rank * a.own;
+  const int units = max(0, min(a.own, rows - first)) * kGroups;
+  const int stride = a.own * 128;
+  const bool alone = a.split == 1;
+  if (a.bulk && !alone && threadIdx.x == 0)
+    mbar_arrive_expect_tx(&recv, (uint32_t)(a.split * (units / kGroups)) * 512u);
+  Values8 r = {}, b = {};
+  auto fetch = [&](int u) {
+    const int t = u / kGroups, c = c0 + (u - t * kGroups) * 8;
+    if (u >= units || c >= a.N) return;
+    if (!kGated && a.bias != nullptr) b.load(a.bias, c, a.out_dtype);
+    if (a.residual != nullptr)
+      r.load(a.residual, (int64_t)(t0 + first + t) * a.ldr + c, a.out_dtype);
+  };
+  fetch(threadIdx.x);  // the first long before it is needed
+
+  if (warp == kTmaWarp) {
     if (lane == 0) {
       uint32_t st = 0, ph = 0, issued = 0;
       for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(&empty[st], ph ^ 1u, &abort_flag, a.status, kCode)) break;
+        if (!mbar_wait(&empty[st], ph ^ 1u, &abort_flag, a.status, kStatusTimeoutDense)) break;
         mbar_arrive_expect_tx(&full[st], stage_bytes);
         uint8_t *dst = ring + st * stage_bytes;
         if (kGated)
@@ -174,14 +243,14 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     if (lane == 0) {
       const uint32_t idesc = kE4m3 ? idesc_mxf8(128, a.n) : idesc_16(a.dtype, false, false, 128, a.n);
       const uint64_t w0 = sdesc_k_sw128(smem_u32(ring));
       uint32_t st = 0, ph = 0;
       for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(&full[st], ph, &abort_flag, a.status, kCode)) break;
-        if (kE4m3 && !mbar_wait(&sf_full[st], ph, &abort_flag, a.status, kCode)) break;
+        if (!mbar_wait(&full[st], ph, &abort_flag, a.status, kStatusTimeoutDense)) break;
+        if (kE4m3 && !mbar_wait(&sf_full[st], ph, &abort_flag, a.status, kStatusTimeoutDense)) break;
         tc_fence_after();
         const uint64_t wd = w0 + st * (stage_bytes >> 4), xd = wd + (kWBytes >> 4);
         const uint32_t sf = tmem + a.sf_col + st * kSmallSfCols;
@@ -206,27 +275,27 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     if (kE4m3) {
       // Scale factors of stage kb, the same in each warp's 32 lanes: column j
-      // of the first 4 holds W rows 32 j + lane, of the next 8 X rows 32 j +
+      // of the first 4 holds W rows 32 j + lane, of the next 4 X rows 32 j +
       // lane; the word's four bytes are the four 32-deep parts of the 128.
       const int nb = nkb;
       const int8_t *ws = a.w_scale + (int64_t)(c0 / 128) * nb;
       uint32_t st = 0, ph = 0;
       for (int kb = k0; kb < k1 && ok; ++kb) {
         const uint32_t w = e8m0x4(ws[kb]);
-        uint32_t x[8];
+        uint32_t x[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const int t = 32 * j + lane;
           x[j] = t < rows ? e8m0x4(a.x_scale[(int64_t)(t0 + t) * nb + kb]) : 0x7f7f7f7fu;
         }
         ok = __all_sync(0xffffffffu,
-                        mbar_wait(&empty[st], ph ^ 1u, &abort_flag, a.status, kCode));
+                        mbar_wait(&empty[st], ph ^ 1u, &abort_flag, a.status, kStatusTimeoutDense));
         if (!ok) break;
         tc_fence_after();
         const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + a.sf_col + st * kSmallSfCols;
         const uint32_t w4[4] = {w, w, w, w};
         tmem_st4(at, w4);
-        tmem_st8(at + 4, x);
+        tmem_st4(at + 4, x);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -237,53 +306,134 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
-    ok = mbar_wait(&tfull, 0, &abort_flag, a.status, kCode) && ok;
-    if (__all_sync(0xffffffffu, ok)) {
-      tc_fence_after();
-      const uint32_t tb = tmem + ((uint32_t)(warp * 32) << 16);
-      float *p = part + warp * 32 + lane;
-      for (int q = 0; q < a.n; q += 16) {
-        float v[16];
-        tmem_ld16f(tb + q, v);
+    ok = mbar_wait(&tfull, 0, &abort_flag, a.status, kStatusTimeoutDense) && ok;
+    ok = __all_sync(0xffffffffu, ok);
+    const uint32_t tb = tmem + ((uint32_t)(warp * 32) << 16);
+    if (a.bulk) {
+      // the ring's place: this CTA's partial tile [row of X][row of W], then
+      // what it receives
+      cluster_arrive();  // this CTA's ring is done
+      if (ok) {
+        tc_fence_after();
+        float *p = reinterpret_cast<float *>(ring) + warp * 32 + lane;
+        for (int q = 0; q < rows; q += 16) {
+          float v[16];
+          tmem_ld16f(tb + q, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[(q + i) * 128] = v[i];
+          for (int i = 0; i < 16; ++i) p[(q + i) * 128] = v[i];
+        }
+      }
+      fence_proxy_async_shared();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      cluster_wait();  // every ring is done
+      const int to = (int)threadIdx.x;
+      if (ok && !alone && to < a.split) {
+        const int n = min(a.own, rows - to * a.own);
+        if (n > 0)
+          bulk_send(cluster_addr(part + (int)rank * stride, (uint32_t)to),
+                    ring + (uint32_t)(to * a.own) * 512u, (uint32_t)n * 512u,
+                    cluster_addr(&recv, (uint32_t)to));
+      }
+    } else {
+      cluster_wait();  // every CTA runs
+      if (ok) {
+        // each row of X goes to the CTA that adds it: 128 bytes a warp and row
+        tc_fence_after();
+        const float *p = part + (int)rank * stride + warp * 32 + lane;
+        float v[16];
+        tmem_ld16f(tb, v);
+        int to = 0, t = 0;  // rank, its row
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (i < rows) st_cluster(cluster_addr(p + t * 128, (uint32_t)to), v[i]);
+          if (++t == a.own) {
+            t = 0;
+            ++to;
+          }
+        }
       }
     }
     tc_fence_before();
+    __syncwarp();
   }
-  cluster_sync_all();  // partial tiles of every rank in place
-  tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, a.tmem_cols);
-
-  if (!abort_flag) {
-    constexpr int kGroups = kCols / 8;
-    const int units = rows * kGroups;
-    for (int u = (int)threadIdx.x * a.split + (int)rank; u < units; u += kThreads * a.split) {
-      const int t = u / kGroups, g = u - t * kGroups, c = c0 + g * 8;
-      if (c >= a.N) continue;
-      const int64_t row = t0 + t;
-      float f[8], r[8], b[8];
-      if (!kGated && a.bias != nullptr) load8(b, a.bias, c, a.out_dtype);
-      if (a.residual != nullptr) load8(r, a.residual, row * a.ldr + c, a.out_dtype);
-      cluster_add8(f, part + t * 128 + g * 8, a.split);
+  if (warp >= kTmaWarp) {
+    if (a.bulk) cluster_arrive();
+    cluster_wait();
+  }
+  // every rank's partial tile is here
+  if (a.bulk) {
+    const bool got = alone || units == 0 || mbar_wait(&recv, 0, &abort_flag, a.status, kStatusTimeoutDense);
+    tc_fence_before();
+    __syncthreads();  // and TMEM has been read
+    tc_fence_after();
+    if (!got) abort_flag = 1;
+    cluster_arrive();  // received: the others' copies no longer read their shared memory
+  } else {
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+  }
+  if (warp == kMmaWarp) tmem_dealloc(tmem, a.tmem_cols);
+  const int todo = abort_flag ? 0 : units;
+  for (int u = (int)threadIdx.x; u < todo; u += kThreads) {
+    const int t = u / kGroups, g = u - t * kGroups, c = c0 + g * 8;
+    if (c < a.N) {
+      float f[8];
+      add_parts(f, part + t * 128 + g * 8, a.split, stride);
       if (kGated) {
         float up[8];
-        cluster_add8(up, part + t * 128 + 64 + g * 8, a.split);
+        add_parts(up, part + t * 128 + 64 + g * 8, a.split, stride);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = f[i] * sigmoid(f[i]) * up[i];
       } else {
-        if (a.bias != nullptr)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] += b[i];
+        if (a.bias != nullptr) b.add_to(f, a.out_dtype);
         activate_all(a.act, f);
       }
-      if (a.residual != nullptr)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += r[i];
-      store8(f, a.d, row * a.ldd + c, a.out_dtype);
+      if (a.residual != nullptr) r.add_to(f, a.out_dtype);
+      store8(f, a.d, (int64_t)(t0 + first + t) * a.ldd + c, a.out_dtype);
+    }
+    fetch(u + kThreads);
+  }
+  __syncwarp();
+  if (a.bulk) cluster_wait();  // this CTA's copies have been received
+}
+
+// Rows of X a tile, tiles, parts of K and about how long it takes (us).
+struct SmallPlan {
+  int n, chunks, split;
+  float us;
+};
+
+// The split with the least estimated time, fitted as plan_pair's: a stage takes
+// 0.27 us and 0.0012 for each row of X (E4M3: a tenth more; half as much again
+// where SMs hold two CTAs), a launch 6.5 us, the exchange of a split 1 us; HBM
+// takes what W's bytes take.  A split that does not fit in one round loses (192
+// rows of 4096 x 4096: 26 us split by four, 20 by two).  Tiles of 128 rows
+// measured no faster.
+SmallPlan plan_small(const DenseGemm &g) {
+  const bool e4m3 = g.dtype == MOE_DTYPE_E4M3;
+  const int cols = g.epi == kEpiGated ? 64 : 128, kb = e4m3 ? 128 : 64;
+  const int nkb = (g.K + kb - 1) / kb;
+  SmallPlan p = {};
+  p.chunks = (g.M + kChunk - 1) / kChunk;
+  p.n = ((g.M + p.chunks - 1) / p.chunks + 15) / 16 * 16;
+  const int64_t tiles = (int64_t)((g.N + cols - 1) / cols) * p.chunks;
+  const float stage = (0.27f + 0.0012f * (float)p.n) * (e4m3 ? 1.1f : 1.0f);
+  const float hbm = (float)g.N * (float)g.K * (g.epi == kEpiGated ? 2.f : 1.f) *
+                    (float)type_bytes(g.dtype) / 6.6e6f;
+  for (int split = 1; split == 1 || (split <= kMaxSplit && 2 * split <= nkb); split *= 2) {
+    const int64_t ctas = tiles * split, slots = 2 * num_sms();
+    if (split > 1 && ctas > slots) break;
+    const int64_t rounds = (ctas + slots - 1) / slots;
+    const float stages = (float)(rounds * ((nkb + split - 1) / split));
+    const float us = 6.5f + std::max(stages * stage * (ctas > num_sms() ? 1.5f : 1.0f), hbm) +
+                     (split == 1 ? 0.f : 1.f);
+    if (p.us == 0.f || us <= p.us) {
+      p.us = us;
+      p.split = split;
     }
   }
-  cluster_sync_all();  // no CTA's shared memory goes while a peer reads it
+  return p;
 }
 
 template <bool kGated, bool kE4m3>
@@ -292,32 +442,32 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
   constexpr int kCols = kGated ? 64 : 128, kKb = kE4m3 ? 128 : 64;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const SmallPlan plan = plan_small(g);
 
   SmallArgs a = {};
   a.T = g.M;
   a.N = g.N;
   a.K = g.K;
-  const int chunks = (g.M + kSmallRows - 1) / kSmallRows;
-  a.n = ((g.M + chunks - 1) / chunks + 15) / 16 * 16;
+  a.n = plan.n;
+  a.split = plan.split;
   const uint32_t stage = kWBytes + (uint32_t)a.n * 128u;
-  // Two CTAs share an SM while a ring of at least four stages fits in half of
-  // its shared memory (n <= 64): one streams while the other adds and stores.
-  const int per_sm = a.n <= 64 ? 2 : 1;
-  const uint32_t room = per_sm == 2 ? 110u * 1024u : 220u * 1024u;
-  a.stages = std::min<int>(kMaxStages, (int)(room / stage));
-  const size_t smem = 1024 + (size_t)a.stages * stage;
+  // Two CTAs share an SM: one streams while the other adds and stores.
+  a.stages = std::min<int>(kMaxStages, (int)(102u * 1024u / stage));
   uint32_t cols = (uint32_t)a.n;
   a.sf_col = cols;
   if (kE4m3) cols += (uint32_t)a.stages * kSmallSfCols;
   a.tmem_cols = 32;
   while (a.tmem_cols < cols) a.tmem_cols *= 2;
 
-  // As many parts of K as keep every CTA resident at once.
-  const int tiles = (g.N + kCols - 1) / kCols * chunks;
-  const int nkb = (g.K + kKb - 1) / kKb;
-  a.split = 1;
-  while (a.split < kMaxSplit && tiles * a.split * 2 <= num_sms() * per_sm && a.split * 2 <= nkb)
-    a.split *= 2;
+  // Up to 16 rows: single stores to a place behind the ring (8 KB), as soon as
+  // a CTA is done.  More: bulk copies, out of and into the ring's place, after
+  // every CTA of the cluster is done (single stores took 4 us at 64 rows).
+  a.own = (a.n + a.split - 1) / a.split;
+  a.bulk = a.n > 16;
+  const uint32_t ring_bytes = (uint32_t)a.stages * stage;
+  const uint32_t part_bytes = (uint32_t)(a.split * a.own) * 512u;
+  a.part_off = !a.bulk ? ring_bytes : (a.split == 1 ? 0u : (uint32_t)a.n * 512u);
+  const size_t smem = 1024 + std::max(ring_bytes, a.part_off + part_bytes);
 
   a.dtype = g.dtype;
   a.out_dtype = g.out_dtype;
@@ -354,7 +504,7 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(tiles / chunks * a.split), (unsigned)chunks);
+  cfg.gridDim = dim3((unsigned)((g.N + kCols - 1) / kCols * a.split), (unsigned)plan.chunks);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -364,6 +514,8 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
 }
 
 }  // namespace
+
+float dense_small_us(const DenseGemm &g) { return plan_small(g).us; }
 
 cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s) {
   if (g.dtype == MOE_DTYPE_E4M3) return launch<false, true>(g, s);

@@ -14,7 +14,11 @@
 // codes); backward: 3 read, 1 written.  A row lives in the registers of one
 // group of threads (kV chunks of 8 elements a thread), so every tensor is read
 // once, and the mean costs one shuffle reduction and one exchange through
-// shared memory.
+// shared memory.  With many rows the CTAs stay and walk the rows, and each
+// thread copies its own chunks of the next rows to shared memory meanwhile
+// (cp.async into a ring that no other thread touches): loads stay in flight
+// through the reductions without taking registers.  The arithmetic is done on
+// pairs (f32x2): with one instruction an element it took as long as the bytes.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -26,76 +30,170 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormBwdThreads = 512;
+constexpr int kNormRowThreads = 512;  // of the CTAs that walk rows
 
-// 8 consecutive elements as loaded: 16 bytes (bf16, fp16) or 32 (fp32).
+// ---------------------------------------------------------- pairs of fp32 --
+
+typedef unsigned long long pair_t;  // (low word, high word)
+
+__device__ __forceinline__ pair_t make_pair(float lo, float hi) {
+  pair_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float lo_of(pair_t p) {
+  return __uint_as_float((uint32_t)p);
+}
+__device__ __forceinline__ float hi_of(pair_t p) {
+  return __uint_as_float((uint32_t)(p >> 32));
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
+  pair_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
+  pair_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
+  pair_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// --------------------------------------------------------------- chunks --
+
+// A chunk is 8 elements in pieces of 16 bytes: one piece of 8 (bf16, fp16) or
+// two of 4 (fp32).  Piece i of a thread's chunk v is number (v * pieces + i) *
+// group + thread of the row, so a warp's pieces lie side by side.
 template <typename T>
-struct Raw8 {
-  uint4 a[sizeof(T) / 2];
+struct Chunk {
+  static constexpr int kPieces = sizeof(T) / 2;
+  static constexpr int kEach = 8 / kPieces;  // elements of a piece
+  uint4 a[kPieces];
 };
-
 template <typename T>
-__device__ __forceinline__ Raw8<T> load_raw(const T *p) {
-  Raw8<T> r;
-  // not the read-only path: outputs may overlay inputs row for row
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.a[i].x), "=r"(r.a[i].y), "=r"(r.a[i].z), "=r"(r.a[i].w)
-                 : "l"(reinterpret_cast<const uint4 *>(p) + i));
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ Raw8<T> zero_raw() {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.a[i] = make_uint4(0, 0, 0, 0);
-  return r;
+__device__ __forceinline__ int column(int v, int i, int group, int t) {
+  return ((v * Chunk<T>::kPieces + i) * group + t) * Chunk<T>::kEach;
 }
 
-__device__ __forceinline__ void to_float(const Raw8<__nv_bfloat16> &r, float (&f)[8]) {
-  const uint32_t w[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
+// `p`: the row.  Pieces past H (or all, where `live` is false) are zero.
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_chunk(const T *p, int v, int group, int t, int H,
+                                               bool live) {
+  Chunk<T> r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < Chunk<T>::kPieces; ++i) {
+    const int c = column<T>(v, i, group, t);
+    r.a[i] = make_uint4(0, 0, 0, 0);
+    // not the read-only path: outputs may overlay inputs row for row
+    if (live && c < H)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.a[i].x), "=r"(r.a[i].y), "=r"(r.a[i].z), "=r"(r.a[i].w)
+                   : "l"(p + c));
+  }
+  return r;
+}
+
+// A thread's ring in shared memory: `at` is this thread's 16 bytes of a chunk's
+// first piece; the pieces of all threads of the CTA lie side by side.
+template <typename T>
+__device__ __forceinline__ void ring_fill(uint32_t at, const T *p, int v, int group, int t, int H,
+                                          int threads) {
+#pragma unroll
+  for (int i = 0; i < Chunk<T>::kPieces; ++i) {
+    const int c = column<T>(v, i, group, t);
+    if (c < H)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + i * threads * 16),
+                   "l"(p + c)
+                   : "memory");
   }
 }
-__device__ __forceinline__ void to_float(const Raw8<__half> &r, float (&f)[8]) {
+template <typename T>
+__device__ __forceinline__ Chunk<T> ring_read(uint32_t at, int v, int group, int t, int H,
+                                              int threads, bool live) {
+  Chunk<T> r;
+#pragma unroll
+  for (int i = 0; i < Chunk<T>::kPieces; ++i) {
+    r.a[i] = make_uint4(0, 0, 0, 0);
+    if (live && column<T>(v, i, group, t) < H)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.a[i].x), "=r"(r.a[i].y), "=r"(r.a[i].z), "=r"(r.a[i].w)
+                   : "r"(at + i * threads * 16)
+                   : "memory");
+  }
+  return r;
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `ahead` (at most 3) of this thread's fills have landed.
+__device__ __forceinline__ void ring_wait(int ahead) {
+  switch (ahead) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
+
+__device__ __forceinline__ void to_pairs(const Chunk<__nv_bfloat16> &r, pair_t (&f)[4]) {
+  const uint32_t w[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = make_pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void to_pairs(const Chunk<__half> &r, pair_t (&f)[4]) {
   const uint32_t w[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
+    f[i] = make_pair(v.x, v.y);
   }
 }
-__device__ __forceinline__ void to_float(const Raw8<float> &r, float (&f)[8]) {
+__device__ __forceinline__ void to_pairs(const Chunk<float> &r, pair_t (&f)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    f[4 * i] = __uint_as_float(r.a[i].x);
-    f[4 * i + 1] = __uint_as_float(r.a[i].y);
-    f[4 * i + 2] = __uint_as_float(r.a[i].z);
-    f[4 * i + 3] = __uint_as_float(r.a[i].w);
+    f[2 * i] = make_pair(__uint_as_float(r.a[i].x), __uint_as_float(r.a[i].y));
+    f[2 * i + 1] = make_pair(__uint_as_float(r.a[i].z), __uint_as_float(r.a[i].w));
   }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ Chunk<__nv_bfloat16> from_pairs(const pair_t (&f)[4], __nv_bfloat16) {
+  Chunk<__nv_bfloat16> r;
+  r.a[0] = make_uint4(pack_bf16x2(lo_of(f[0]), hi_of(f[0])), pack_bf16x2(lo_of(f[1]), hi_of(f[1])),
+                      pack_bf16x2(lo_of(f[2]), hi_of(f[2])), pack_bf16x2(lo_of(f[3]), hi_of(f[3])));
+  return r;
 }
-__device__ __forceinline__ void store8(__half *p, const float (&f)[8]) {
+__device__ __forceinline__ Chunk<__half> from_pairs(const pair_t (&f)[4], __half) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    const __half2 h = __floats2half2_rn(lo_of(f[i]), hi_of(f[i]));
     w[i] = *reinterpret_cast<const uint32_t *>(&h);
   }
-  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  Chunk<__half> r;
+  r.a[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  return r;
 }
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ Chunk<float> from_pairs(const pair_t (&f)[4], float) {
+  Chunk<float> r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r.a[i] = make_uint4(__float_as_uint(lo_of(f[2 * i])), __float_as_uint(hi_of(f[2 * i])),
+                        __float_as_uint(lo_of(f[2 * i + 1])), __float_as_uint(hi_of(f[2 * i + 1])));
+  return r;
+}
+// Rounded to T, to the row `p`.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T *p, const pair_t (&f)[4], int v, int group, int t,
+                                            int H) {
+  const Chunk<T> r = from_pairs(f, T());
+#pragma unroll
+  for (int i = 0; i < Chunk<T>::kPieces; ++i) {
+    const int c = column<T>(v, i, group, t);
+    if (c < H) *reinterpret_cast<uint4 *>(p + c) = r.a[i];
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -121,89 +219,157 @@ struct NormArgs {
   int8_t *scale;
   int64_t x_stride, r_stride, y_stride;
   int T, H, group, rows;  // threads to a row, rows to a CTA
+  int depth;              // rows of the ring
   float eps;
 };
 
-// kV: chunks of 8 elements a thread.  A CTA takes `rows` rows, `group` threads
-// (whole warps) to each; thread i of a group holds chunks i, i + group, ..., so
-// the 128 elements that share an 8-bit scale lie in 16 neighbouring lanes.
+// y of a chunk as E4M3 codes.  A block of 128 elements lies in 16 neighbouring
+// lanes (8 elements each) or, piece by piece, in 32 (fp32).
+template <typename T>
+__device__ __forceinline__ void store_codes(const NormArgs &a, const pair_t (&y)[4], int64_t row,
+                                            int v, int t, bool live) {
+  constexpr int kPieces = Chunk<T>::kPieces, kPairs = 4 / kPieces;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const pair_t *p = y + i * kPairs;
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) m = fmaxf(m, fmaxf(fabsf(lo_of(p[j])), fabsf(hi_of(p[j]))));
+#pragma unroll
+    for (int o = 64 / Chunk<T>::kEach; o > 0; o >>= 1)
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = block_exp(m);
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    const int c = column<T>(v, i, a.group, t);
+    if (!live || c >= a.H) continue;
+    uint32_t w[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+      w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo_of(p[j]) * inv, hi_of(p[j]) * inv),
+                                                __NV_SATFINITE, __NV_E4M3);
+    uint8_t *q = a.q + row * a.H + c;
+    if (kPairs == 4)
+      *reinterpret_cast<uint2 *>(q) =
+          make_uint2(w[0] | w[1] << 16, w[kPairs > 2 ? 2 : 0] | w[kPairs > 2 ? 3 : 0] << 16);
+    else
+      *reinterpret_cast<uint32_t *>(q) = w[0] | w[1] << 16;
+    if ((c & 127) == 0) a.scale[row * ((a.H + 127) >> 7) + (c >> 7)] = (int8_t)e;
+  }
+}
+
+// This thread's chunks of a row, s = x + residual: residual_out and, once the
+// row's mean is known, y and its codes.  `part`: one float for each warp.
 template <typename T, int kV>
-__global__ void __launch_bounds__(kV == 4 ? kNormMaxThreads / 2 : kNormMaxThreads)
-    add_rms_norm_kernel(const NormArgs a) {
-  __shared__ float s_part[kNormMaxThreads / 32];
-  const int sub = threadIdx.x / a.group, t = threadIdx.x - sub * a.group;
-  const int64_t row = (int64_t)blockIdx.x * a.rows + sub;
+__device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)[kV],
+                                         const Chunk<T> (&rr)[kV], const Chunk<T> (&rw)[kV],
+                                         int64_t row, int sub, int t, float *part) {
   const bool live = row < a.T;
-  const int nch = a.H >> 3;
+  pair_t s[kV][4], sq = make_pair(0.f, 0.f);
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    pair_t r[4];
+    to_pairs(rx[v], s[v]);
+    to_pairs(rr[v], r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[v][i] = add2(s[v][i], r[i]);
+      sq = fma2(s[v][i], s[v][i], sq);
+    }
+    if (a.residual_out != nullptr && live)
+      store_chunk(static_cast<T *>(a.residual_out) + row * a.r_stride, s[v], v, a.group, t, a.H);
+  }
+  const float mine = warp_sum(lo_of(sq) + hi_of(sq));
+  const int warps = a.group >> 5;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  float sum = 0.f;
+  for (int i = 0; i < warps; ++i) sum += part[sub * warps + i];
+  const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+  const pair_t r2 = make_pair(rstd, rstd);
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    pair_t w[4], y[4];
+    to_pairs(rw[v], w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(s[v][i], r2), w[i]);
+    if (a.y != nullptr && live)
+      store_chunk(static_cast<T *>(a.y) + row * a.y_stride, y, v, a.group, t, a.H);
+    if (a.q != nullptr) store_codes<T>(a, y, row, v, t, live);
+  }
+}
+
+// Few rows: a CTA (whole warps) to a row.
+template <typename T, int kV>
+__global__ void __launch_bounds__(kNormMaxThreads) add_rms_norm_kernel(const NormArgs a) {
+  __shared__ float part[kNormMaxThreads / 32];
+  const int64_t row = blockIdx.x;
+  const int t = threadIdx.x;
   const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
   const T *res = static_cast<const T *>(a.residual) + row * a.r_stride;
   pdl_wait();
-  Raw8<T> rx[kV], rr[kV], rw[kV];
+  Chunk<T> rx[kV], rr[kV], rw[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    const int c = t + v * a.group;
-    const bool in = live && c < nch;
-    rx[v] = in ? load_raw(x + c * 8) : zero_raw<T>();
-    rr[v] = in && a.residual != nullptr ? load_raw(res + c * 8) : zero_raw<T>();
+    rx[v] = load_chunk(x, v, a.group, t, a.H, true);
+    rr[v] = load_chunk(res, v, a.group, t, a.H, a.residual != nullptr);
   }
 #pragma unroll
-  for (int v = 0; v < kV; ++v) {
-    const int c = t + v * a.group;
-    rw[v] = c < nch ? load_raw(static_cast<const T *>(a.weight) + c * 8) : zero_raw<T>();
-  }
+  for (int v = 0; v < kV; ++v)
+    rw[v] = load_chunk(static_cast<const T *>(a.weight), v, a.group, t, a.H, true);
   pdl_launch_dependents();
-  float s[kV][8];
-  float sq = 0.f;
+  norm_row<T, kV>(a, rx, rr, rw, row, 0, t, part);
+}
+
+// Many rows: CTA b's group g walks rows b * rows + g, + gridDim.x * rows, ...
+// with `depth` - 1 rows on their way to its ring.
+template <typename T, int kV>
+__global__ void __launch_bounds__(kNormRowThreads) add_rms_norm_rows_kernel(const NormArgs a) {
+  __shared__ float part[2][kNormRowThreads / 32];
+  extern __shared__ uint4 s_ring[];
+  const int sub = threadIdx.x / a.group, t = threadIdx.x - sub * a.group;
+  const int threads = blockDim.x;
+  const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
+  const uint32_t chunk = (uint32_t)threads * 16u * (uint32_t)Chunk<T>::kPieces;
+  const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16u;
+  pdl_wait();
+  pdl_launch_dependents();
+  Chunk<T> rw[kV];
 #pragma unroll
-  for (int v = 0; v < kV; ++v) {
-    float r[8];
-    to_float(rx[v], s[v]);
-    to_float(rr[v], r);
+  for (int v = 0; v < kV; ++v)
+    rw[v] = load_chunk(static_cast<const T *>(a.weight), v, a.group, t, a.H, true);
+  auto fill = [&](int64_t row, int slot) {
+    if (row < a.T) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s[v][i] += r[i];
-      sq = fmaf(s[v][i], s[v][i], sq);
-    }
-    const int c = t + v * a.group;
-    if (a.residual_out != nullptr && live && c < nch)
-      store8(static_cast<T *>(a.residual_out) + row * a.r_stride + c * 8, s[v]);
-  }
-  sq = warp_sum(sq);
-  const int warps = a.group >> 5;
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = sq;
-  __syncthreads();
-  float sum = 0.f;
-  for (int i = 0; i < warps; ++i) sum += s_part[sub * warps + i];
-  const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
-#pragma unroll
-  for (int v = 0; v < kV; ++v) {
-    const int c = t + v * a.group;
-    const bool in = live && c < nch;
-    float w[8], y[8];
-    to_float(rw[v], w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = s[v][i] * rstd * w[i];
-    if (a.y != nullptr && in) store8(static_cast<T *>(a.y) + row * a.y_stride + c * 8, y);
-    if (a.q != nullptr) {
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int e = block_exp(m);
-      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-      if (in) {
-        uint32_t w2[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = make_float2(y[2 * i] * inv, y[2 * i + 1] * inv);
-          w2[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)
-                        << (16 * (i & 1));
-        }
-        *reinterpret_cast<uint2 *>(a.q + row * a.H + c * 8) = make_uint2(w2[0], w2[1]);
-        if ((c & 15) == 0) a.scale[row * ((a.H + 127) >> 7) + (c >> 4)] = (int8_t)e;
+      for (int v = 0; v < kV; ++v) {
+        const uint32_t at = ring + (uint32_t)(slot * 2 * kV + v) * chunk;
+        ring_fill(at, x + row * a.x_stride, v, a.group, t, a.H, threads);
+        if (res != nullptr)
+          ring_fill(at + kV * chunk, res + row * a.r_stride, v, a.group, t, a.H, threads);
       }
     }
+    ring_commit();
+  };
+  const int64_t step = (int64_t)gridDim.x * a.rows;
+  int64_t row = (int64_t)blockIdx.x * a.rows + sub, ahead = row;
+  for (int i = 0; i + 1 < a.depth; ++i, ahead += step) fill(ahead, i);
+  int slot = 0, next = a.depth - 1, buf = 0;
+  // every group makes the same number of trips (the barrier is the CTA's)
+  for (int64_t r0 = (int64_t)blockIdx.x * a.rows; r0 < a.T; r0 += step, row += step, ahead += step) {
+    fill(ahead, next);  // of depth 1 the row itself
+    ring_wait(a.depth - 1);
+    Chunk<T> rx[kV], rr[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+      const uint32_t at = ring + (uint32_t)(slot * 2 * kV + v) * chunk;
+      rx[v] = ring_read<T>(at, v, a.group, t, a.H, threads, row < a.T);
+      rr[v] = ring_read<T>(at + kV * chunk, v, a.group, t, a.H, threads,
+                           row < a.T && res != nullptr);
+    }
+    // two buffers of partial sums: the next trip writes the other one
+    norm_row<T, kV>(a, rx, rr, rw, row, sub, t, part[buf]);
+    buf ^= 1;
+    slot = slot + 1 == a.depth ? 0 : slot + 1;
+    next = next + 1 == a.depth ? 0 : next + 1;
   }
 }
 
@@ -212,214 +378,262 @@ struct NormBwdArgs {
   void *dx;
   float *part;  // [CTAs][H]
   int64_t dy_stride, s_stride, dx_stride;
-  int T, H, group, rows;
+  int T, H, group, rows, depth;
   float eps;
 };
 
-// Persistent: CTA b's group g walks rows b * rows + g, + gridDim.x * rows, ...
-// with the next row's loads in flight while this row is reduced.  dy n is kept
-// per column in registers, joined over the CTA's groups through shared memory
-// at the end and left as one row of partials for the second kernel: a fixed
-// order, so the sums do not change from run to run.
+// As add_rms_norm_rows_kernel.  dy n is kept per column in registers, joined
+// over the CTA's groups through shared memory at the end and left as one row of
+// partials for the second kernel: a fixed order, so the sums do not change from
+// run to run.
 template <typename T, int kV>
-__global__ void __launch_bounds__(kNormBwdThreads) add_rms_norm_bwd_kernel(const NormBwdArgs a) {
-  __shared__ float2 s_part[2][kNormBwdThreads / 32];
-  extern __shared__ float s_dw[];  // [rows][H] when rows > 1
+__global__ void __launch_bounds__(kNormRowThreads) add_rms_norm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float2 s_part[2][kNormRowThreads / 32];
+  extern __shared__ uint4 s_ring[];
+  // wide or fp32 rows leave no registers for the weight: it is read from L1
+  constexpr bool kKeepWeight = kV == 2 && sizeof(T) == 2, kKeepProduct = kV == 2;
   const int sub = threadIdx.x / a.group, t = threadIdx.x - sub * a.group;
-  const int nch = a.H >> 3, warps = a.group >> 5;
+  const int warps = a.group >> 5, threads = blockDim.x;
   const T *dy = static_cast<const T *>(a.dy), *sm = static_cast<const T *>(a.sum);
-  const T *dr = static_cast<const T *>(a.dres);
+  const T *dr = static_cast<const T *>(a.dres), *wt = static_cast<const T *>(a.weight);
+  const uint32_t chunk = (uint32_t)threads * 16u * (uint32_t)Chunk<T>::kPieces;
+  const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16u;
   pdl_wait();
-  // Two chunks of 16 bits leave room for the next row's loads and the weight
-  // in registers; wider rows or types load each row when its turn comes.
-  constexpr bool kAhead = kV == 2 && sizeof(T) == 2;
-  const T *wt = static_cast<const T *>(a.weight);
-  Raw8<T> rw[kV];
-  float acc[kV][8];
+  pdl_launch_dependents();
+  auto weight = [&](int v) {
+    Chunk<T> r;
+#pragma unroll
+    for (int i = 0; i < Chunk<T>::kPieces; ++i) {
+      const int c = column<T>(v, i, a.group, t);
+      r.a[i] = c < a.H ? __ldg(reinterpret_cast<const uint4 *>(wt + c)) : make_uint4(0, 0, 0, 0);
+    }
+    return r;
+  };
+  Chunk<T> rw[kV];
+  pair_t acc[kV][4];
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    const int c = t + v * a.group;
-    if (kAhead) rw[v] = c < nch ? load_raw(wt + c * 8) : zero_raw<T>();
+    if (kKeepWeight) rw[v] = weight(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[v][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[v][i] = make_pair(0.f, 0.f);
   }
-  pdl_launch_dependents();
-  auto fetch = [&](Raw8<T>(&to)[kV], const T *from, int64_t row, int64_t stride) {
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int c = t + v * a.group;
-      to[v] = from != nullptr && row < a.T && c < nch ? load_raw(from + row * stride + c * 8)
-                                                      : zero_raw<T>();
-    }
-  };
-  auto weight = [&](int v, float(&w)[8]) {
-    const int c = t + v * a.group;
-    if (kAhead) {
-      to_float(rw[v], w);
-    } else {
-      Raw8<T> r = zero_raw<T>();
-      if (c < nch)
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-          r.a[i] = __ldg(reinterpret_cast<const uint4 *>(wt + c * 8) + i);
-      to_float(r, w);
-    }
-  };
-  const int64_t step = (int64_t)gridDim.x * a.rows;
-  int64_t row = (int64_t)blockIdx.x * a.rows + sub;
-  Raw8<T> ns[kV], nd[kV], nr[kV];
-  if (kAhead) {
-    fetch(ns, sm, row, a.s_stride);
-    fetch(nd, dy, row, a.dy_stride);
-    fetch(nr, dr, row, a.s_stride);
-  }
-  const float inv_h = 1.0f / (float)a.H;
-  // every group makes the same number of trips (the barrier is the CTA's)
-  const int64_t first = (int64_t)blockIdx.x * a.rows;
-  int buf = 0;
-  for (int64_t r0 = first; r0 < a.T; r0 += step, row += step, buf ^= 1) {
-    Raw8<T> cs[kV], cd[kV], cr[kV];
-    if (kAhead) {
+  auto fill = [&](int64_t row, int slot) {
+    if (row < a.T) {
 #pragma unroll
       for (int v = 0; v < kV; ++v) {
-        cs[v] = ns[v];
-        cd[v] = nd[v];
-        cr[v] = nr[v];
+        const uint32_t at = ring + (uint32_t)(slot * 3 * kV + v) * chunk;
+        ring_fill(at, sm + row * a.s_stride, v, a.group, t, a.H, threads);
+        ring_fill(at + kV * chunk, dy + row * a.dy_stride, v, a.group, t, a.H, threads);
+        if (dr != nullptr)
+          ring_fill(at + 2 * kV * chunk, dr + row * a.s_stride, v, a.group, t, a.H, threads);
       }
-      fetch(ns, sm, row + step, a.s_stride);
-      fetch(nd, dy, row + step, a.dy_stride);
-      fetch(nr, dr, row + step, a.s_stride);
-    } else {
-      fetch(cs, sm, row, a.s_stride);
-      fetch(cd, dy, row, a.dy_stride);
     }
-    float2 p = make_float2(0.f, 0.f);  // sum s^2, sum w dy s
+    ring_commit();
+  };
+  const int64_t step = (int64_t)gridDim.x * a.rows;
+  int64_t row = (int64_t)blockIdx.x * a.rows + sub, ahead = row;
+  for (int i = 0; i + 1 < a.depth; ++i, ahead += step) fill(ahead, i);
+  int slot = 0, next = a.depth - 1, buf = 0;
+  const float inv_h = 1.0f / (float)a.H;
+  // every group makes the same number of trips (the barrier is the CTA's)
+  for (int64_t r0 = (int64_t)blockIdx.x * a.rows; r0 < a.T;
+       r0 += step, row += step, ahead += step, buf ^= 1) {
+    fill(ahead, next);  // of depth 1 the row itself
+    ring_wait(a.depth - 1);
+    const bool live = row < a.T;
+    pair_t s[kV][4], d[kV][4], wd[kV][4];
+    pair_t p0 = make_pair(0.f, 0.f), p1 = p0;  // sum s^2, sum w dy s
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      float s[8], d[8], w[8];
-      to_float(cs[v], s);
-      to_float(cd[v], d);
-      weight(v, w);
+      const uint32_t at = ring + (uint32_t)(slot * 3 * kV + v) * chunk;
+      pair_t w[4];
+      to_pairs(ring_read<T>(at, v, a.group, t, a.H, threads, live), s[v]);
+      to_pairs(ring_read<T>(at + kV * chunk, v, a.group, t, a.H, threads, live), d[v]);
+      to_pairs(kKeepWeight ? rw[v] : weight(v), w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p.x = fmaf(s[i], s[i], p.x);
-        p.y = fmaf(w[i] * d[i], s[i], p.y);
+      for (int i = 0; i < 4; ++i) {
+        const pair_t x = mul2(w[i], d[v][i]);
+        if (kKeepProduct) wd[v][i] = x;
+        p0 = fma2(s[v][i], s[v][i], p0);
+        p1 = fma2(x, s[v][i], p1);
       }
     }
-    p.x = warp_sum(p.x);
-    p.y = warp_sum(p.y);
+    float2 p = make_float2(warp_sum(lo_of(p0) + hi_of(p0)), warp_sum(lo_of(p1) + hi_of(p1)));
     if ((threadIdx.x & 31) == 0) s_part[buf][threadIdx.x >> 5] = p;
     __syncthreads();  // two buffers: the next trip writes the other one
-    float2 q = make_float2(0.f, 0.f);
+    p = make_float2(0.f, 0.f);
     for (int i = 0; i < warps; ++i) {
       const float2 o = s_part[buf][sub * warps + i];
-      q.x += o.x;
-      q.y += o.y;
+      p.x += o.x;
+      p.y += o.y;
     }
-    const float r = 1.0f / sqrtf(q.x * inv_h + a.eps);
-    const float mr = q.y * inv_h * r * r;  // times s: n mean(w dy n) = s r * (r sum(w dy s) / H)
+    const float r = 1.0f / sqrtf(p.x * inv_h + a.eps);
+    // n mean(w dy n) = s m, m = r^2 sum(w dy s) / H
+    const float m = p.y * inv_h * r * r;
+    const pair_t r2 = make_pair(r, r), m2 = make_pair(-m, -m);
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
-      const int c = t + v * a.group;
-      const bool in = row < a.T && c < nch;
-      float s[8], d[8], w[8], e[8], o[8];
-      to_float(cs[v], s);
-      to_float(cd[v], d);
-      weight(v, w);
-      if (!kAhead)
-        cr[v] = in && dr != nullptr ? load_raw(dr + row * a.s_stride + c * 8) : zero_raw<T>();
-      to_float(cr[v], e);
+      const uint32_t at = ring + (uint32_t)(slot * 3 * kV + 2 * kV + v) * chunk;
+      pair_t e[4], o[4], w[4];
+      if (!kKeepProduct) to_pairs(weight(v), w);
+      to_pairs(ring_read<T>(at, v, a.group, t, a.H, threads, live && dr != nullptr), e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i] = fmaf(r, w[i] * d[i] - s[i] * mr, e[i]);
-        acc[v][i] = fmaf(d[i], s[i] * r, acc[v][i]);
+      for (int i = 0; i < 4; ++i) {
+        const pair_t x = kKeepProduct ? wd[v][i] : mul2(w[i], d[v][i]);
+        o[i] = fma2(r2, fma2(s[v][i], m2, x), e[i]);
+        acc[v][i] = fma2(d[v][i], mul2(s[v][i], r2), acc[v][i]);
       }
-      if (in) store8(static_cast<T *>(a.dx) + row * a.dx_stride + c * 8, o);
+      if (live) store_chunk(static_cast<T *>(a.dx) + row * a.dx_stride, o, v, a.group, t, a.H);
     }
+    slot = slot + 1 == a.depth ? 0 : slot + 1;
+    next = next + 1 == a.depth ? 0 : next + 1;
   }
   if (a.part == nullptr) return;
+  // this thread's columns in the order of T's pieces, as fp32
+  auto leave = [&](float *to) {
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        constexpr int kPairs = 4 / Chunk<T>::kPieces;
+        const int c = column<T>(v, i / kPairs, a.group, t) + i % kPairs * 2;
+        if (c < a.H) *reinterpret_cast<float2 *>(to + c) = make_float2(lo_of(acc[v][i]), hi_of(acc[v][i]));
+      }
+  };
   float *out = a.part + (int64_t)blockIdx.x * a.H;
-  if (a.rows > 1) {
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int c = t + v * a.group;
-      if (c < nch) store8(s_dw + (int64_t)sub * a.H + c * 8, acc[v]);
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
-      float w = 0.f;
-      for (int g = 0; g < a.rows; ++g) w += s_dw[(int64_t)g * a.H + c];
-      out[c] = w;
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const int c = t + v * a.group;
-      if (c < nch) store8(out + c * 8, acc[v]);
-    }
+  if (a.rows == 1) return leave(out);
+  float *s_dw = reinterpret_cast<float *>(s_ring);  // [rows][H]
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();  // no thread's ring is in use
+  leave(s_dw + (int64_t)sub * a.H);
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+    float w = 0.f;
+    for (int g = 0; g < a.rows; ++g) w += s_dw[(int64_t)g * a.H + c];
+    out[c] = w;
   }
 }
 
 // Column sums of `part` [n][ld] over its n rows, in a fixed order: 32 columns
-// a CTA, 8 rows at a time.
-__global__ void __launch_bounds__(256)
+// a CTA, 32 rows at a time (of which four in flight a thread).
+__global__ void __launch_bounds__(1024)
     column_sum_kernel(const float *part, int n, int cols, int64_t ld, float *out, int accumulate) {
-  __shared__ float s[8][33];
+  __shared__ float s[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   pdl_wait();
   pdl_launch_dependents();
   float v = 0.f;
-  if (c < cols)
-    for (int r = ry; r < n; r += 8) v += part[(int64_t)r * ld + c];
+  if (c < cols) {
+    int r = ry;
+    for (; r + 96 < n; r += 128) {
+      const float *p = part + (int64_t)r * ld + c;
+      const float a0 = p[0], a1 = p[32 * ld], a2 = p[64 * ld], a3 = p[96 * ld];
+      v += a0;
+      v += a1;
+      v += a2;
+      v += a3;
+    }
+    for (; r < n; r += 32) v += part[(int64_t)r * ld + c];
+  }
   s[ry][cx] = v;
   __syncthreads();
-  if (ry == 0 && c < cols) {
-    for (int i = 1; i < 8; ++i) v += s[i][cx];
-    out[c] = accumulate ? out[c] + v : v;
-  }
+  // warp w: column w of the CTA, lane l its row lane l
+  v = warp_sum(s[cx][ry]);
+  const int col = blockIdx.x * 32 + ry;
+  if (cx == 0 && col < cols) out[col] = accumulate ? out[col] + v : v;
 }
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
+// Opts a kernel in to `bytes` of dynamic shared memory; `allowed`: the kernel's
+// own record of what it has, per device.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, size_t (&allowed)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (bytes <= allowed[dev]) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) allowed[dev] = bytes;
+  return e;
+}
+
+// Rows of a ring: up to four where `per_sm` CTAs of an SM have room for at least
+// two, else two of a CTA that has the SM to itself, or one.
+int ring_depth(size_t row_bytes, int per_sm) {
+  const int d = (int)((size_t)(200 / per_sm * 1024) / row_bytes);
+  return d >= 2 ? std::min(d, 4) : (2 * row_bytes <= 200 * 1024 ? 2 : 1);
+}
+
+template <typename T, int kV>
+cudaError_t launch_norm_rows(const NormArgs &a, dim3 grid, dim3 block, size_t smem, cudaStream_t s) {
+  static size_t allowed[64] = {};
+  const cudaError_t e = allow_smem(add_rms_norm_rows_kernel<T, kV>, smem, allowed);
+  return e != cudaSuccess
+             ? e
+             : launch_pdl(add_rms_norm_rows_kernel<T, kV>, grid, block, smem, s, a);
+}
+
 template <typename T>
 cudaError_t norm_forward(NormArgs a, cudaStream_t s) {
   const int nch = a.H / 8;
-  // Few rows: latency counts, one chunk a thread where 1024 threads hold the
-  // row.  Many rows: four chunks a thread keep more loads in flight for each
-  // barrier.
-  const bool few = a.T <= 2 * num_sms();
-  int v = few ? (nch <= kNormMaxThreads ? 1 : 2) : 4;
-  if (nch <= 32) v = 1;
-  a.group = round_up((nch + v - 1) / v, 32);
-  a.rows = few ? 1 : std::max(1, 256 / a.group);
-  const dim3 grid((unsigned)((a.T + a.rows - 1) / a.rows)), block((unsigned)(a.group * a.rows));
-  switch (v) {
-    case 1: return launch_pdl(add_rms_norm_kernel<T, 1>, grid, block, 0, s, a);
-    case 2: return launch_pdl(add_rms_norm_kernel<T, 2>, grid, block, 0, s, a);
-    default: return launch_pdl(add_rms_norm_kernel<T, 4>, grid, block, 0, s, a);
+  if (a.T <= 2 * num_sms()) {
+    // latency counts: one chunk a thread where 1024 threads hold the row
+    const int v = nch <= kNormMaxThreads ? 1 : 2;
+    a.rows = 1;
+    a.group = round_up((nch + v - 1) / v, 32);
+    const dim3 grid((unsigned)a.T), block((unsigned)a.group);
+    return v == 1 ? launch_pdl(add_rms_norm_kernel<T, 1>, grid, block, 0, s, a)
+                  : launch_pdl(add_rms_norm_kernel<T, 2>, grid, block, 0, s, a);
   }
+  // Four chunks a thread and three CTAs an SM; two where codes are made, which
+  // wants the registers (8192 x 7168: 73 us of three, 82 of two; to E4M3 66 of
+  // two, 81 of three).
+  a.group = round_up((nch + 3) / 4, 32);
+  a.rows = std::max(1, 256 / a.group);
+  const int per_sm = a.q != nullptr ? 2 : 3;
+  const size_t row_bytes = (size_t)8 * a.group * a.rows * 8 * sizeof(T);
+  a.depth = ring_depth(row_bytes, per_sm);
+  const size_t smem = (size_t)a.depth * row_bytes;
+  const int fit = (int)std::min<size_t>(per_sm, std::max<size_t>(1, 210 * 1024 / smem));
+  const int ctas = std::min((a.T + a.rows - 1) / a.rows, fit * num_sms());
+  return launch_norm_rows<T, 4>(a, dim3((unsigned)ctas), dim3((unsigned)(a.group * a.rows)), smem, s);
 }
 
-// Threads to a row, rows to a CTA and CTAs of the backward pass.
-void norm_bwd_shape(int T, int H, int sms, int *v, int *group, int *rows, int *ctas) {
+// Threads to a row, rows to a CTA and CTAs of the backward pass: two an SM while
+// their registers fit (8192 x 4096: 49 us of two, 69 of one; 8192 x 7168, whose
+// 448 threads do not fit twice: 86 of two, 80 of one).
+void norm_bwd_shape(int T, int H, int sms, int *v, int *group, int *rows, int *per_sm, int *ctas) {
   const int nch = H / 8;
-  *v = nch <= 2 * kNormBwdThreads ? 2 : 4;
+  *v = nch <= 2 * kNormRowThreads ? 2 : 4;
   *group = round_up((nch + *v - 1) / *v, 32);
   *rows = std::max(1, 256 / *group);
-  // the joined column sums of the CTA's groups go through shared memory
-  while (*rows > 1 && (size_t)*rows * H * 4 > 48 * 1024) *rows /= 2;
-  *ctas = std::min((T + *rows - 1) / *rows, 2 * sms);
+  *per_sm = *group * *rows <= 256 ? 2 : 1;
+  *ctas = std::min((T + *rows - 1) / *rows, *per_sm * sms);
+}
+
+template <typename T, int kV>
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t s) {
+  static size_t allowed[64] = {};
+  const cudaError_t e = allow_smem(add_rms_norm_bwd_kernel<T, kV>, smem, allowed);
+  return e != cudaSuccess
+             ? e
+             : launch_pdl(add_rms_norm_bwd_kernel<T, kV>, grid, block, smem, s, a);
 }
 
 template <typename T>
 cudaError_t norm_backward(NormBwdArgs a, float *dweight, cudaStream_t s) {
-  int v, ctas;
-  norm_bwd_shape(a.T, a.H, num_sms(), &v, &a.group, &a.rows, &ctas);
-  const size_t smem = a.rows > 1 ? (size_t)a.rows * a.H * 4 : 0;
+  int v, per_sm, ctas;
+  norm_bwd_shape(a.T, a.H, num_sms(), &v, &a.group, &a.rows, &per_sm, &ctas);
+  const size_t row_bytes = (size_t)3 * v * a.group * a.rows * 8 * sizeof(T);
+  a.depth = ring_depth(row_bytes, per_sm);
+  const size_t smem = std::max((size_t)a.depth * row_bytes,
+                               a.rows > 1 ? (size_t)a.rows * a.H * 4 : 0);
   const dim3 grid((unsigned)ctas), block((unsigned)(a.group * a.rows));
-  cudaError_t e = v == 2 ? launch_pdl(add_rms_norm_bwd_kernel<T, 2>, grid, block, smem, s, a)
-                         : launch_pdl(add_rms_norm_bwd_kernel<T, 4>, grid, block, smem, s, a);
+  cudaError_t e = v == 2 ? launch_norm_bwd<T, 2>(a, grid, block, smem, s)
+                         : launch_norm_bwd<T, 4>(a, grid, block, smem, s);
   if (e == cudaSuccess && dweight != nullptr)
     e = launch_column_sum(a.part, ctas, a.H, a.H, dweight, 0, s);
   return e;
@@ -429,13 +643,13 @@ cudaError_t norm_backward(NormBwdArgs a, float *dweight, cudaStream_t s) {
 
 cudaError_t launch_column_sum(const float *part, int n, int cols, int64_t ld, float *out,
                               int accumulate, cudaStream_t s) {
-  return launch_pdl(column_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, s, part, n,
+  return launch_pdl(column_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, s, part, n,
                     cols, ld, out, accumulate);
 }
 
 size_t norm_bwd_part_bytes(const moe_norm_desc_t &d) {
-  int v, group, rows, ctas;
-  norm_bwd_shape(d.T, d.H, kRouteSizingSms, &v, &group, &rows, &ctas);
+  int v, group, rows, per_sm, ctas;
+  norm_bwd_shape(d.T, d.H, kRouteSizingSms, &v, &group, &rows, &per_sm, &ctas);
   return (size_t)ctas * d.H * 4;
 }
 
@@ -443,7 +657,7 @@ cudaError_t launch_add_rms_norm(const moe_norm_desc_t &d, const void *x, const v
                                 const void *weight, void *residual_out, void *y, uint8_t *q,
                                 int8_t *scale, cudaStream_t s) {
   NormArgs a = {x, residual, weight, residual_out, y, q, scale, d.x_stride, d.residual_stride,
-                d.y_stride, d.T, d.H, 0, 0, d.eps};
+                d.y_stride, d.T, d.H, 0, 0, 0, d.eps};
   switch (d.dtype) {
     case MOE_DTYPE_BF16: return norm_forward<__nv_bfloat16>(a, s);
     case MOE_DTYPE_FP16: return norm_forward<__half>(a, s);
@@ -455,7 +669,7 @@ cudaError_t launch_add_rms_norm_backward(const moe_norm_desc_t &d, const void *d
                                          const void *sum, const void *weight, void *dx,
                                          float *dweight, float *part, cudaStream_t s) {
   NormBwdArgs a = {dy, dres, sum, weight, dx, dweight != nullptr ? part : nullptr, d.y_stride,
-                   d.residual_stride, d.x_stride, d.T, d.H, 0, 0, d.eps};
+                   d.residual_stride, d.x_stride, d.T, d.H, 0, 0, 0, d.eps};
   switch (d.dtype) {
     case MOE_DTYPE_BF16: return norm_backward<__nv_bfloat16>(a, dweight, s);
     case MOE_DTYPE_FP16: return norm_backward<__half>(a, dweight, s);

@@ -272,10 +272,10 @@ moe_status_t moe_linear_backward(const moe_linear_desc_t *in, const void *dy, co
   cudaError_t e = cudaSuccess;
   if (d.T > 0 && (dbias != nullptr || (act && (dx != nullptr || dw != nullptr))))
     e = launch_act_grad(dy, d.y_stride, preact, d.T, d.N, d.act, d.dtype,
-                        act ? at(workspace, L.dz) : nullptr, dbias != nullptr ? part : nullptr, s);
-  if (e == cudaSuccess && dbias != nullptr)
-    e = launch_column_sum(part, d.T > 0 ? act_grad_slices(d.T, d.N) : 0, d.N, d.N, dbias,
-                          accumulate, s);
+                        dx != nullptr || dw != nullptr ? at(workspace, L.dz) : nullptr, part,
+                        static_cast<uint32_t *>(workspace) + kBiasCounterWord, dbias, accumulate, s);
+  else if (dbias != nullptr && !accumulate)
+    e = cudaMemsetAsync(dbias, 0, (size_t)d.N * 4, s);
   if (e == cudaSuccess && dx != nullptr && d.T > 0)
     e = launch_dense_pair(product(d.T, d.K, d.N, d.dtype, dz, ldz, false, w, d.K, true, dx,
                                   d.x_stride, d.dtype, workspace),

@@ -47,11 +47,13 @@ cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s);
 float dense_pair_us(const DenseGemm &g);
 float dense_small_us(const DenseGemm &g);
 
-// dz = dy act'(z) in 16 bits (dz null: not written; z null: dz = dy) and the
-// column sums of each slice of the rows (part [slices][N], or null).
+// dz = dy act'(z) in 16 bits (act none: not written) and the column sums of the
+// unrounded dz to dbias (null: none), by way of part [slices][N] and one zero
+// counter for each 128 columns.
 int act_grad_slices(int T, int N);
 cudaError_t launch_act_grad(const void *dy, int64_t ldy, const float *z, int T, int N, int act,
-                            int dtype, void *dz, float *part, cudaStream_t s);
+                            int dtype, void *dz, float *part, uint32_t *counter, float *dbias,
+                            int accumulate, cudaStream_t s);
 
 // ------------------------------------------------------------ element types --
 

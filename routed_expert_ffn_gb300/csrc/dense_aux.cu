@@ -1,10 +1,15 @@
-// The row-wise passes of the dense operators' gradients.
+#ifndef AG_CTAS
+#define AG_CTAS 608
+#endif
+// The row-wise pass of the dense operators' gradients.
 //
 // act_grad: dz = dy act'(z), rounded once to the 16-bit type the gradient
 // products take, with the column sums of the unrounded dz for the bias.
-// Bound: HBM (dy and z read, dz written).  A CTA takes 256 columns (a thread
-// 8 of them) and one slice of the rows; the slices' column sums are partials
-// that column_sum adds in a fixed order.
+// Bound: HBM (dy and z read, dz written).  A CTA takes 128 columns (a lane 4
+// of them: 16 bytes of z, 8 of dy) and one slice of the rows, four rows a
+// thread in flight.  A slice's column sums go to the workspace; the last CTA
+// of the columns adds the slices in order, so the sums do not change from run
+// to run (a kernel of its own for that cost 4 us of a gradient of 110).
 #include <algorithm>
 
 #include "dense.cuh"
@@ -13,74 +18,136 @@ namespace moe {
 
 namespace {
 
-constexpr int kCols = 256, kRowLanes = 8;  // 32 threads x 8 columns, 8 rows at a time
+constexpr int kCols = 128, kRowLanes = 8, kAhead = 4;
 
-__global__ void __launch_bounds__(256)
-    act_grad_kernel(const uint16_t *__restrict__ dy, int64_t ldy, const float *__restrict__ z,
-                    int T, int N, int rows, int act, int dtype, uint16_t *__restrict__ dz,
-                    float *__restrict__ part) {
-  __shared__ float s[kRowLanes][kCols];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int c = blockIdx.x * kCols + tx * 8;
-  const int r0 = blockIdx.y * rows, r1 = min(T, r0 + rows);
-  pdl_wait();
-  pdl_launch_dependents();
-  float sum[8] = {};
-  if (c < N) {
-#pragma unroll 2
-    for (int r = r0 + ty; r < r1; r += kRowLanes) {
-      const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(dy + (int64_t)r * ldy + c));
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-      float d[8];
+struct ActGradArgs {
+  const uint16_t *dy;
+  const float *z;
+  uint16_t *dz;
+  float *part, *dbias;
+  uint32_t *counter;  // one for each 128 columns, zero before and after
+  int64_t ldy;
+  int T, N, rows, act, dtype, accumulate;
+};
+
+template <int kAct>
+__device__ __forceinline__ void act_grad_rows(const ActGradArgs &a, int c, int r0, int r1,
+                                              float (&sum)[4]) {
+  for (int r = r0; r < r1; r += kRowLanes * kAhead) {
+    uint2 dy[kAhead];
+    float4 z[kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack16(dtype, w[i]);
-        d[2 * i] = v.x;
-        d[2 * i + 1] = v.y;
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = r + i * kRowLanes;
+      if (row < r1) {
+        dy[i] = __ldg(reinterpret_cast<const uint2 *>(a.dy + (int64_t)row * a.ldy + c));
+        if (kAct != MOE_ACT_NONE)
+          z[i] = __ldg(reinterpret_cast<const float4 *>(a.z + (int64_t)row * a.N + c));
       }
-      if (z != nullptr) {
-        const float4 *p = reinterpret_cast<const float4 *>(z + (int64_t)r * N + c);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        const float zz[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= activate_slope(act, zz[i]);
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = r + i * kRowLanes;
+      if (row >= r1) break;
+      const float2 lo = unpack16(a.dtype, dy[i].x), hi = unpack16(a.dtype, dy[i].y);
+      float d[4] = {lo.x, lo.y, hi.x, hi.y};
+      if (kAct != MOE_ACT_NONE) {
+        const float zz[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] *= activate_slope(kAct, zz[j]);
+        if (a.dz != nullptr)
+          *reinterpret_cast<uint2 *>(a.dz + (int64_t)row * a.N + c) =
+              make_uint2(pack16(a.dtype, d[0], d[1]), pack16(a.dtype, d[2], d[3]));
       }
-      if (dz != nullptr)
-        *reinterpret_cast<uint4 *>(dz + (int64_t)r * N + c) =
-            make_uint4(pack16(dtype, d[0], d[1]), pack16(dtype, d[2], d[3]),
-                       pack16(dtype, d[4], d[5]), pack16(dtype, d[6], d[7]));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += d[i];
+      for (int j = 0; j < 4; ++j) sum[j] += d[j];
     }
   }
-  if (part == nullptr) return;
+}
+
+__global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a) {
+  __shared__ float s[kRowLanes][kCols];
+  __shared__ bool last;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * kCols, c = c0 + tx * 4;
+  const int first = blockIdx.y * a.rows, r0 = first + ty, r1 = min(a.T, first + a.rows);
+  pdl_wait();
+  pdl_launch_dependents();
+  float sum[4] = {};
+  if (c < a.N) {
+    switch (a.act) {
+      case MOE_ACT_RELU: act_grad_rows<MOE_ACT_RELU>(a, c, r0, r1, sum); break;
+      case MOE_ACT_GELU: act_grad_rows<MOE_ACT_GELU>(a, c, r0, r1, sum); break;
+      case MOE_ACT_GELU_TANH: act_grad_rows<MOE_ACT_GELU_TANH>(a, c, r0, r1, sum); break;
+      case MOE_ACT_SILU: act_grad_rows<MOE_ACT_SILU>(a, c, r0, r1, sum); break;
+      default: act_grad_rows<MOE_ACT_NONE>(a, c, r0, r1, sum); break;
+    }
+  }
+  if (a.dbias == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[ty][tx * 8 + i] = sum[i];
+  for (int i = 0; i < 4; ++i) s[ty][tx * 4 + i] = sum[i];
   __syncthreads();
-  const int col = blockIdx.x * kCols + threadIdx.x;
-  if (col < N) {
+  const int j = threadIdx.x & (kCols - 1), col = c0 + j;
+  if (threadIdx.x < kCols && col < a.N) {
     float v = 0.f;
-    for (int i = 0; i < kRowLanes; ++i) v += s[i][threadIdx.x];
-    part[(int64_t)blockIdx.y * N + col] = v;
+    for (int i = 0; i < kRowLanes; ++i) v += s[i][j];
+    a.part[(int64_t)blockIdx.y * a.N + col] = v;
+    __threadfence();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(a.counter + blockIdx.x, 1u) == gridDim.y - 1;
+    if (last) a.counter[blockIdx.x] = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
+  // two threads a column, half of the slices each
+  const int half = threadIdx.x / kCols, mid = gridDim.y / 2;
+  float v = 0.f;
+  if (col < a.N) {
+    const int from = half == 0 ? 0 : mid, to = half == 0 ? mid : (int)gridDim.y;
+#pragma unroll 4
+    for (int i = from; i < to; ++i) v += __ldcg(a.part + (int64_t)i * a.N + col);
+  }
+  __syncthreads();
+  if (half == 1) s[0][j] = v;
+  __syncthreads();
+  if (half == 0 && col < a.N) {
+    v += s[0][j];
+    a.dbias[col] = a.accumulate ? a.dbias[col] + v : v;
   }
 }
 
 }  // namespace
 
 // Slices of the rows: about four CTAs for each of 152 SMs, each with at least
-// 16 rows.
+// 32 rows.
 int act_grad_slices(int T, int N) {
   const int cols = (N + kCols - 1) / kCols;
-  return std::max(1, std::min((608 + cols - 1) / cols, (T + 15) / 16));
+  return std::max(1, std::min((AG_CTAS + cols - 1) / cols, (T + 31) / 32));
 }
 
 cudaError_t launch_act_grad(const void *dy, int64_t ldy, const float *z, int T, int N, int act,
-                            int dtype, void *dz, float *part, cudaStream_t s) {
+                            int dtype, void *dz, float *part, uint32_t *counter, float *dbias,
+                            int accumulate, cudaStream_t s) {
   const int slices = act_grad_slices(T, N);
-  const int rows = (T + slices - 1) / slices;
+  ActGradArgs a = {};
+  a.dy = static_cast<const uint16_t *>(dy);
+  a.z = z;
+  a.dz = static_cast<uint16_t *>(dz);
+  a.part = part;
+  a.dbias = dbias;
+  a.counter = counter;
+  a.ldy = ldy;
+  a.T = T;
+  a.N = N;
+  a.rows = (T + slices - 1) / slices;
+  a.act = act;
+  a.dtype = dtype;
+  a.accumulate = accumulate;
   return launch_pdl(act_grad_kernel, dim3((unsigned)((N + kCols - 1) / kCols), (unsigned)slices),
-                    dim3(256), 0, s, static_cast<const uint16_t *>(dy), ldy, z, T, N, rows, act,
-                    dtype, static_cast<uint16_t *>(dz), part);
+                    dim3(256), 0, s, a);
 }
 
 }  // namespace moe

@@ -45,15 +45,22 @@ constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kSfWarp = kEpiWarps + 2;           // E4M3
 // E4M3 leaves the last 64 TMEM columns to scale factors, four slots of four
 // stages each: accumulators of 224 columns.
-template <bool kE4m3>
+// The gradient of the gated product stores three tiles and turns two for each
+// 32 columns: it has three output slots and a place to turn, and a stage less.
+template <int kEpi, bool kE4m3>
 struct Shape {
+  static constexpr bool grad = kEpi == kEpiGatedGrad;
   static constexpr int threads = (kEpiWarps + 2 + (kE4m3 ? 1 : 0)) * 32;
-  static constexpr int stages = kE4m3 ? 5 : 6;
+  static constexpr int stages = kE4m3 || grad ? 5 : 6;
   static constexpr int acc = kE4m3 ? 224 : 256;  // columns of an accumulator
   static constexpr int kb = kE4m3 ? 128 : 64;    // K elements of a stage (128 bytes)
   static constexpr uint32_t sf_col = 2 * acc;
+  static constexpr uint32_t out_bytes = grad ? 8192 : 4096;  // of an epilogue warp
+  static constexpr int slots = grad ? 3 : 2;                 // of 32 x 32 16-bit values
 };
-static_assert(Shape<true>::sf_col + 4 * kSfCols <= 512, "TMEM columns");
+typedef Shape<kEpiLinear, false> Shape16;
+typedef Shape<kEpiLinear, true> Shape8;
+static_assert(Shape8::sf_col + 4 * kSfCols <= 512, "TMEM columns");
 constexpr int kMaxStages = 6;
 constexpr int kSfGroup = 8;                       // stages to a hand-over of scale factors
 constexpr int kSfBufs = 3;
@@ -67,17 +74,21 @@ constexpr uint32_t kStageBytes = kABytes + kBBytes;
 // other pair's arrive (both in the ring's place), 16 KB for 32 columns.
 constexpr uint32_t kChunkBytes = kBM * 32 * 4;
 constexpr uint32_t kRecvOff = 4 * kChunkBytes;
-constexpr uint32_t kSlotBytes = 4096;            // an epilogue warp's: 32 x 32 fp32, or two of 16 bits
+constexpr uint32_t kSlotBytes = 2048;            // 32 x 32 16-bit values
+constexpr uint32_t kTileBytes = 4096;            // 32 x 32 fp32
 constexpr uint32_t kTmemCols = 512;
-template <bool kE4m3>
+template <int kEpi, bool kE4m3>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)Shape<kE4m3>::stages * kStageBytes + kEpiWarps * kSlotBytes +
+  typedef Shape<kEpi, kE4m3> S;
+  return 1024 + (size_t)S::stages * kStageBytes + kEpiWarps * S::out_bytes +
          (2 * kMaxStages + 6 + 2 * kSfBufs) * 8 + 16 +
          (kE4m3 ? 128 + kSfBufs * 2 * kSfBlock : 0);
 }
-static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448,
+static_assert(smem_bytes<kEpiLinear, false>() <= 232448 &&
+                  smem_bytes<kEpiLinear, true>() <= 232448 &&
+                  smem_bytes<kEpiGatedGrad, false>() <= 232448,
               "shared memory per CTA");
-static_assert(2 * kRecvOff <= Shape<true>::stages * kStageBytes, "exchange buffers");
+static_assert(2 * kRecvOff <= Shape8::stages * kStageBytes, "exchange buffers");
 // Row tiles of a raster group: tiles that run together share the A rows of 8
 // row tiles and the B rows of ~10 column tiles, ~20 MB at K = 4096: in L2.
 constexpr int kGroupM = 8;
@@ -199,10 +210,12 @@ __device__ __forceinline__ Tile tile_at(int tile, const PairArgs &a) {
   return t;
 }
 
-// A warp's output buffer: two slots of 32 x 32 16-bit values, or one of fp32.
+// A warp's output buffer: kCount slots of 32 x 32 16-bit values, of which two
+// hold one of fp32.
+template <int kCount>
 struct Slots {
   uint8_t *base;
-  uint32_t n;
+  uint32_t next;
   bool wide;  // the last store was fp32
   // Each waits for the stores that still read what it hands out.
   __device__ __forceinline__ uint8_t *take16(int lane) {
@@ -210,11 +223,13 @@ struct Slots {
       if (wide)
         bulk_wait_read<0>();
       else
-        bulk_wait_read<1>();
+        bulk_wait_read<kCount - 1>();
     }
     wide = false;
     __syncwarp();
-    return base + (n++ & 1u) * (kSlotBytes / 2);
+    uint8_t *p = base + next * kSlotBytes;
+    next = next + 1 == kCount ? 0 : next + 1;
+    return p;
   }
   __device__ __forceinline__ uint8_t *take32(int lane) {
     if (lane == 0) bulk_wait_read<0>();
@@ -237,6 +252,12 @@ __device__ __forceinline__ void put16(uint8_t *slot, int lane, int dtype, const 
     *reinterpret_cast<uint4 *>(slot + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
   }
 }
+__device__ __forceinline__ void put16(uint8_t *slot, int lane, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4 *>(slot + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+}
 __device__ __forceinline__ void put32(uint8_t *slot, int lane, const float (&f)[32]) {
 #pragma unroll
   for (int c = 0; c < 8; ++c)
@@ -248,6 +269,18 @@ __device__ __forceinline__ void add32(float (&f)[32], const uint8_t *slot, int l
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const float4 v = *reinterpret_cast<const float4 *>(slot + lane * 128 + ((c ^ (lane & 7)) << 4));
+    f[4 * c] += v.x;
+    f[4 * c + 1] += v.y;
+    f[4 * c + 2] += v.z;
+    f[4 * c + 3] += v.w;
+  }
+}
+// 16 of the values, the first or the second half.
+__device__ __forceinline__ void add16(float (&f)[16], const uint8_t *slot, int half, int lane) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float4 v = *reinterpret_cast<const float4 *>(slot + lane * 128 +
+                                                       (((4 * half + c) ^ (lane & 7)) << 4));
     f[4 * c] += v.x;
     f[4 * c + 1] += v.y;
     f[4 * c + 2] += v.z;
@@ -312,30 +345,50 @@ struct Values32 {
   }
 };
 
-// 32 consecutive fp32 values; those past `left` are zero.
-__device__ __forceinline__ void read32(float (&f)[32], const float *p, int left) {
+// 32 rows of 16 fp32 values, loaded four lanes to a row (whole sectors; a lane to
+// a row fetched them twice) and turned by way of shared memory so that lane r has
+// row r.  Rows and columns past the ends are zero.
+struct Tile16 {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float *p, int64_t ld, int rows, int cols, int lane) {
+    const int r = lane >> 2, c = (lane & 3) * 4;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const float4 v = 4 * c < left ? __ldg(reinterpret_cast<const float4 *>(p) + c)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-    f[4 * c] = v.x;
-    f[4 * c + 1] = v.y;
-    f[4 * c + 2] = v.z;
-    f[4 * c + 3] = v.w;
+    for (int i = 0; i < 4; ++i)
+      v[i] = 8 * i + r < rows && c < cols
+                 ? __ldg(reinterpret_cast<const float4 *>(p + (int64_t)(8 * i + r) * ld + c))
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-}
+  __device__ __forceinline__ void turn(uint8_t *to, int lane, float (&f)[16]) const {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4 *>(to + (8 * i + r) * 64 + ((c ^ ((r >> 1) & 3)) << 4)) = v[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 o =
+          *reinterpret_cast<const float4 *>(to + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+      f[4 * i] = o.x;
+      f[4 * i + 1] = o.y;
+      f[4 * i + 2] = o.z;
+      f[4 * i + 3] = o.w;
+    }
+    __syncwarp();
+  }
+};
 
 template <int kEpi, bool kAMn, bool kBMn, bool kE4m3>
-__global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
+__global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
     dense_pair_kernel(const __grid_constant__ PairMaps maps, const PairArgs a) {
-  constexpr int kStages = Shape<kE4m3>::stages, kKb = Shape<kE4m3>::kb;
-  constexpr uint32_t kAcc = Shape<kE4m3>::acc;
+  typedef Shape<kEpi, kE4m3> S;
+  constexpr int kStages = S::stages, kKb = S::kb;
+  constexpr uint32_t kAcc = S::acc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *ring = smem;
   uint8_t *slots = ring + kStages * kStageBytes;
-  uint64_t *full = reinterpret_cast<uint64_t *>(slots + kEpiWarps * kSlotBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(slots + kEpiWarps * S::out_bytes);
   uint64_t *empty = full + kMaxStages;
   uint64_t *tfull = empty + kMaxStages;
   uint64_t *tempty = tfull + 2;
@@ -473,8 +526,33 @@ __global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
       const uint32_t b0 = smem_u32(ring + kABytes) >> 4 | (kBMn ? kDescLoMn : kDescLoK);
       uint32_t off = 0;
       uint32_t st = 0, ph = 0, tl = 0;
-      uint32_t sg = 0, sph = 0, sslot = 0;  // E4M3: hand-over buffer, TMEM slot
-      bool ok = true;
+      // E4M3: scale factors go to TMEM in blocks of four stages, each block
+      // while the products of the one before it run
+      const int per_tile = (k_end - k_first + 3) / 4;
+      int blocks = cid < total ? (total - cid + ncl - 1) / ncl * per_tile : 0, in_tile = 0;
+      uint32_t sg = 0, sph = 0, filled = 0, used = 0;  // hand-over buffer; TMEM slots
+      auto copy_block = [&]() -> bool {
+        if (blocks == 0) return true;
+        const uint32_t part = (uint32_t)in_tile % (kSfGroup / 4);
+        if (part == 0 && !mbar_wait(&sf_full[sg], sph, abort_flag, a.status, kStatusTimeoutDense))
+          return false;
+        tc_fence_after();
+        const uint32_t to = tmem_base + Shape8::sf_col + (filled++ & 3u) * kSfCols;
+        const uint64_t sd = sdesc_sf(smem_u32(sf_blocks + (sg * 2 + part) * kSfBlock));
+#pragma unroll
+        for (uint32_t i = 0; i < 3; ++i) sf_copy_pair(to + 4 * i, sd + i * (512 >> 4));
+        --blocks;
+        if (++in_tile == per_tile) in_tile = 0;
+        if (part == kSfGroup / 4 - 1 || in_tile == 0) {
+          umma_commit_pair(&sf_empty[sg], pair_mask);
+          if (++sg == kSfBufs) {
+            sg = 0;
+            sph ^= 1u;
+          }
+        }
+        return true;
+      };
+      bool ok = !kE4m3 || copy_block();
       for (int tile = cid; ok && tile < total; tile += ncl, ++tl) {
         const uint32_t buf = tl & 1u, use = tl >> 1;
         if (!mbar_wait(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) break;
@@ -488,22 +566,11 @@ __global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
           }
           uint32_t sf = 0, id = idesc;
           if (kE4m3) {
-            if (ki % kSfGroup == 0 &&
-                !mbar_wait(&sf_full[sg], sph, abort_flag, a.status, kStatusTimeoutDense)) {
-              ok = false;
-              break;
-            }
-            if (ki % 4 == 0) ++sslot;
-            sf = tmem_base + Shape<true>::sf_col + (sslot & 3u) * kSfCols;
+            if (ki % 4 == 0) ++used;
+            sf = tmem_base + Shape8::sf_col + ((used - 1) & 3u) * kSfCols;
             id |= idesc_sf_byte((uint32_t)ki & 3u);
           }
           tc_fence_after();
-          if (kE4m3 && ki % 4 == 0) {
-            const uint64_t sd =
-                sdesc_sf(smem_u32(sf_blocks + (sg * 2 + (uint32_t)(ki >> 2 & 1)) * kSfBlock));
-#pragma unroll
-            for (uint32_t i = 0; i < 3; ++i) sf_copy_pair(sf + 4 * i, sd + i * (512 >> 4));
-          }
           const uint32_t ad = a0 + off, bd = b0 + off;
 #pragma unroll
           for (uint32_t q = 0; q < 4; ++q) {
@@ -515,12 +582,9 @@ __global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
             }
           }
           umma_commit_pair(&empty[st], pair_mask);
-          if (kE4m3 && (ki % kSfGroup == kSfGroup - 1 || kb == k_end - 1)) {
-            umma_commit_pair(&sf_empty[sg], pair_mask);
-            if (++sg == kSfBufs) {
-              sg = 0;
-              sph ^= 1u;
-            }
+          if (kE4m3 && ki % 4 == 0 && !copy_block()) {
+            ok = false;
+            break;
           }
           off += kStageBytes >> 4;
           if (++st == (uint32_t)kStages) {
@@ -545,61 +609,76 @@ __global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
     // block of W).  The MMA thread copies the blocks to TMEM in the order of its
     // products.  One hand-over for eight stages: it takes a release at cluster
     // scope, which measured 0.85 us (a stage takes 0.25).
+    // Loads run one hand-over ahead.
     const int last = (a.N - 1) >> 7;
-    uint32_t g = 0, ph = 0;
-    bool ok = true;
-    for (int tile = cid; ok && tile < total; tile += ncl) {
+    uint32_t nx[2][4], nw[2];
+    auto load = [&](int tile, int kb) {
       const Tile t = tile_at(tile, a);
-      for (int kb = k_first; kb < k_end; kb += kSfGroup) {
-        uint32_t x[2][4], w[2][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = min(t.m0 + (int)rank * kBM + 32 * j + lane, a.M - 1);
-          const int8_t *e = a.a_scale + (int64_t)r * nkb + kb;
-          x[0][j] = e8m0_4(e, nkb - kb);
-          x[1][j] = e8m0_4(e + 4, nkb - kb - 4);
-        }
-        {
-          // lane j: the words of 32 columns
-          const int blk = min((t.j * a.cols + 32 * (lane & 7)) >> 7, last);
-          const int8_t *e = a.b_scale + (int64_t)blk * nkb + kb;
-          const uint32_t w0 = e8m0_4(e, nkb - kb), w1 = e8m0_4(e + 4, nkb - kb - 4);
+      for (int j = 0; j < 4; ++j) {
+        const int r = min(t.m0 + (int)rank * kBM + 32 * j + lane, a.M - 1);
+        const int8_t *e = a.a_scale + (int64_t)r * nkb + kb;
+        nx[0][j] = e8m0_4(e, nkb - kb);
+        nx[1][j] = e8m0_4(e + 4, nkb - kb - 4);
+      }
+      // lane j: the words of 32 columns
+      const int blk = min((t.j * a.cols + 32 * (lane & 7)) >> 7, last);
+      const int8_t *e = a.b_scale + (int64_t)blk * nkb + kb;
+      nw[0] = e8m0_4(e, nkb - kb);
+      nw[1] = e8m0_4(e + 4, nkb - kb - 4);
+    };
+    uint32_t g = 0, ph = 0;
+    int tile = cid, kb = k_first;
+    if (tile < total) load(tile, kb);
+    while (tile < total) {
+      uint32_t x[2][4], w[2][8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            w[0][j] = __shfl_sync(0xffffffffu, w0, j);
-            w[1][j] = __shfl_sync(0xffffffffu, w1, j);
-          }
-        }
-        const bool free = mbar_wait(&sf_empty[g], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense);
-        if (!__all_sync(0xffffffffu, free)) {
-          ok = false;
-          break;
-        }
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint4 *to = reinterpret_cast<uint4 *>(sf_blocks + (g * 2 + i) * kSfBlock) + lane;
-          to[0] = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
-          to[32] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-          to[64] = make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(&sf_full[g], lead));
-        if (++g == kSfBufs) {
-          g = 0;
-          ph ^= 1u;
-        }
+        for (int j = 0; j < 4; ++j) x[i][j] = nx[i][j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[i][j] = __shfl_sync(0xffffffffu, nw[i], j);
+      }
+      kb += kSfGroup;
+      if (kb >= k_end) {
+        kb = k_first;
+        tile += ncl;
+      }
+      if (tile < total) load(tile, kb);
+      const bool free =
+          mbar_wait(&sf_empty[g], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense);
+      if (!__all_sync(0xffffffffu, free)) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint4 *to = reinterpret_cast<uint4 *>(sf_blocks + (g * 2 + i) * kSfBlock) + lane;
+        to[0] = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+        to[32] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        to[64] = make_uint4(w[i][4], w[i][5], w[i][6], w[i][7]);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&sf_full[g], lead));
+      if (++g == kSfBufs) {
+        g = 0;
+        ph ^= 1u;
       }
     }
     __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue --
     // warps w and w + 4 share 32 TMEM lanes and take every other 32 columns
-    Slots slot = {slots + warp * kSlotBytes, 0, false};
+    Slots<S::slots> slot = {slots + warp * S::out_bytes, 0, false};
+    uint8_t *turning = slot.base + S::slots * kSlotBytes;  // kEpiGatedGrad
     const int quad = warp & 3, turn = (warp >> 2) * 32;
     uint32_t tl = 0;
     Values32 bias, res;  // kEpiLinear: of the next chunk
+    Tile16 next_g, next_u;  // kEpiGatedGrad: of the next 16 columns
     auto fetch = [&](int c, int row) {
+      if (kEpi == kEpiGatedGrad) {
+        const float *sv = a.saved + (int64_t)(row - lane) * 2 * a.N + c;
+        next_g.load(sv, 2 * (int64_t)a.N, a.M - (row - lane), a.N - c, lane);
+        next_u.load(sv + a.N, 2 * (int64_t)a.N, a.M - (row - lane), a.N - c, lane);
+      }
       if (kEpi != kEpiLinear) return;
       if (a.bias != nullptr) bias.load(a.bias, c, a.N - c, a.out_dtype);
       if (a.residual != nullptr)
@@ -633,7 +712,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
         cluster_arrive();  // this CTA's ring is done
         if (ok)
           for (int c = ofirst + turn; c < oend; c += 64) {
-            uint8_t *p = ring + (uint32_t)((c - ofirst) / 32 * kPer) * kChunkBytes + quad * kSlotBytes;
+            uint8_t *p = ring + (uint32_t)((c - ofirst) / 32 * kPer) * kChunkBytes + quad * kTileBytes;
             float v[32];
             tmem_ld32(tb + (c - c0), v);
             put32(p, lane, v);
@@ -654,7 +733,7 @@ __global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
-      const uint8_t *others = ring + kRecvOff + quad * kSlotBytes;
+      const uint8_t *others = ring + kRecvOff + quad * kTileBytes;
       const int cstart = cfirst;
       cend = row0 < a.M ? min(a.N, cend) : cfirst;
       for (int c = cfirst + turn; c < cend; c += 64) {
@@ -704,29 +783,43 @@ __global__ void __launch_bounds__(Shape<kE4m3>::threads, 1)
           put16(p, lane, a.dtype, v);
           send_2d(&maps.d, p, lane, c, row0);
         } else {
-          // dh = acc;  p = sigmoid(g):  h = g p u, dg = dh u p (1 + g (1 - p)), du = dh g p
-          float g[32], u[32];
-          const float *sv = a.saved + (int64_t)row * 2 * a.N + c;
-          read32(g, sv, left);
-          read32(u, sv + a.N, left);
-          tmem_ld32(tb + (c - c0), v);
-          if (a.split == 2) add32(v, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, lane);
-          float o[32];
+          // dh = acc;  s = sigmoid(g):  h = g s u, dg = dh u s (1 + g (1 - s)), du = dh g s
+          uint32_t wh[16], wg[16], wu[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float p = sigmoid(g[i]), gp = g[i] * p;
-            o[i] = gp * u[i];
-            u[i] = v[i] * u[i] * p * (1.0f + g[i] * (1.0f - p));
-            v[i] = v[i] * gp;
+          for (int q = 0; q < 2; ++q) {
+            float g[16], u[16], dh[16];
+            next_g.turn(turning, lane, g);
+            next_u.turn(turning, lane, u);
+            if (q == 0)
+              fetch(c + 16, row);
+            else if (c + 64 < cend)
+              fetch(c + 64, row);
+            tmem_ld16f(tb + (c - c0) + 16 * q, dh);
+            if (a.split == 2)
+              add16(dh, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, q, lane);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float h[2], dg[2], du[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float s = sigmoid(g[i + k]), gs = g[i + k] * s;
+                h[k] = gs * u[i + k];
+                dg[k] = dh[i + k] * u[i + k] * s * (1.0f + g[i + k] * (1.0f - s));
+                du[k] = dh[i + k] * gs;
+              }
+              wh[8 * q + i / 2] = pack16(a.dtype, h[0], h[1]);
+              wg[8 * q + i / 2] = pack16(a.dtype, dg[0], dg[1]);
+              wu[8 * q + i / 2] = pack16(a.dtype, du[0], du[1]);
+            }
           }
           uint8_t *p = slot.take16(lane);
-          put16(p, lane, a.dtype, o);
+          put16(p, lane, wh);
           send_2d(&maps.d, p, lane, c, row0);
           p = slot.take16(lane);
-          put16(p, lane, a.dtype, u);
+          put16(p, lane, wg);
           send_3d(&maps.extra, p, lane, c, row0, 0);
           p = slot.take16(lane);
-          put16(p, lane, a.dtype, v);
+          put16(p, lane, wu);
           send_3d(&maps.extra, p, lane, c, row0, 1);
         }
       }
@@ -771,7 +864,7 @@ struct PairPlan {
 // 14336 at 512 rows 66.6 -> 43.2 us.
 PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
   const bool e4m3 = g.dtype == MOE_DTYPE_E4M3, gated = g.epi == kEpiGated;
-  const int kb = e4m3 ? Shape<true>::kb : Shape<false>::kb;
+  const int kb = e4m3 ? Shape8::kb : Shape16::kb;
   const int nkb = (g.K + kb - 1) / kb;
   PairPlan p = {};
   p.mt = (g.M + kTileM - 1) / kTileM;
@@ -779,7 +872,7 @@ PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
   for (int split = 1; split <= 2; ++split) {
     const int part = split == 1 ? nkb : (nkb + 15) / 16 * 8;  // E4M3: whole groups of scales
     if (split == 2 && part >= nkb) continue;
-    for (int bn = e4m3 ? Shape<true>::acc : Shape<false>::acc; bn >= 64; bn -= gated ? 64 : 32) {
+    for (int bn = e4m3 ? Shape8::acc : Shape16::acc; bn >= 64; bn -= gated ? 64 : 32) {
       const int cols = gated ? bn / 2 : bn;
       const int nt = (g.N + cols - 1) / cols;
       const int64_t tiles = (int64_t)mt * nt;
@@ -810,7 +903,7 @@ cudaError_t resident_clusters(int (&out)[2]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (resident[dev][0] == 0) {
-    constexpr size_t kBytes = smem_bytes<kE4m3>();
+    constexpr size_t kBytes = smem_bytes<kEpi, kE4m3>();
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
     if (e != cudaSuccess) return e;
@@ -822,7 +915,7 @@ cudaError_t resident_clusters(int (&out)[2]) {
       attr[0].val.clusterDim.y = 1;
       attr[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3((unsigned)(num_sms() / (2 * p) * (2 * p)));
-      cfg.blockDim = dim3(Shape<kE4m3>::threads);
+      cfg.blockDim = dim3(Shape<kEpi, kE4m3>::threads);
       cfg.dynamicSmemBytes = kBytes;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
@@ -841,7 +934,7 @@ cudaError_t resident_clusters(int (&out)[2]) {
 // `us` not null: only the estimated time.
 template <int kEpi, bool kAMn, bool kBMn, bool kE4m3 = false>
 cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
-  constexpr int kKb = Shape<kE4m3>::kb;
+  constexpr int kKb = Shape<kEpi, kE4m3>::kb;
   int resident[2];
   cudaError_t e = resident_clusters<kEpi, kAMn, kBMn, kE4m3>(resident);
   if (e != cudaSuccess) return e;
@@ -911,8 +1004,8 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(2 * a.split * plan.clusters));
-  cfg.blockDim = dim3(Shape<kE4m3>::threads);
-  cfg.dynamicSmemBytes = smem_bytes<kE4m3>();
+  cfg.blockDim = dim3(Shape<kEpi, kE4m3>::threads);
+  cfg.dynamicSmemBytes = smem_bytes<kEpi, kE4m3>();
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;

@@ -161,7 +161,11 @@ constexpr int kDecodeBarrierWord = kSplitCounterWord + 2 * kMaxSplitTiles;
 constexpr int kDecodePieceWord = kDecodeBarrierWord + 32;
 constexpr int kDecodeSegWord = kDecodePieceWord + 2 * kDecodeMaxCtas;
 constexpr size_t kStatusBlockBytes = (size_t)(kDecodeSegWord + kMaxE + 16) * 4;
-// The dense operators' workspaces: the same status block, then their buffers.
+// The dense operators' workspaces: the same status block (with the bias
+// gradient's counters, one for each 128 of 2^18 columns, in the place of the
+// split-K counters), then their buffers.
+constexpr int kBiasCounterWord = kSplitCounterWord;
+static_assert(2 * kMaxSplitTiles >= (1 << 18) / 128, "bias counters");
 constexpr size_t kStatusPad = (kStatusBlockBytes + 1023) / 1024 * 1024;
 
 // ------------------------------------------------------ argument checks --

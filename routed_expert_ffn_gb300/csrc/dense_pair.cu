@@ -180,6 +180,12 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
 }
 
+// An arrival that hands over TMEM alone: tcgen05.fence orders the reads before
+// it, and no memory is released (a release at cluster scope takes 0.85 us, which
+// a tile of few K stages waits for).
+__device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // The cluster's barrier in two halves.
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -306,42 +312,90 @@ __device__ __forceinline__ void send_3d(const CUtensorMap *m, uint8_t *slot, int
   }
 }
 
-// 32 consecutive values of the output type at `p` + off, of which `left` exist
-// (a multiple of 8; the rest zero): loaded early, added later.
-struct Values32 {
-  uint4 v[8];
-  __device__ __forceinline__ void load(const void *p, int64_t off, int left, int dtype) {
+// The bias of a tile's 256 columns, 8 to a lane; loaded a tile ahead.
+struct TileBias {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const void *p, int c, int N, int dtype, int lane) {
+    c += lane * 8;
+    if (c >= N) return;
     if (dtype == MOE_DTYPE_FP32) {
-      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + off);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = 4 * c < left ? q[c] : make_uint4(0, 0, 0, 0);
+      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + c);
+      lo = __ldg(q);
+      hi = __ldg(q + 1);
     } else {
-      const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = 8 * c < left ? q[c] : make_uint4(0, 0, 0, 0);
+      lo = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + c));
     }
   }
-  __device__ __forceinline__ void add_to(float (&f)[32], int dtype) const {
-    if (dtype == MOE_DTYPE_FP32) {
+  // f[i] += the bias of column 32 `chunk` + i
+  __device__ __forceinline__ void add_to(float (&f)[32], int chunk, int dtype) const {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        f[4 * c] += __uint_as_float(v[c].x);
-        f[4 * c + 1] += __uint_as_float(v[c].y);
-        f[4 * c + 2] += __uint_as_float(v[c].z);
-        f[4 * c + 3] += __uint_as_float(v[c].w);
-      }
-    } else {
+    for (int l = 0; l < 4; ++l) {
+      const int from = chunk * 4 + l;
+      if (dtype == MOE_DTYPE_FP32) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        for (int i = 0; i < 8; ++i)
+          f[8 * l + i] += __uint_as_float(__shfl_sync(0xffffffffu, w[i], from));
+      } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 u = unpack16(dtype, w[i]);
-          f[8 * c + 2 * i] += u.x;
-          f[8 * c + 2 * i + 1] += u.y;
+          const float2 u = unpack16(dtype, __shfl_sync(0xffffffffu, w[i], from));
+          f[8 * l + 2 * i] += u.x;
+          f[8 * l + 2 * i + 1] += u.y;
         }
       }
     }
+  }
+};
+
+// 32 rows of 32 values of the output type: loaded four lanes (16 bits) or eight
+// (fp32) to a row, so that a request takes whole sectors of few lines -- a lane
+// to a row made the epilogue of 4096 x 4096 with a residual 14 us longer -- and
+// turned by way of the output slot so that lane r has row r.  Rows and columns
+// past the ends are zero.
+struct Rows32 {
+  uint4 v[8];
+  __device__ __forceinline__ void load(const void *p, int64_t ld, int rows, int cols, int dtype,
+                                       int lane) {
+    const bool wide = dtype == MOE_DTYPE_FP32;
+    const int r = wide ? lane >> 3 : lane >> 2, c = wide ? (lane & 7) * 4 : (lane & 3) * 8;
+    const int step = wide ? 4 : 8;
+    const char *q = static_cast<const char *>(p) + ((int64_t)r * ld + c) * (wide ? 4 : 2);
+    const int64_t stride = ld * step * (wide ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < 4 || wide)
+        v[i] = step * i + r < rows && c < cols ? *reinterpret_cast<const uint4 *>(q + i * stride)
+                                               : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void add_to(float (&f)[32], uint8_t *slot, int dtype, int lane) const {
+    if (dtype == MOE_DTYPE_FP32) {
+      const int r = lane >> 3, c = lane & 7;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4 *>(slot + (4 * i + r) * 128 + ((c ^ ((4 * i + r) & 7)) << 4)) = v[i];
+      __syncwarp();
+      add32(f, slot, lane);
+    } else {
+      const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(slot + (8 * i + r) * 64 + ((c ^ ((r >> 1) & 3)) << 4)) = v[i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 o =
+            *reinterpret_cast<const uint4 *>(slot + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 u = unpack16(dtype, w[j]);
+          f[8 * i + 2 * j] += u.x;
+          f[8 * i + 2 * j + 1] += u.y;
+        }
+      }
+    }
+    __syncwarp();
   }
 };
 
@@ -671,7 +725,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
     uint8_t *turning = slot.base + S::slots * kSlotBytes;  // kEpiGatedGrad
     const int quad = warp & 3, turn = (warp >> 2) * 32;
     uint32_t tl = 0;
-    Values32 bias, res;  // kEpiLinear: of the next chunk
+    Rows32 res;             // kEpiLinear: the residual of the next 32 columns
     Tile16 next_g, next_u;  // kEpiGatedGrad: of the next 16 columns
     auto fetch = [&](int c, int row) {
       if (kEpi == kEpiGatedGrad) {
@@ -679,14 +733,44 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
         next_g.load(sv, 2 * (int64_t)a.N, a.M - (row - lane), a.N - c, lane);
         next_u.load(sv + a.N, 2 * (int64_t)a.N, a.M - (row - lane), a.N - c, lane);
       }
-      if (kEpi != kEpiLinear) return;
-      if (a.bias != nullptr) bias.load(a.bias, c, a.N - c, a.out_dtype);
-      if (a.residual != nullptr)
-        res.load(a.residual, (int64_t)row * a.ldr + c, row < a.M ? a.N - c : 0, a.out_dtype);
+      if (kEpi == kEpiLinear && a.residual != nullptr)
+        res.load(static_cast<const char *>(a.residual) +
+                     ((int64_t)(row - lane) * a.ldr + c) * (a.out_dtype == MOE_DTYPE_FP32 ? 4 : 2),
+                 a.ldr, a.M - (row - lane), a.N - c, a.out_dtype, lane);
     };
+    // What a tile's epilogue reads comes to L2 a tile ahead: a lane a row, the two
+    // warps of the rows every other 128 bytes.
+    auto warm_row = [&](const void *p, int64_t row, int64_t ld, int c, int bytes) {
+      const int n = min(a.cols, a.N - c) * bytes;
+      const char *q = static_cast<const char *>(p) + (row * ld + c) * bytes;
+      for (int o = turn * 4; o < n; o += 256)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + o));
+    };
+    auto warm = [&](int tile) {
+      if (tile >= total || kEpi == kEpiGated || (kEpi == kEpiLinear && a.residual == nullptr)) return;
+      const Tile t = tile_at(tile, a);
+      const int64_t row = t.m0 + (int)rank * kBM + quad * 32 + lane;
+      if (row >= a.M) return;
+      if (kEpi == kEpiLinear)
+        warm_row(a.residual, row, a.ldr, t.j * a.cols, a.out_dtype == MOE_DTYPE_FP32 ? 4 : 2);
+      if (kEpi == kEpiGatedGrad) {
+        warm_row(a.saved, row, 2 * (int64_t)a.N, t.j * a.cols, 4);
+        warm_row(a.saved + a.N, row, 2 * (int64_t)a.N, t.j * a.cols, 4);
+      }
+    };
+    warm(cid);
+    TileBias bias = {}, next_bias = {};
+    auto load_bias = [&](int tile) {
+      if (kEpi == kEpiLinear && a.bias != nullptr && tile < total)
+        next_bias.load(a.bias, tile_at(tile, a).j * a.cols, a.N, a.out_dtype, lane);
+    };
+    load_bias(cid);
     for (int tile = cid; tile < total; tile += ncl, ++tl) {
       const Tile t = tile_at(tile, a);
       const uint32_t buf = tl & 1u, use = tl >> 1;
+      warm(tile + ncl);
+      bias = next_bias;
+      load_bias(tile + ncl);
       const int row0 = t.m0 + (int)rank * kBM + quad * 32, row = row0 + lane;
       const int c0 = t.j * a.cols;
       int cfirst = c0, cend = c0 + a.cols;  // the columns this CTA finishes
@@ -737,28 +821,26 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       const int cstart = cfirst;
       cend = row0 < a.M ? min(a.N, cend) : cfirst;
       for (int c = cfirst + turn; c < cend; c += 64) {
-        const int left = row < a.M ? a.N - c : 0;  // this row's columns from c on
         float v[32];
         if (kEpi == kEpiLinear) {
+          const Rows32 mine = res;
+          if (a.residual != nullptr && c + 64 < cend) fetch(c + 64, row);
           tmem_ld32(tb + (c - c0), v);
           if (a.split == 2) add32(v, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, lane);
-          if (a.bias != nullptr) bias.add_to(v, a.out_dtype);
+          if (a.bias != nullptr) bias.add_to(v, (c - c0) / 32, a.out_dtype);
           if (a.extra) {
             uint8_t *p = slot.take32(lane);
             put32(p, lane, v);
             send_2d(&maps.extra, p, lane, c, row0);
           }
           activate_all(a.act, v);
-          if (a.residual != nullptr) res.add_to(v, a.out_dtype);
-          if (c + 64 < cend) fetch(c + 64, row);
-          uint8_t *p;
-          if (a.out_dtype == MOE_DTYPE_FP32) {
-            p = slot.take32(lane);
+          const bool wide = a.out_dtype == MOE_DTYPE_FP32;
+          uint8_t *p = wide ? slot.take32(lane) : slot.take16(lane);
+          if (a.residual != nullptr) mine.add_to(v, p, a.out_dtype, lane);
+          if (wide)
             put32(p, lane, v);
-          } else {
-            p = slot.take16(lane);
+          else
             put16(p, lane, a.out_dtype, v);
-          }
           send_2d(&maps.d, p, lane, c, row0);
         } else if (kEpi == kEpiGated) {
           float u[32];
@@ -825,7 +907,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[buf], lead));
+      if (lane == 0) arrive_relaxed(cluster_addr(&tempty[buf], lead));
     }
     // the slots outlive the copies that read them
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

@@ -132,19 +132,21 @@ cudaError_t forward(const DenseGemm &g, cudaStream_t s) {
   return launch_dense_pair(g, s);
 }
 
-// dw[M,N] (+)= a^T b over T rows; T = 0 leaves zeros, or what is accumulated.
-cudaError_t weight_grad(int M, int N, int T, int dtype, const void *a, int64_t lda, const void *b,
-                        int64_t ldb, void *dw, int dw_dtype, int accumulate, void *ws,
-                        cudaStream_t s) {
-  if (T == 0)
-    return accumulate ? cudaSuccess
-                      : cudaMemsetAsync(dw, 0, (size_t)M * N * (dw_dtype == MOE_DTYPE_FP32 ? 4 : 2), s);
+// dw[M,N] (+)= a^T b over T rows.
+DenseGemm weight_grad(int M, int N, int T, int dtype, const void *a, int64_t lda, const void *b,
+                      int64_t ldb, void *dw, int dw_dtype, int accumulate, void *ws) {
   DenseGemm g = product(M, N, T, dtype, a, lda, true, b, ldb, true, dw, N, dw_dtype, ws);
   if (accumulate) {
     g.residual = dw;
     g.ldr = N;
   }
-  return launch_dense_pair(g, s);
+  return g;
+}
+
+// The gradient of a weight over no rows: zeros, or what is accumulated.
+cudaError_t no_rows(void *dw, int64_t n, int dw_dtype, int accumulate, cudaStream_t s) {
+  if (dw == nullptr || accumulate) return cudaSuccess;
+  return cudaMemsetAsync(dw, 0, (size_t)n * (dw_dtype == MOE_DTYPE_FP32 ? 4 : 2), s);
 }
 
 }  // namespace
@@ -269,20 +271,25 @@ moe_status_t moe_linear_backward(const moe_linear_desc_t *in, const void *dy, co
   float *part = reinterpret_cast<float *>(at(workspace, L.part));
   const void *dz = act ? at(workspace, L.dz) : dy;
   const int64_t ldz = act ? d.N : d.y_stride;
+  if (d.T == 0) {
+    cudaError_t e = no_rows(dbias, d.N, MOE_DTYPE_FP32, accumulate, s);
+    if (e == cudaSuccess) e = no_rows(dw, (int64_t)d.N * d.K, dw_dtype, accumulate, s);
+    return cuda_status(e);
+  }
   cudaError_t e = cudaSuccess;
-  if (d.T > 0 && (dbias != nullptr || (act && (dx != nullptr || dw != nullptr))))
+  if (dbias != nullptr || (act && (dx != nullptr || dw != nullptr)))
     e = launch_act_grad(dy, d.y_stride, preact, d.T, d.N, d.act, d.dtype,
                         dx != nullptr || dw != nullptr ? at(workspace, L.dz) : nullptr, part,
                         static_cast<uint32_t *>(workspace) + kBiasCounterWord, dbias, accumulate, s);
-  else if (dbias != nullptr && !accumulate)
-    e = cudaMemsetAsync(dbias, 0, (size_t)d.N * 4, s);
-  if (e == cudaSuccess && dx != nullptr && d.T > 0)
-    e = launch_dense_pair(product(d.T, d.K, d.N, d.dtype, dz, ldz, false, w, d.K, true, dx,
-                                  d.x_stride, d.dtype, workspace),
-                          s);
-  if (e == cudaSuccess && dw != nullptr)
-    e = weight_grad(d.N, d.K, d.T, d.dtype, dz, ldz, x, d.x_stride, dw, dw_dtype, accumulate,
-                    workspace, s);
+  DenseGemm g[2];
+  int n = 0;
+  if (dx != nullptr)
+    g[n++] = product(d.T, d.K, d.N, d.dtype, dz, ldz, false, w, d.K, true, dx, d.x_stride, d.dtype,
+                     workspace);
+  if (dw != nullptr)
+    g[n++] = weight_grad(d.N, d.K, d.T, d.dtype, dz, ldz, x, d.x_stride, dw, dw_dtype, accumulate,
+                         workspace);
+  if (e == cudaSuccess && n > 0) e = launch_dense_multi(g, n, s);
   return cuda_status(e);
 }
 
@@ -338,25 +345,30 @@ moe_status_t moe_gated_ffn_backward(const moe_ffn_desc_t *d, const void *dy, con
   cudaStream_t s = (cudaStream_t)stream;
   void *h = at(workspace, L.h), *dgu = at(workspace, L.dgu);
   const int T = d->T, H = d->H, I = d->I;
-  cudaError_t e = cudaSuccess;
-  if (T > 0 && (dx != nullptr || dw13 != nullptr || dw2 != nullptr)) {
-    DenseGemm g = product(T, I, H, d->dtype, dy, H, false, w2, I, true, nullptr, 0, d->dtype,
-                          workspace);
-    g.epi = kEpiGatedGrad;
-    g.saved = const_cast<float *>(saved);
-    g.dgu = dgu;
-    g.h = h;
-    e = launch_dense_pair(g, s);
+  if (T == 0) {
+    cudaError_t e = no_rows(dw13, 2 * (int64_t)I * H, dw_dtype, accumulate, s);
+    if (e == cudaSuccess) e = no_rows(dw2, (int64_t)H * I, dw_dtype, accumulate, s);
+    return cuda_status(e);
   }
-  if (e == cudaSuccess && dx != nullptr && T > 0)
-    e = launch_dense_pair(product(T, H, 2 * I, d->dtype, dgu, 2 * (int64_t)I, false, w13, H, true,
-                                  dx, H, d->dtype, workspace),
-                          s);
-  if (e == cudaSuccess && dw13 != nullptr)
-    e = weight_grad(2 * I, H, T, d->dtype, dgu, 2 * (int64_t)I, x, H, dw13, dw_dtype, accumulate,
-                    workspace, s);
-  if (e == cudaSuccess && dw2 != nullptr)
-    e = weight_grad(H, I, T, d->dtype, dy, H, h, I, dw2, dw_dtype, accumulate, workspace, s);
+  DenseGemm g[3];
+  int n = 0;
+  if (dx != nullptr)
+    g[n++] = product(T, H, 2 * I, d->dtype, dgu, 2 * (int64_t)I, false, w13, H, true, dx, H,
+                     d->dtype, workspace);
+  if (dw13 != nullptr)
+    g[n++] = weight_grad(2 * I, H, T, d->dtype, dgu, 2 * (int64_t)I, x, H, dw13, dw_dtype,
+                         accumulate, workspace);
+  if (dw2 != nullptr)
+    g[n++] = weight_grad(H, I, T, d->dtype, dy, H, h, I, dw2, dw_dtype, accumulate, workspace);
+  if (n == 0) return MOE_OK;
+  DenseGemm up = product(T, I, H, d->dtype, dy, H, false, w2, I, true, nullptr, 0, d->dtype,
+                         workspace);
+  up.epi = kEpiGatedGrad;
+  up.saved = const_cast<float *>(saved);
+  up.dgu = dgu;
+  up.h = h;
+  cudaError_t e = launch_dense_pair(up, s);
+  if (e == cudaSuccess) e = launch_dense_multi(g, n, s);
   return cuda_status(e);
 }
 

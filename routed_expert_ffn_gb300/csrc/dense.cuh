@@ -38,6 +38,9 @@ struct DenseGemm {
 
 // Prefill and training sizes: 256-row tiles on CTA pairs (dense_pair.cu).
 cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s);
+// Two or three products with MN-major B and nothing but a residual in their
+// epilogues, in one launch: g[1] and g[2] of equal depth, g[0] of any.
+cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s);
 // Few rows: weight rows as the MMA's M, rows of A as its N, K split over a
 // cluster (dense_small.cu).  K-major operands, no preact or saved, at most
 // kSmallRows rows.

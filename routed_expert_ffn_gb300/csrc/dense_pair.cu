@@ -32,6 +32,7 @@
 // Every wait is bounded; on expiry the CTA latches the status bit and leaves
 // its loops, and both CTAs meet at a cluster barrier before TMEM is freed.
 #include <algorithm>
+#include <type_traits>
 
 #include "dense.cuh"
 #include "pair_ptx.cuh"
@@ -93,19 +94,39 @@ static_assert(2 * kRecvOff <= Shape8::stages * kStageBytes, "exchange buffers");
 // row tiles and the B rows of ~10 column tiles, ~20 MB at K = 4096: in L2.
 constexpr int kGroupM = 8;
 
-struct PairMaps {
-  CUtensorMap a, b, d, extra;  // extra: preact, saved or dgu
+// One product of a launch.
+struct Problem {
+  int M, N, nkb;  // nkb: stages of K
+  int mt, nt;     // row and column tiles
+  int a_mn;       // (kMulti) whether A is MN-major
+  int out_dtype;
+  const void *residual;
+  int64_t ldr;
+};
+struct ProblemMaps {
+  CUtensorMap a, b, d;
 };
 
+// Up to three products in one launch (kMulti): a gradient's dX and dWs, which do
+// not depend on each other, share one round-up to whole rounds and one tail.
+// Clusters first take the tiles of product 0 in turn, then those of the others;
+// the clusters that had a tile of product 0 less go on for more rounds.
+template <bool kMulti>
+struct PairMaps {
+  ProblemMaps p[kMulti ? 3 : 1];
+  CUtensorMap extra;  // preact, saved or dgu
+};
+
+template <bool kMulti>
 struct PairArgs {
-  int M, N, K;
+  Problem p[kMulti ? 3 : 1];
+  int tiles0, tiles1, tiles;  // of product 0, of 1 and of 1 and 2 (kMulti)
+  int shared_rounds;          // rounds of products 1 and 2 that every cluster takes
   int bn, cols;  // accumulator columns of a tile; output columns of a tile
-  int mt, nt;
   int split;     // pairs to a tile, K split between them (1 or 2)
   int kb_part;   // stages of K to a pair
-  int dtype, out_dtype, act;
-  const void *bias, *residual;
-  int64_t ldr;
+  int dtype, act;
+  const void *bias;
   const float *saved;
   int extra;  // kEpiLinear: store preact; kEpiGated: store saved
   const int8_t *a_scale, *b_scale;
@@ -204,16 +225,38 @@ __device__ __forceinline__ void bulk_send(uint32_t dst, const void *src, uint32_
 }
 
 struct Tile {
-  int m0, j;  // first row, column tile
+  int p, m0, j;  // product, first row, column tile
 };
-__device__ __forceinline__ Tile tile_at(int tile, const PairArgs &a) {
-  const int per = kGroupM * a.nt;
+__device__ __forceinline__ Tile tile_at(const Problem &q, int p, int tile) {
+  const int per = kGroupM * q.nt;
   const int g = tile / per, r = tile - g * per;
-  const int gm = min(kGroupM, a.mt - g * kGroupM);
+  const int gm = min(kGroupM, q.mt - g * kGroupM);
   Tile t;
+  t.p = p;
   t.j = r / gm;
   t.m0 = (g * kGroupM + r - t.j * gm) * kTileM;
   return t;
+}
+// Cluster c's i-th tile, of n clusters; false past its last.
+template <bool kMulti>
+__device__ __forceinline__ bool work_at(const PairArgs<kMulti> &a, int i, int c, int n, Tile *t) {
+  int k = i * n + c;
+  if (k < a.tiles0) {
+    *t = tile_at(a.p[0], 0, k);
+    return true;
+  }
+  if (!kMulti) return false;
+  const int more = a.tiles0 % n;  // clusters with one tile of product 0 more
+  const int j = i - a.tiles0 / n - (c < more ? 1 : 0);
+  if (j < a.shared_rounds)
+    k = j * n + c;
+  else if (c >= more)
+    k = a.shared_rounds * n + (j - a.shared_rounds) * (n - more) + c - more;
+  else
+    return false;
+  if (k >= a.tiles) return false;
+  *t = k < a.tiles1 ? tile_at(a.p[1], 1, k) : tile_at(a.p[kMulti ? 2 : 0], 2, k - a.tiles1);
+  return true;
 }
 
 // A warp's output buffer: kCount slots of 32 x 32 16-bit values, of which two
@@ -431,9 +474,10 @@ struct Tile16 {
   }
 };
 
-template <int kEpi, bool kAMn, bool kBMn, bool kE4m3>
+template <int kEpi, bool kAMn, bool kBMn, bool kE4m3, bool kMulti>
 __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
-    dense_pair_kernel(const __grid_constant__ PairMaps maps, const PairArgs a) {
+    dense_pair_kernel(const __grid_constant__ PairMaps<kMulti> maps,
+                      const __grid_constant__ PairArgs<kMulti> a) {
   typedef Shape<kEpi, kE4m3> S;
   constexpr int kStages = S::stages, kKb = S::kb;
   constexpr uint32_t kAcc = S::acc;
@@ -486,9 +530,9 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
     tmem_relinquish_pair();
   }
   if (warp == kTmaWarp && lane == 0) {
-    tma_prefetch_desc(&maps.a);
-    tma_prefetch_desc(&maps.b);
-    tma_prefetch_desc(&maps.d);
+    tma_prefetch_desc(&maps.p[0].a);
+    tma_prefetch_desc(&maps.p[0].b);
+    tma_prefetch_desc(&maps.p[0].d);
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -497,9 +541,10 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
   cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = a.mt * a.nt;
-  const int nkb = (a.K + kKb - 1) / kKb;
-  const int k_first = min(nkb, kpart * a.kb_part), k_end = min(nkb, k_first + a.kb_part);
+  // this pair's stages of K (kMulti: all of each product's)
+  const int k_first = min(a.p[0].nkb, kpart * a.kb_part);
+  const int k_last = min(a.p[0].nkb, k_first + a.kb_part);
+  auto stages_of = [&](int p) { return kMulti ? a.p[p].nkb : k_last - k_first; };
   const int half = a.bn >> 1;
   const int cid = blockIdx.x / (2 * a.split), ncl = gridDim.x / (2 * a.split);
 
@@ -513,33 +558,31 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       uint32_t st = 0, ph = 0, issued = 0;
       uint8_t *da = ring;
       bool ok = true;
-      for (int tile = cid; ok && tile < total; tile += ncl) {
-        const Tile t = tile_at(tile, a);
-        const int m = t.m0 + (int)rank * kBM;
-        const int n = kEpi == kEpiGated ? t.j * a.cols : t.j * a.cols + (int)rank * half;
+      Tile t;
+      // the stages of a tile, A's majorness known at compile time
+      auto fill = [&](auto a_mn, const CUtensorMap *ma, const CUtensorMap *mb, int m, int n,
+                      int k_end) -> bool {
         for (int kb = k_first; kb < k_end; ++kb) {
-          if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
-            ok = false;
-            break;
-          }
+          if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense))
+            return false;
           const uint32_t bar = full0 + st * 8;
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
           uint8_t *db = da + kABytes;
           const int k = kb * kKb;
-          if (kAMn) {
-            tma_load_2d_pair(da, &maps.a, bar, m, k);
-            tma_load_2d_pair(da + 8192, &maps.a, bar, m + 64, k);
+          if (a_mn.value) {
+            tma_load_2d_pair(da, ma, bar, m, k);
+            tma_load_2d_pair(da + 8192, ma, bar, m + 64, k);
           } else {
-            tma_load_2d_pair(da, &maps.a, bar, k, m);
+            tma_load_2d_pair(da, ma, bar, k, m);
           }
           if (kEpi == kEpiGated) {
             // the even CTA holds the gate columns' rows, the odd CTA the up columns'
-            tma_load_3d_pair(db, &maps.b, bar, k, n, (int)rank);
+            tma_load_3d_pair(db, mb, bar, k, n, (int)rank);
           } else if (kBMn) {
             for (int i = 0; i < b_boxes; ++i)
-              tma_load_2d_pair(db + i * 8192, &maps.b, bar, n + 64 * i, k);
+              tma_load_2d_pair(db + i * 8192, mb, bar, n + 64 * i, k);
           } else {
-            tma_load_2d_pair(db, &maps.b, bar, k, n);
+            tma_load_2d_pair(db, mb, bar, k, n);
           }
           ++issued;
           da += kStageBytes;
@@ -549,6 +592,17 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
             da = ring;
           }
         }
+        return true;
+      };
+      for (int i = 0; ok && work_at(a, i, cid, ncl, &t); ++i) {
+        const ProblemMaps *map = &maps.p[t.p];
+        const int m = t.m0 + (int)rank * kBM;
+        const int n = kEpi == kEpiGated ? t.j * a.cols : t.j * a.cols + (int)rank * half;
+        const int k_end = k_first + stages_of(t.p);
+        if (!kMulti || a.p[t.p].a_mn == (kAMn ? 1 : 0))
+          ok = fill(std::integral_constant<bool, kAMn>(), &map->a, &map->b, m, n, k_end);
+        else
+          ok = fill(std::integral_constant<bool, !kAMn>(), &map->a, &map->b, m, n, k_end);
       }
       if (rank == 0) {
         // every copy of both CTAs completes on these barriers
@@ -570,20 +624,18 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- MMA issuer --
     if (rank == 0 && lane == 0) {
-      constexpr uint32_t kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;  // 16 K, in 16 bytes
-      const uint32_t idesc = kE4m3 ? idesc_mxf8(2 * kBM, a.bn)
-                                   : idesc_16(a.dtype, kAMn, kBMn, 2 * kBM, a.bn);
+      constexpr uint32_t kBStep = kBMn ? 128 : 2;  // 16 of K, in 16 bytes
       // operand descriptors: the high words do not change, the low ones hold the
       // address in 16-byte units
       constexpr uint32_t kAHi = kAMn ? kDescHiMn : kDescHiK, kBHi = kBMn ? kDescHiMn : kDescHiK;
-      const uint32_t a0 = smem_u32(ring) >> 4 | (kAMn ? kDescLoMn : kDescLoK);
+      static_assert(kDescHiMn == kDescHiK, "one high word for either A (kMulti)");
       const uint32_t b0 = smem_u32(ring + kABytes) >> 4 | (kBMn ? kDescLoMn : kDescLoK);
       uint32_t off = 0;
       uint32_t st = 0, ph = 0, tl = 0;
       // E4M3: scale factors go to TMEM in blocks of four stages, each block
       // while the products of the one before it run
-      const int per_tile = (k_end - k_first + 3) / 4;
-      int blocks = cid < total ? (total - cid + ncl - 1) / ncl * per_tile : 0, in_tile = 0;
+      const int per_tile = (k_last - k_first + 3) / 4;
+      int blocks = cid < a.tiles0 ? (a.tiles0 - cid + ncl - 1) / ncl * per_tile : 0, in_tile = 0;
       uint32_t sg = 0, sph = 0, filled = 0, used = 0;  // hand-over buffer; TMEM slots
       auto copy_block = [&]() -> bool {
         if (blocks == 0) return true;
@@ -607,17 +659,15 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
         return true;
       };
       bool ok = !kE4m3 || copy_block();
-      for (int tile = cid; ok && tile < total; tile += ncl, ++tl) {
-        const uint32_t buf = tl & 1u, use = tl >> 1;
-        if (!mbar_wait(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) break;
-        tc_fence_after();
-        const uint32_t d0 = tmem_base + buf * kAcc;
-        for (int kb = k_first; kb < k_end; ++kb) {
-          const int ki = kb - k_first;
-          if (!mbar_wait(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
-            ok = false;
-            break;
-          }
+      Tile t;
+      auto multiply = [&](auto a_mn, uint32_t d0, int k_count) -> bool {
+        constexpr bool kMn = decltype(a_mn)::value;
+        constexpr uint32_t kAStep = kMn ? 128 : 2;
+        const uint32_t a0 = smem_u32(ring) >> 4 | (kMn ? kDescLoMn : kDescLoK);
+        const uint32_t idesc = kE4m3 ? idesc_mxf8(2 * kBM, a.bn)
+                                     : idesc_16(a.dtype, kMn, kBMn, 2 * kBM, a.bn);
+        for (int ki = 0; ki < k_count; ++ki) {
+          if (!mbar_wait(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) return false;
           uint32_t sf = 0, id = idesc;
           if (kE4m3) {
             if (ki % 4 == 0) ++used;
@@ -636,10 +686,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
             }
           }
           umma_commit_pair(&empty[st], pair_mask);
-          if (kE4m3 && ki % 4 == 0 && !copy_block()) {
-            ok = false;
-            break;
-          }
+          if (kE4m3 && ki % 4 == 0 && !copy_block()) return false;
           off += kStageBytes >> 4;
           if (++st == (uint32_t)kStages) {
             st = 0;
@@ -647,6 +694,17 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
             off = 0;
           }
         }
+        return true;
+      };
+      for (int i = 0; ok && work_at(a, i, cid, ncl, &t); ++i, ++tl) {
+        const uint32_t buf = tl & 1u, use = tl >> 1;
+        if (!mbar_wait(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) break;
+        tc_fence_after();
+        const uint32_t d0 = tmem_base + buf * kAcc;
+        if (!kMulti || a.p[t.p].a_mn == (kAMn ? 1 : 0))
+          ok = multiply(std::integral_constant<bool, kAMn>(), d0, stages_of(t.p));
+        else
+          ok = multiply(std::integral_constant<bool, !kAMn>(), d0, stages_of(t.p));
         if (!ok) break;
         umma_commit_pair(&tfull[buf], pair_mask);
       }
@@ -664,13 +722,13 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
     // products.  One hand-over for eight stages: it takes a release at cluster
     // scope, which measured 0.85 us (a stage takes 0.25).
     // Loads run one hand-over ahead.
-    const int last = (a.N - 1) >> 7;
+    const int last = (a.p[0].N - 1) >> 7, nkb = a.p[0].nkb, total = a.tiles0;
     uint32_t nx[2][4], nw[2];
     auto load = [&](int tile, int kb) {
-      const Tile t = tile_at(tile, a);
+      const Tile t = tile_at(a.p[0], 0, tile);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = min(t.m0 + (int)rank * kBM + 32 * j + lane, a.M - 1);
+        const int r = min(t.m0 + (int)rank * kBM + 32 * j + lane, a.p[0].M - 1);
         const int8_t *e = a.a_scale + (int64_t)r * nkb + kb;
         nx[0][j] = e8m0_4(e, nkb - kb);
         nx[1][j] = e8m0_4(e + 4, nkb - kb - 4);
@@ -694,7 +752,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
         for (int j = 0; j < 8; ++j) w[i][j] = __shfl_sync(0xffffffffu, nw[i], j);
       }
       kb += kSfGroup;
-      if (kb >= k_end) {
+      if (kb >= k_last) {
         kb = k_first;
         tile += ncl;
       }
@@ -727,50 +785,34 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
     uint32_t tl = 0;
     Rows32 res;             // kEpiLinear: the residual of the next 32 columns
     Tile16 next_g, next_u;  // kEpiGatedGrad: of the next 16 columns
-    auto fetch = [&](int c, int row) {
+    auto bytes_of = [](int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; };
+    auto fetch = [&](const Problem &q, int c, int row) {
       if (kEpi == kEpiGatedGrad) {
-        const float *sv = a.saved + (int64_t)(row - lane) * 2 * a.N + c;
-        next_g.load(sv, 2 * (int64_t)a.N, a.M - (row - lane), a.N - c, lane);
-        next_u.load(sv + a.N, 2 * (int64_t)a.N, a.M - (row - lane), a.N - c, lane);
+        const float *sv = a.saved + (int64_t)(row - lane) * 2 * q.N + c;
+        next_g.load(sv, 2 * (int64_t)q.N, q.M - (row - lane), q.N - c, lane);
+        next_u.load(sv + q.N, 2 * (int64_t)q.N, q.M - (row - lane), q.N - c, lane);
       }
-      if (kEpi == kEpiLinear && a.residual != nullptr)
-        res.load(static_cast<const char *>(a.residual) +
-                     ((int64_t)(row - lane) * a.ldr + c) * (a.out_dtype == MOE_DTYPE_FP32 ? 4 : 2),
-                 a.ldr, a.M - (row - lane), a.N - c, a.out_dtype, lane);
+      if (kEpi == kEpiLinear && q.residual != nullptr)
+        res.load(static_cast<const char *>(q.residual) +
+                     ((int64_t)(row - lane) * q.ldr + c) * bytes_of(q.out_dtype),
+                 q.ldr, q.M - (row - lane), q.N - c, q.out_dtype, lane);
     };
-    // What a tile's epilogue reads comes to L2 a tile ahead: a lane a row, the two
-    // warps of the rows every other 128 bytes.
-    auto warm_row = [&](const void *p, int64_t row, int64_t ld, int c, int bytes) {
-      const int n = min(a.cols, a.N - c) * bytes;
-      const char *q = static_cast<const char *>(p) + (row * ld + c) * bytes;
-      for (int o = turn * 4; o < n; o += 256)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + o));
-    };
-    auto warm = [&](int tile) {
-      if (tile >= total || kEpi == kEpiGated || (kEpi == kEpiLinear && a.residual == nullptr)) return;
-      const Tile t = tile_at(tile, a);
-      const int64_t row = t.m0 + (int)rank * kBM + quad * 32 + lane;
-      if (row >= a.M) return;
-      if (kEpi == kEpiLinear)
-        warm_row(a.residual, row, a.ldr, t.j * a.cols, a.out_dtype == MOE_DTYPE_FP32 ? 4 : 2);
-      if (kEpi == kEpiGatedGrad) {
-        warm_row(a.saved, row, 2 * (int64_t)a.N, t.j * a.cols, 4);
-        warm_row(a.saved + a.N, row, 2 * (int64_t)a.N, t.j * a.cols, 4);
-      }
-    };
-    warm(cid);
     TileBias bias = {}, next_bias = {};
-    auto load_bias = [&](int tile) {
-      if (kEpi == kEpiLinear && a.bias != nullptr && tile < total)
-        next_bias.load(a.bias, tile_at(tile, a).j * a.cols, a.N, a.out_dtype, lane);
+    auto ahead = [&](const Tile &t) {
+      if (kEpi == kEpiLinear && !kMulti && a.bias != nullptr)
+        next_bias.load(a.bias, t.j * a.cols, a.p[0].N, a.p[0].out_dtype, lane);
     };
-    load_bias(cid);
-    for (int tile = cid; tile < total; tile += ncl, ++tl) {
-      const Tile t = tile_at(tile, a);
+    Tile t, t_next;
+    bool more = work_at(a, 0, cid, ncl, &t_next);
+    if (more) ahead(t_next);
+    for (int i = 0; more; ++tl) {
+      t = t_next;
+      const Problem &q = a.p[t.p];
+      const ProblemMaps &map = maps.p[t.p];
       const uint32_t buf = tl & 1u, use = tl >> 1;
-      warm(tile + ncl);
       bias = next_bias;
-      load_bias(tile + ncl);
+      more = work_at(a, ++i, cid, ncl, &t_next);
+      if (more) ahead(t_next);
       const int row0 = t.m0 + (int)rank * kBM + quad * 32, row = row0 + lane;
       const int c0 = t.j * a.cols;
       int cfirst = c0, cend = c0 + a.cols;  // the columns this CTA finishes
@@ -779,7 +821,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       const int mid = c0 + (a.cols / 32 + 1) / 2 * 32;
       if (a.split == 2 && kpart == 0) cend = mid;
       if (a.split == 2 && kpart == 1) cfirst = mid;
-      fetch(cfirst + turn, row);
+      fetch(q, cfirst + turn, row);
       bool ok = mbar_wait(&tfull[buf], use & 1u, abort_flag, a.status, kStatusTimeoutDense);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && a.split == 1) break;
@@ -819,29 +861,29 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       }
       const uint8_t *others = ring + kRecvOff + quad * kTileBytes;
       const int cstart = cfirst;
-      cend = row0 < a.M ? min(a.N, cend) : cfirst;
+      cend = row0 < q.M ? min(q.N, cend) : cfirst;
       for (int c = cfirst + turn; c < cend; c += 64) {
         float v[32];
         if (kEpi == kEpiLinear) {
           const Rows32 mine = res;
-          if (a.residual != nullptr && c + 64 < cend) fetch(c + 64, row);
+          if (q.residual != nullptr && c + 64 < cend) fetch(q, c + 64, row);
           tmem_ld32(tb + (c - c0), v);
           if (a.split == 2) add32(v, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, lane);
-          if (a.bias != nullptr) bias.add_to(v, (c - c0) / 32, a.out_dtype);
+          if (a.bias != nullptr) bias.add_to(v, (c - c0) / 32, q.out_dtype);
           if (a.extra) {
             uint8_t *p = slot.take32(lane);
             put32(p, lane, v);
             send_2d(&maps.extra, p, lane, c, row0);
           }
           activate_all(a.act, v);
-          const bool wide = a.out_dtype == MOE_DTYPE_FP32;
+          const bool wide = q.out_dtype == MOE_DTYPE_FP32;
           uint8_t *p = wide ? slot.take32(lane) : slot.take16(lane);
-          if (a.residual != nullptr) mine.add_to(v, p, a.out_dtype, lane);
+          if (q.residual != nullptr) mine.add_to(v, p, q.out_dtype, lane);
           if (wide)
             put32(p, lane, v);
           else
-            put16(p, lane, a.out_dtype, v);
-          send_2d(&maps.d, p, lane, c, row0);
+            put16(p, lane, q.out_dtype, v);
+          send_2d(&map.d, p, lane, c, row0);
         } else if (kEpi == kEpiGated) {
           float u[32];
           tmem_ld32(tb + (c - c0), v);
@@ -863,22 +905,22 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
           for (int i = 0; i < 32; ++i) v[i] = v[i] * sigmoid(v[i]) * u[i];
           uint8_t *p = slot.take16(lane);
           put16(p, lane, a.dtype, v);
-          send_2d(&maps.d, p, lane, c, row0);
+          send_2d(&map.d, p, lane, c, row0);
         } else {
           // dh = acc;  s = sigmoid(g):  h = g s u, dg = dh u s (1 + g (1 - s)), du = dh g s
           uint32_t wh[16], wg[16], wu[16];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int hf = 0; hf < 2; ++hf) {
             float g[16], u[16], dh[16];
             next_g.turn(turning, lane, g);
             next_u.turn(turning, lane, u);
-            if (q == 0)
-              fetch(c + 16, row);
+            if (hf == 0)
+              fetch(q, c + 16, row);
             else if (c + 64 < cend)
-              fetch(c + 64, row);
-            tmem_ld16f(tb + (c - c0) + 16 * q, dh);
+              fetch(q, c + 64, row);
+            tmem_ld16f(tb + (c - c0) + 16 * hf, dh);
             if (a.split == 2)
-              add16(dh, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, q, lane);
+              add16(dh, others + (uint32_t)((c - cstart) / 32) * kChunkBytes, hf, lane);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               float h[2], dg[2], du[2];
@@ -889,14 +931,14 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
                 dg[k] = dh[i + k] * u[i + k] * s * (1.0f + g[i + k] * (1.0f - s));
                 du[k] = dh[i + k] * gs;
               }
-              wh[8 * q + i / 2] = pack16(a.dtype, h[0], h[1]);
-              wg[8 * q + i / 2] = pack16(a.dtype, dg[0], dg[1]);
-              wu[8 * q + i / 2] = pack16(a.dtype, du[0], du[1]);
+              wh[8 * hf + i / 2] = pack16(a.dtype, h[0], h[1]);
+              wg[8 * hf + i / 2] = pack16(a.dtype, dg[0], dg[1]);
+              wu[8 * hf + i / 2] = pack16(a.dtype, du[0], du[1]);
             }
           }
           uint8_t *p = slot.take16(lane);
           put16(p, lane, wh);
-          send_2d(&maps.d, p, lane, c, row0);
+          send_2d(&map.d, p, lane, c, row0);
           p = slot.take16(lane);
           put16(p, lane, wg);
           send_3d(&maps.extra, p, lane, c, row0, 0);
@@ -978,9 +1020,9 @@ PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
 }
 
 // Clusters of one and of two pairs that can run at once (per device, queried once).
-template <int kEpi, bool kAMn, bool kBMn, bool kE4m3>
+template <int kEpi, bool kAMn, bool kBMn, bool kE4m3, bool kMulti>
 cudaError_t resident_clusters(int (&out)[2]) {
-  auto kern = dense_pair_kernel<kEpi, kAMn, kBMn, kE4m3>;
+  auto kern = dense_pair_kernel<kEpi, kAMn, kBMn, kE4m3, kMulti>;
   static int resident[64][2] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -1013,70 +1055,30 @@ cudaError_t resident_clusters(int (&out)[2]) {
   return cudaSuccess;
 }
 
-// `us` not null: only the estimated time.
-template <int kEpi, bool kAMn, bool kBMn, bool kE4m3 = false>
-cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
-  constexpr int kKb = Shape<kEpi, kE4m3>::kb;
-  int resident[2];
-  cudaError_t e = resident_clusters<kEpi, kAMn, kBMn, kE4m3>(resident);
-  if (e != cudaSuccess) return e;
-  const PairPlan plan = plan_pair(g, resident);
-  if (us != nullptr) {
-    *us = plan.us;
-    return cudaSuccess;
-  }
-
-  PairArgs a = {};
-  a.M = g.M;
-  a.N = g.N;
-  a.K = g.K;
-  a.bn = plan.bn;
-  a.cols = plan.cols;
-  a.mt = plan.mt;
-  a.nt = plan.nt;
-  a.split = plan.split;
-  a.kb_part = plan.kb_part;
-  a.dtype = g.dtype;
-  a.out_dtype = g.out_dtype;
-  a.act = g.act;
-  a.bias = g.bias;
-  a.residual = g.residual;
-  a.ldr = g.ldr;
-  a.saved = g.saved;
-  a.a_scale = g.a_scale;
-  a.b_scale = g.b_scale;
-  a.status = g.status;
-  const int half = a.bn / 2;
-
-  PairMaps maps;
+// Maps and arguments of one product in tiles of bn columns.
+template <int kEpi>
+bool set_problem(const DenseGemm &g, int bn, Problem *q, ProblemMaps *m) {
+  const bool e4m3 = g.dtype == MOE_DTYPE_E4M3;
+  const int kb = e4m3 ? Shape8::kb : Shape16::kb, half = bn / 2;
+  const int cols = kEpi == kEpiGated ? half : bn;
+  *q = {g.M, g.N, (g.K + kb - 1) / kb, (g.M + kTileM - 1) / kTileM, (g.N + cols - 1) / cols,
+        g.a_mn ? 1 : 0, g.out_dtype, g.residual, g.ldr};
   const CUtensorMapSwizzle in = CU_TENSOR_MAP_SWIZZLE_128B;
-  bool ok = kAMn ? map_2d(&maps.a, g.dtype, in, g.a, g.K, g.M, g.lda, kBK, 64)
-                 : map_2d(&maps.a, g.dtype, in, g.a, g.M, g.K, g.lda, kBM, kKb);
+  bool ok = g.a_mn ? map_2d(&m->a, g.dtype, in, g.a, g.K, g.M, g.lda, kBK, 64)
+                   : map_2d(&m->a, g.dtype, in, g.a, g.M, g.K, g.lda, kBM, kb);
   if (kEpi == kEpiGated)
-    ok = ok && map_two(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, g.ldb * g.N, half, kBK, 1);
+    ok = ok && map_two(&m->b, g.dtype, in, g.b, g.N, g.K, g.ldb, g.ldb * g.N, half, kBK, 1);
   else
-    ok = ok && (kBMn ? map_2d(&maps.b, g.dtype, in, g.b, g.K, g.N, g.ldb, kBK, 64)
-                     : map_2d(&maps.b, g.dtype, in, g.b, g.N, g.K, g.ldb, half, kKb));
-  if (kEpi == kEpiLinear) {
-    ok = ok && map_2d(&maps.d, g.out_dtype, out_swizzle(g.out_dtype), g.d, g.M, g.N, g.ldd, 32, 32);
-    a.extra = g.preact != nullptr;
-    maps.extra = maps.d;
-    if (a.extra)
-      ok = ok && map_2d(&maps.extra, MOE_DTYPE_FP32, out_swizzle(MOE_DTYPE_FP32), g.preact, g.M,
-                        g.N, g.N, 32, 32);
-  } else if (kEpi == kEpiGated) {
-    ok = ok && map_2d(&maps.d, g.dtype, out_swizzle(g.dtype), g.d, g.M, g.N, g.ldd, 32, 32);
-    a.extra = g.saved != nullptr;
-    maps.extra = maps.d;
-    if (a.extra)
-      ok = ok && map_two(&maps.extra, MOE_DTYPE_FP32, out_swizzle(MOE_DTYPE_FP32), g.saved, g.M,
-                         g.N, 2 * (int64_t)g.N, g.N, 32, 32, 1);
-  } else {
-    ok = ok && map_2d(&maps.d, g.dtype, out_swizzle(g.dtype), g.h, g.M, g.N, g.N, 32, 32) &&
-         map_two(&maps.extra, g.dtype, out_swizzle(g.dtype), g.dgu, g.M, g.N, 2 * (int64_t)g.N,
-                 g.N, 32, 32, 1);
-  }
-  if (!ok) return cudaErrorInvalidValue;
+    ok = ok && (g.b_mn ? map_2d(&m->b, g.dtype, in, g.b, g.K, g.N, g.ldb, kBK, 64)
+                       : map_2d(&m->b, g.dtype, in, g.b, g.N, g.K, g.ldb, half, kb));
+  if (kEpi == kEpiGatedGrad)
+    return ok && map_2d(&m->d, g.dtype, out_swizzle(g.dtype), g.h, g.M, g.N, g.N, 32, 32);
+  return ok && map_2d(&m->d, g.out_dtype, out_swizzle(g.out_dtype), g.d, g.M, g.N, g.ldd, 32, 32);
+}
+
+template <int kEpi, bool kAMn, bool kBMn, bool kE4m3, bool kMulti>
+cudaError_t start(const PairMaps<kMulti> &maps, const PairArgs<kMulti> &a, int clusters,
+                  cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1085,13 +1087,57 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(2 * a.split * plan.clusters));
+  cfg.gridDim = dim3((unsigned)(2 * a.split * clusters));
   cfg.blockDim = dim3(Shape<kEpi, kE4m3>::threads);
   cfg.dynamicSmemBytes = smem_bytes<kEpi, kE4m3>();
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, dense_pair_kernel<kEpi, kAMn, kBMn, kE4m3>, maps, a);
+  return cudaLaunchKernelEx(&cfg, dense_pair_kernel<kEpi, kAMn, kBMn, kE4m3, kMulti>, maps, a);
+}
+
+// `us` not null: only the estimated time.
+template <int kEpi, bool kAMn, bool kBMn, bool kE4m3 = false>
+cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
+  int resident[2];
+  cudaError_t e = resident_clusters<kEpi, kAMn, kBMn, kE4m3, false>(resident);
+  if (e != cudaSuccess) return e;
+  const PairPlan plan = plan_pair(g, resident);
+  if (us != nullptr) {
+    *us = plan.us;
+    return cudaSuccess;
+  }
+
+  PairArgs<false> a = {};
+  PairMaps<false> maps;
+  bool ok = set_problem<kEpi>(g, plan.bn, &a.p[0], &maps.p[0]);
+  a.tiles0 = a.p[0].mt * a.p[0].nt;
+  a.bn = plan.bn;
+  a.cols = plan.cols;
+  a.split = plan.split;
+  a.kb_part = plan.kb_part;
+  a.dtype = g.dtype;
+  a.act = g.act;
+  a.bias = g.bias;
+  a.saved = g.saved;
+  a.a_scale = g.a_scale;
+  a.b_scale = g.b_scale;
+  a.status = g.status;
+  maps.extra = maps.p[0].d;
+  const CUtensorMapSwizzle wide = out_swizzle(MOE_DTYPE_FP32);
+  if (kEpi == kEpiLinear && g.preact != nullptr) {
+    a.extra = 1;
+    ok = ok && map_2d(&maps.extra, MOE_DTYPE_FP32, wide, g.preact, g.M, g.N, g.N, 32, 32);
+  } else if (kEpi == kEpiGated && g.saved != nullptr) {
+    a.extra = 1;
+    ok = ok && map_two(&maps.extra, MOE_DTYPE_FP32, wide, g.saved, g.M, g.N, 2 * (int64_t)g.N, g.N,
+                       32, 32, 1);
+  } else if (kEpi == kEpiGatedGrad) {
+    ok = ok && map_two(&maps.extra, g.dtype, out_swizzle(g.dtype), g.dgu, g.M, g.N,
+                       2 * (int64_t)g.N, g.N, 32, 32, 1);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  return start<kEpi, kAMn, kBMn, kE4m3, false>(maps, a, plan.clusters, s);
 }
 
 cudaError_t pair_call(const DenseGemm &g, cudaStream_t s, float *us) {
@@ -1115,6 +1161,61 @@ float dense_pair_us(const DenseGemm &g) {
 
 cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s) {
   return pair_call(g, s, nullptr);
+}
+
+cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s) {
+  if (n == 1) return launch_dense_pair(g[0], s);
+  int resident[2];
+  cudaError_t e = resident_clusters<kEpiLinear, true, true, false, true>(resident);
+  if (e != cudaSuccess) return e;
+  const int ncl = resident[0];
+  // Tile width by plan_pair's figures, each product's tiles at their own depth;
+  // a tile takes 3.3 us at least (its epilogue).
+  int bn = 0;
+  double best = 0, cost[3] = {};
+  for (int w = Shape16::acc; w >= 64; w -= 32) {
+    double c[3], sum = 0, most = 0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t tiles = (int64_t)((g[i].M + kTileM - 1) / kTileM) * ((g[i].N + w - 1) / w);
+      c[i] = std::max(3.3, (g[i].K + Shape16::kb - 1) / Shape16::kb *
+                               (0.26 + 0.0004 * std::max(0, w - 128)));
+      sum += (double)tiles * c[i];
+      most = std::max(most, c[i]);
+    }
+    const double us = std::max(sum / ncl, most) + 0.5 * most + 0.02 * w;
+    if (bn == 0 || us < best) {
+      best = us;
+      bn = w;
+      for (int i = 0; i < n; ++i) cost[i] = c[i];
+    }
+  }
+  PairArgs<true> a = {};
+  PairMaps<true> maps;
+  bool ok = true;
+  for (int i = 0; i < n; ++i) ok = ok && set_problem<kEpiLinear>(g[i], bn, &a.p[i], &maps.p[i]);
+  if (!ok) return cudaErrorInvalidValue;
+  maps.extra = maps.p[0].d;
+  if (n == 2) maps.p[2] = maps.p[1];
+  a.tiles0 = a.p[0].mt * a.p[0].nt;
+  a.tiles1 = a.p[1].mt * a.p[1].nt;
+  a.tiles = a.tiles1 + (n == 3 ? a.p[2].mt * a.p[2].nt : 0);
+  // Every cluster works for about the same time: those with a tile of product 0
+  // more leave that much of the others' to the rest.
+  const int more = a.tiles0 % ncl;
+  const double other = cost[1];
+  const double whole = ((double)a.tiles0 * cost[0] + (double)a.tiles * other) / ncl;
+  const int all = (a.tiles + ncl - 1) / ncl;
+  a.shared_rounds =
+      more == 0 ? all
+                : std::min(all, std::max(0, (int)((whole - (a.tiles0 / ncl + 1) * cost[0]) / other + 0.5)));
+  a.bn = a.cols = bn;
+  a.split = 1;
+  a.dtype = g[0].dtype;
+  a.act = MOE_ACT_NONE;
+  a.status = g[0].status;
+  const int used = (int)std::min<int64_t>(ncl, (int64_t)a.tiles0 + a.tiles);
+  if (used < ncl) a.shared_rounds = 0;  // a tile each
+  return start<kEpiLinear, true, true, false, true>(maps, a, used, s);
 }
 
 }  // namespace moe

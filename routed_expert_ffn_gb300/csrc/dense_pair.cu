@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
+    {
       const int b_boxes = (half + 63) >> 6;
       const uint32_t bytes =
           kABytes + (kBMn ? (uint32_t)b_boxes * 8192u : (uint32_t)half * 128u);
@@ -563,9 +563,10 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       auto fill = [&](auto a_mn, const CUtensorMap *ma, const CUtensorMap *mb, int m, int n,
                       int k_end) -> bool {
         for (int kb = k_first; kb < k_end; ++kb) {
-          if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense))
+          if (!mbar_wait_warp(&empty[st], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense))
             return false;
           const uint32_t bar = full0 + st * 8;
+          if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
           uint8_t *db = da + kABytes;
           const int k = kb * kKb;
@@ -583,6 +584,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
               tma_load_2d_pair(db + i * 8192, mb, bar, n + 64 * i, k);
           } else {
             tma_load_2d_pair(db, mb, bar, k, n);
+          }
           }
           ++issued;
           da += kStageBytes;
@@ -623,7 +625,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- MMA issuer --
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t kBStep = kBMn ? 128 : 2;  // 16 of K, in 16 bytes
       // operand descriptors: the high words do not change, the low ones hold the
       // address in 16-byte units
@@ -640,17 +642,19 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       auto copy_block = [&]() -> bool {
         if (blocks == 0) return true;
         const uint32_t part = (uint32_t)in_tile % (kSfGroup / 4);
-        if (part == 0 && !mbar_wait(&sf_full[sg], sph, abort_flag, a.status, kStatusTimeoutDense))
+        if (part == 0 && !mbar_wait_warp(&sf_full[sg], sph, abort_flag, a.status, kStatusTimeoutDense))
           return false;
         tc_fence_after();
         const uint32_t to = tmem_base + Shape8::sf_col + (filled++ & 3u) * kSfCols;
         const uint64_t sd = sdesc_sf(smem_u32(sf_blocks + (sg * 2 + part) * kSfBlock));
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t i = 0; i < 3; ++i) sf_copy_pair(to + 4 * i, sd + i * (512 >> 4));
+          for (uint32_t i = 0; i < 3; ++i) sf_copy_pair(to + 4 * i, sd + i * (512 >> 4));
+        }
         --blocks;
         if (++in_tile == per_tile) in_tile = 0;
         if (part == kSfGroup / 4 - 1 || in_tile == 0) {
-          umma_commit_pair(&sf_empty[sg], pair_mask);
+          if (elect_one()) umma_commit_pair(&sf_empty[sg], pair_mask);
           if (++sg == kSfBufs) {
             sg = 0;
             sph ^= 1u;
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
         const uint32_t idesc = kE4m3 ? idesc_mxf8(2 * kBM, a.bn)
                                      : idesc_16(a.dtype, kMn, kBMn, 2 * kBM, a.bn);
         for (int ki = 0; ki < k_count; ++ki) {
-          if (!mbar_wait(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) return false;
+          if (!mbar_wait_warp(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) return false;
           uint32_t sf = 0, id = idesc;
           if (kE4m3) {
             if (ki % 4 == 0) ++used;
@@ -676,16 +680,18 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
           }
           tc_fence_after();
           const uint32_t ad = a0 + off, bd = b0 + off;
+          if (elect_one()) {
 #pragma unroll
-          for (uint32_t q = 0; q < 4; ++q) {
-            const uint32_t acc = ((uint32_t)ki | q) != 0 ? 1u : 0u;
-            if (kE4m3) {
-              umma_mxf8_pair(d0, ad + 2 * q, kAHi, bd + 2 * q, kBHi, id, sf, sf + 4, acc);
-            } else {
-              umma_16_pair(d0, ad + q * kAStep, kAHi, bd + q * kBStep, kBHi, idesc, acc);
+            for (uint32_t q = 0; q < 4; ++q) {
+              const uint32_t acc = ((uint32_t)ki | q) != 0 ? 1u : 0u;
+              if (kE4m3) {
+                umma_mxf8_pair(d0, ad + 2 * q, kAHi, bd + 2 * q, kBHi, id, sf, sf + 4, acc);
+              } else {
+                umma_16_pair(d0, ad + q * kAStep, kAHi, bd + q * kBStep, kBHi, idesc, acc);
+              }
             }
+            umma_commit_pair(&empty[st], pair_mask);
           }
-          umma_commit_pair(&empty[st], pair_mask);
           if (kE4m3 && ki % 4 == 0 && !copy_block()) return false;
           off += kStageBytes >> 4;
           if (++st == (uint32_t)kStages) {
@@ -698,7 +704,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
       };
       for (int i = 0; ok && work_at(a, i, cid, ncl, &t); ++i, ++tl) {
         const uint32_t buf = tl & 1u, use = tl >> 1;
-        if (!mbar_wait(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) break;
+        if (!mbar_wait_warp(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) break;
         tc_fence_after();
         const uint32_t d0 = tmem_base + buf * kAcc;
         if (!kMulti || a.p[t.p].a_mn == (kAMn ? 1 : 0))
@@ -706,9 +712,10 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
         else
           ok = multiply(std::integral_constant<bool, !kAMn>(), d0, stages_of(t.p));
         if (!ok) break;
-        umma_commit_pair(&tfull[buf], pair_mask);
+        if (elect_one()) umma_commit_pair(&tfull[buf], pair_mask);
       }
-      umma_commit_pair(fin, (uint16_t)(1u << lead));
+      if (elect_one()) umma_commit_pair(fin, (uint16_t)(1u << lead));
+      __syncwarp();
       mbar_wait_drain(fin, 0);
     }
     __syncwarp();

@@ -217,17 +217,19 @@ __global__ void __launch_bounds__(kThreads)
   fetch(threadIdx.x);  // the first long before it is needed
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {
+    {
       uint32_t st = 0, ph = 0, issued = 0;
       for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(&empty[st], ph ^ 1u, &abort_flag, a.status, kStatusTimeoutDense)) break;
-        mbar_arrive_expect_tx(&full[st], stage_bytes);
-        uint8_t *dst = ring + st * stage_bytes;
-        if (kGated)
-          tma_load_3d(dst, &maps.w, &full[st], kb * kKb, c0, 0);
-        else
-          tma_load_2d(dst, &maps.w, &full[st], kb * kKb, c0);
-        tma_load_2d(dst + kWBytes, &maps.x, &full[st], kb * kKb, t0);
+        if (!mbar_wait_warp(&empty[st], ph ^ 1u, &abort_flag, a.status, kStatusTimeoutDense)) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[st], stage_bytes);
+          uint8_t *dst = ring + st * stage_bytes;
+          if (kGated)
+            tma_load_3d(dst, &maps.w, &full[st], kb * kKb, c0, 0);
+          else
+            tma_load_2d(dst, &maps.w, &full[st], kb * kKb, c0);
+          tma_load_2d(dst + kWBytes, &maps.x, &full[st], kb * kKb, t0);
+        }
         ++issued;
         if (++st == (uint32_t)a.stages) {
           st = 0;
@@ -244,31 +246,35 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
+    {
       const uint32_t idesc = kE4m3 ? idesc_mxf8(128, a.n) : idesc_16(a.dtype, false, false, 128, a.n);
       const uint64_t w0 = sdesc_k_sw128(smem_u32(ring));
       uint32_t st = 0, ph = 0;
       for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait(&full[st], ph, &abort_flag, a.status, kStatusTimeoutDense)) break;
-        if (kE4m3 && !mbar_wait(&sf_full[st], ph, &abort_flag, a.status, kStatusTimeoutDense)) break;
+        if (!mbar_wait_warp(&full[st], ph, &abort_flag, a.status, kStatusTimeoutDense)) break;
+        if (kE4m3 &&
+            !mbar_wait_warp(&sf_full[st], ph, &abort_flag, a.status, kStatusTimeoutDense))
+          break;
         tc_fence_after();
         const uint64_t wd = w0 + st * (stage_bytes >> 4), xd = wd + (kWBytes >> 4);
         const uint32_t sf = tmem + a.sf_col + st * kSmallSfCols;
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t q = 0; q < 4; ++q) {
-          const uint32_t acc = (kb != k0 || q != 0) ? 1u : 0u;
-          if (kE4m3)
-            umma_mxf8(tmem, wd + 2 * q, xd + 2 * q, idesc, sf, sf + 4, acc);
-          else
-            umma_bf16(tmem, wd + 2 * q, xd + 2 * q, idesc, acc);
+          for (uint32_t q = 0; q < 4; ++q) {
+            const uint32_t acc = (kb != k0 || q != 0) ? 1u : 0u;
+            if (kE4m3)
+              umma_mxf8(tmem, wd + 2 * q, xd + 2 * q, idesc, sf, sf + 4, acc);
+            else
+              umma_bf16(tmem, wd + 2 * q, xd + 2 * q, idesc, acc);
+          }
+          umma_commit(&empty[st]);
         }
-        umma_commit(&empty[st]);
         if (++st == (uint32_t)a.stages) {
           st = 0;
           ph ^= 1u;
         }
       }
-      umma_commit(&tfull);
+      if (elect_one()) umma_commit(&tfull);
     }
     __syncwarp();
   } else {

@@ -123,8 +123,8 @@ DenseGemm product(int M, int N, int K, int dtype, const void *a, int64_t lda, bo
 // A forward product by the kernel that is estimated to take less: the one for
 // few rows reads W at the rate of HBM but X once for each 128 columns; the
 // tiled one wants 256 rows for each 64 to 256 columns.  4096 x 4096 (us, few
-// rows against tiled): 24 rows 9.6 and 23, 128 rows 15.2 and 16.8, 192 rows 20.2
-// and 16.7.  preact and saved are stored by the tiled kernel only.
+// rows against tiled): 32 rows 9.6 and 14.1, 128 rows 14.9 and 14.8, 192 rows
+// 19.0 and 14.7.  preact and saved are stored by the tiled kernel only.
 cudaError_t forward(const DenseGemm &g, cudaStream_t s) {
   if (g.M <= kSmallRows && g.preact == nullptr && g.saved == nullptr &&
       dense_small_us(g) <= dense_pair_us(g))

@@ -258,6 +258,11 @@ inline CUtensorMapDataType map_type(int dtype) {
 inline int type_bytes(int dtype) {
   return dtype == MOE_DTYPE_FP32 ? 4 : (dtype == MOE_DTYPE_E4M3 ? 1 : 2);
 }
+// What HBM needs for B (a gated product's: both halves), in us.
+inline float weight_us(const DenseGemm &g) {
+  return (float)g.N * (float)g.K * (g.epi == kEpiGated ? 2.f : 1.f) *
+         (float)type_bytes(g.dtype) / 6.6e6f;
+}
 
 // [rows][cols] with rows `ld` elements apart, boxes of box_rows x box_cols.
 inline bool map_2d(CUtensorMap *m, int dtype, CUtensorMapSwizzle sw, const void *p, int64_t rows,

@@ -987,16 +987,23 @@ struct PairPlan {
   float us;
 };
 
+// Time of one stage (64 of K, E4M3 128) of a tile of bn columns.
+float stage_us(bool e4m3, int bn) {
+  return e4m3 ? 0.28f + 0.00035f * (float)bn : std::max(0.18f, 0.12f + 0.00062f * (float)bn);
+}
+
 // The plan with the least estimated time.  Fitted to the kernel on one GB300
-// over 24 to 1024 rows, N of 512 to 14336, K of 512 to 14336 (each within a few
-// per cent): a stage takes 0.26 us up to 128 columns and 0.31 at 256 (E4M3:
-// 0.37 and 0.41), a launch with its first copies 6 us, the last tile's epilogue
-// 0.02 us a column.  Splitting K in two halves a single round's stages: 4096 x
-// 14336 at 512 rows 66.6 -> 43.2 us.
+// over 32 to 2048 rows, N of 1024 to 8192, K of 1024 to 14336: a stage takes
+// 0.18 us up to 96 columns and 0.28 at 256 (E4M3: 0.30 at 64 and 0.36 at 224), a
+// launch with its first copies and its last epilogue 5.8 us and 0.013 for each
+// column, and half of the time that HBM needs for W is not hidden.  Splitting K
+// in two costs 1.2 us (E4M3: 3.5) and halves a single round's stages: 4096 x
+// 14336 at 512 rows 53.3 -> 42.4 us.
 PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
   const bool e4m3 = g.dtype == MOE_DTYPE_E4M3, gated = g.epi == kEpiGated;
   const int kb = e4m3 ? Shape8::kb : Shape16::kb;
   const int nkb = (g.K + kb - 1) / kb;
+  const float hbm = weight_us(g);
   PairPlan p = {};
   p.mt = (g.M + kTileM - 1) / kTileM;
   const int mt = p.mt;
@@ -1009,9 +1016,9 @@ PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
       const int64_t tiles = (int64_t)mt * nt;
       if (split == 2 && (tiles > resident[1] || cols < 64)) continue;  // one tile a cluster
       const int64_t rounds = (tiles + resident[split - 1] - 1) / resident[split - 1];
-      const float stage = (e4m3 ? 0.37f : 0.26f) + 0.0004f * (float)std::max(0, bn - 128);
-      const float us = 6.0f + 0.02f * (float)bn + (split == 2 ? 1.0f : 0.0f) +
-                       (float)(rounds * part) * stage;
+      const float once = e4m3 ? 5.2f + 0.01f * (float)bn : 5.8f + 0.013f * (float)bn;
+      const float us = once + (split == 1 ? 0.f : e4m3 ? 3.5f : 1.2f) +
+                       (float)(rounds * part) * stage_us(e4m3, bn) + 0.5f * hbm;
       if (p.us == 0.f || us < p.us) {
         p.us = us;
         p.bn = bn;
@@ -1184,8 +1191,7 @@ cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s) {
     double c[3], sum = 0, most = 0;
     for (int i = 0; i < n; ++i) {
       const int64_t tiles = (int64_t)((g[i].M + kTileM - 1) / kTileM) * ((g[i].N + w - 1) / w);
-      c[i] = std::max(3.3, (g[i].K + Shape16::kb - 1) / Shape16::kb *
-                               (0.26 + 0.0004 * std::max(0, w - 128)));
+      c[i] = std::max(3.3, (g[i].K + Shape16::kb - 1) / Shape16::kb * (double)stage_us(false, w));
       sum += (double)tiles * c[i];
       most = std::max(most, c[i]);
     }

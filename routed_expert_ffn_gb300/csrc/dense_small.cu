@@ -411,11 +411,11 @@ struct SmallPlan {
 };
 
 // The split with the least estimated time, fitted as plan_pair's: a stage takes
-// 0.27 us and 0.0012 for each row of X (E4M3: a tenth more; half as much again
-// where SMs hold two CTAs), a launch 6.5 us, the exchange of a split 1 us; HBM
-// takes what W's bytes take.  A split that does not fit in one round loses (192
-// rows of 4096 x 4096: 26 us split by four, 20 by two).  Tiles of 128 rows
-// measured no faster.
+// 0.2 us and 0.0014 for each row of X (E4M3: 0.27 and 0.0005; where SMs hold two
+// CTAs 1.4 and 1.25 times that), a launch 3.2 us and 0.05 for each row (two CTAs:
+// 0.07).  4096 x 4096 at 64 rows: 26.2 us unsplit, 12.0 split by eight.  A split
+// that does not fit in one round loses (192 rows: 26 us split by four, 19 by
+// two).  Tiles of 128 rows measured no faster.
 SmallPlan plan_small(const DenseGemm &g) {
   const bool e4m3 = g.dtype == MOE_DTYPE_E4M3;
   const int cols = g.epi == kEpiGated ? 64 : 128, kb = e4m3 ? 128 : 64;
@@ -424,16 +424,17 @@ SmallPlan plan_small(const DenseGemm &g) {
   p.chunks = (g.M + kChunk - 1) / kChunk;
   p.n = ((g.M + p.chunks - 1) / p.chunks + 15) / 16 * 16;
   const int64_t tiles = (int64_t)((g.N + cols - 1) / cols) * p.chunks;
-  const float stage = (0.27f + 0.0012f * (float)p.n) * (e4m3 ? 1.1f : 1.0f);
-  const float hbm = (float)g.N * (float)g.K * (g.epi == kEpiGated ? 2.f : 1.f) *
-                    (float)type_bytes(g.dtype) / 6.6e6f;
+  const float rows = (float)p.n;
+  const float stage = e4m3 ? 0.27f + 0.0005f * rows : 0.2f + 0.0014f * rows;
+  const float hbm = weight_us(g);
   for (int split = 1; split == 1 || (split <= kMaxSplit && 2 * split <= nkb); split *= 2) {
     const int64_t ctas = tiles * split, slots = 2 * num_sms();
     if (split > 1 && ctas > slots) break;
     const int64_t rounds = (ctas + slots - 1) / slots;
     const float stages = (float)(rounds * ((nkb + split - 1) / split));
-    const float us = 6.5f + std::max(stages * stage * (ctas > num_sms() ? 1.5f : 1.0f), hbm) +
-                     (split == 1 ? 0.f : 1.f);
+    const bool two = ctas > num_sms();
+    const float us = 3.2f + (two ? 0.07f : 0.05f) * rows +
+                     stages * stage * (!two ? 1.0f : e4m3 ? 1.25f : 1.4f) + 0.5f * hbm;
     if (p.us == 0.f || us <= p.us) {
       p.us = us;
       p.split = split;

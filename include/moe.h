@@ -538,7 +538,9 @@ moe_status_t moe_reshard_tp_to_ep_unpack(int32_t E_local, int32_t H, int32_t I, 
  *   MOE_DTYPE_E4M3 rows); 0 means dense rows.
  * - Workspaces: one buffer of the operator's *_workspace_size(desc) bytes,
  *   256-byte aligned, initialised once with moe_workspace_init(); read its
- *   status word with moe_get_device_status().
+ *   status word with moe_get_device_status(): bit 8 (MOE_ERR_TIMEOUT) is set
+ *   where a matrix kernel's wait ran out of time.  Calls on one stream may share
+ *   a buffer of the largest size; calls that overlap may not.
  */
 enum {
   MOE_DTYPE_BF16 = 0,

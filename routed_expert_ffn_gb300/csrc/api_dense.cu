@@ -197,7 +197,7 @@ moe_status_t moe_add_rms_norm_backward(const moe_norm_desc_t *in, const void *dy
   if (d.T == 0) {
     if (dweight == nullptr) return MOE_OK;
     if ((st = check_device()) != MOE_OK) return st;
-    return cuda_status(launch_column_sum(part, 0, d.H, d.H, dweight, 0, (cudaStream_t)stream));
+    return cuda_status(launch_column_sum(part, 0, d.H, d.H, dweight, (cudaStream_t)stream));
   }
   if (!ok_ptr(dy) || !ok_opt(dresidual) || !ok_ptr(sum) || !ok_ptr(weight) || !ok_ptr(dx))
     return MOE_ERR_INVALID_ARG;

@@ -1,6 +1,3 @@
-#ifndef AG_CTAS
-#define AG_CTAS 608
-#endif
 // The row-wise pass of the dense operators' gradients.
 //
 // act_grad: dz = dy act'(z), rounded once to the 16-bit type the gradient
@@ -19,6 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kCols = 128, kRowLanes = 8, kAhead = 4;
+constexpr int kCtas = 4 * 152;
 
 struct ActGradArgs {
   const uint16_t *dy;
@@ -121,11 +119,10 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradArgs a) {
 
 }  // namespace
 
-// Slices of the rows: about four CTAs for each of 152 SMs, each with at least
-// 32 rows.
+// Slices of the rows: about four CTAs an SM, each with at least 32 rows.
 int act_grad_slices(int T, int N) {
   const int cols = (N + kCols - 1) / kCols;
-  return std::max(1, std::min((AG_CTAS + cols - 1) / cols, (T + 31) / 32));
+  return std::max(1, std::min((kCtas + cols - 1) / cols, (T + 31) / 32));
 }
 
 cudaError_t launch_act_grad(const void *dy, int64_t ldy, const float *z, int T, int N, int act,

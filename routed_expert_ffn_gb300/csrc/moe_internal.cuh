@@ -309,9 +309,9 @@ size_t norm_bwd_part_bytes(const moe_norm_desc_t &d);  // fp32 column partials
 cudaError_t launch_add_rms_norm_backward(const moe_norm_desc_t &d, const void *dy, const void *dres,
                                          const void *sum, const void *weight, void *dx,
                                          float *dweight, float *part, cudaStream_t s);
-// out[c] (+)= sum over r < n of part[r * ld + c], in a fixed order (norm.cu).
+// out[c] = sum over r < n of part[r * ld + c], in a fixed order (norm.cu).
 cudaError_t launch_column_sum(const float *part, int n, int cols, int64_t ld, float *out,
-                              int accumulate, cudaStream_t s);
+                              cudaStream_t s);
 
 int num_sms();  // of the current device (cached)
 

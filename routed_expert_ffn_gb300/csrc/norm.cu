@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kNormRowThreads) add_rms_norm_bwd_kernel(const
 // Column sums of `part` [n][ld] over its n rows, in a fixed order: 32 columns
 // a CTA, 32 rows at a time (of which four in flight a thread).
 __global__ void __launch_bounds__(1024)
-    column_sum_kernel(const float *part, int n, int cols, int64_t ld, float *out, int accumulate) {
+    column_sum_kernel(const float *part, int n, int cols, int64_t ld, float *out) {
   __shared__ float s[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(1024)
   // warp w: column w of the CTA, lane l its row lane l
   v = warp_sum(s[cx][ry]);
   const int col = blockIdx.x * 32 + ry;
-  if (cx == 0 && col < cols) out[col] = accumulate ? out[col] + v : v;
+  if (cx == 0 && col < cols) out[col] = v;
 }
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
@@ -635,16 +635,16 @@ cudaError_t norm_backward(NormBwdArgs a, float *dweight, cudaStream_t s) {
   cudaError_t e = v == 2 ? launch_norm_bwd<T, 2>(a, grid, block, smem, s)
                          : launch_norm_bwd<T, 4>(a, grid, block, smem, s);
   if (e == cudaSuccess && dweight != nullptr)
-    e = launch_column_sum(a.part, ctas, a.H, a.H, dweight, 0, s);
+    e = launch_column_sum(a.part, ctas, a.H, a.H, dweight, s);
   return e;
 }
 
 }  // namespace
 
 cudaError_t launch_column_sum(const float *part, int n, int cols, int64_t ld, float *out,
-                              int accumulate, cudaStream_t s) {
+                              cudaStream_t s) {
   return launch_pdl(column_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, s, part, n,
-                    cols, ld, out, accumulate);
+                    cols, ld, out);
 }
 
 size_t norm_bwd_part_bytes(const moe_norm_desc_t &d) {

@@ -181,3 +181,51 @@ def test_captured_training_step():
     for v, w in zip((y, *outs), want):
         assert torch.equal(v, w)
     status_ok(ws)
+
+
+@pytest.mark.parametrize("T,H,I", [(200, 7176, 136), (300, 4104, 264), (513, 2056, 72)])
+def test_deep_products(T, H, I):
+    """Few tiles and many terms in the gated product and in its gradient: K is split between CTA
+    pairs where that pays."""
+    t = inputs(T, H, I, BF16)
+    d = moe.ffn_desc(T, H, I, moe.MOE_DTYPE_BF16)
+    ws = moe.alloc_workspace(d)
+    y, saved = torch.empty_like(t["x"]), torch.empty(T, 2 * I, device="cuda")
+    g, u, h, eg, eu, eh = hidden(t, I)
+    for keep in (saved, None):
+        y.fill_(9.0)
+        moe.moe_gated_ffn(d, t["x"], t["w13"], t["w2"], t["r"], keep, y, ws)
+        status_ok(ws)
+        w2 = t["w2"].double()
+        want = h @ w2.t() + t["r"].double()
+        er = eh + (h.abs() + eh) * half_step(BF16) + tiny(BF16)
+        e = er @ w2.abs().t() + product_bound(h, w2, I) + want.abs() * 2.0 ** -24
+        assert_within(y, want, e + (want.abs() + e) * half_step(BF16) + tiny(BF16), "y")
+    assert_within(saved, torch.cat([g, u], 1), torch.cat([eg, eu], 1) + 1e-30, "saved")
+    outs = [torch.empty_like(t[k]) for k in ("x", "w13", "w2")]
+    moe.moe_gated_ffn_backward(d, t["dy"], t["x"], t["w13"], t["w2"], saved, *outs, ws)
+    status_ok(ws)
+    leaves = [t[k].double().requires_grad_() for k in ("x", "w13", "w2")]
+    g, u = (leaves[0] @ leaves[1].t()).chunk(2, 1)
+    out = (torch.nn.functional.silu(g) * u) @ leaves[2].t()
+    for got, want in zip(outs, torch.autograd.grad(out, leaves, t["dy"].double())):
+        assert rel_l2(got, want) <= 2 * half_step(BF16)
+
+
+def test_offsets_past_32_bits():
+    """2^20 rows of 2056 columns: more than 2^31 elements."""
+    T, H, I, rows = 1 << 20, 2056, 8, 1024
+    t = inputs(rows, H, I, BF16)
+    d = moe.ffn_desc(T, H, I, moe.MOE_DTYPE_BF16)
+    ws = moe.alloc_workspace(d)
+    x, y = t["x"].repeat(T // rows, 1), torch.zeros(T, H, dtype=BF16, device="cuda")
+    moe.moe_gated_ffn(d, x, t["w13"], t["w2"], x, None, y, ws)
+    status_ok(ws)
+    _, _, h, _, _, eh = hidden(t, I)
+    w2 = t["w2"].double()
+    want = h @ w2.t() + t["x"].double()
+    er = eh + (h.abs() + eh) * half_step(BF16) + tiny(BF16)
+    e = er @ w2.abs().t() + product_bound(h, w2, I) + want.abs() * 2.0 ** -24
+    assert_within(y[:rows], want, e + (want.abs() + e) * half_step(BF16) + tiny(BF16), "first rows")
+    for i in range(0, T, T // 16):
+        assert bool((y[i:i + T // 16].view(-1, rows, H) == y[:rows]).all()), f"rows from {i}"

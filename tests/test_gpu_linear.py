@@ -287,3 +287,72 @@ def test_captured_in_a_graph_and_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (BF16, FP32), (FP16, FP16)])
+@pytest.mark.parametrize("T,N,K", [(150, 264, 14344), (200, 520, 7176), (300, 264, 4104),
+                                   (513, 1000, 8200), (700, 72, 2056)])
+def test_deep_products(T, N, K, dtype, out):
+    """Few tiles and many terms: K is split between CTA pairs."""
+    x, w = randn(81, T, K, dtype=dtype), randn(82, N, K, std=K ** -0.5, dtype=dtype)
+    b, r = randn(83, N, dtype=out), randn(84, T, N + 16, dtype=out)[:, :N]
+    d = moe.linear_desc(T, N, K, moe.dtype_of(x), "silu", out_dtype=moe.dtype_of(b),
+                        residual_stride=N + 16)
+    ws = moe.alloc_workspace(d)
+    y = torch.full((T, N), 3.0, dtype=out, device="cuda")
+    moe.moe_linear(d, x, w, b, r, y, ws)
+    status_ok(ws)
+    _, want, bound = forward_bound(x.double(), w.double(), b.double(), r.double(), "silu", y, out)
+    assert_within(y, want, bound, "y")
+
+
+@pytest.mark.parametrize("T,N,K", [(200, 136, 7184), (300, 392, 4112), (513, 264, 9216)])
+def test_deep_e4m3(T, N, K):
+    x, w = randn(85, T, K, dtype=FP32), randn(86, N, K, std=K ** -0.5, dtype=FP32)
+    x = x * torch.exp2(torch.arange(K, device="cuda").div(128, rounding_mode="floor") % 7).float()
+    r = randn(87, T, N)
+    (xq, xe), (wq, we) = quantized(x, 1), quantized(w, 128)
+    d = moe.linear_desc(T, N, K, moe.MOE_DTYPE_E4M3)
+    ws = moe.alloc_workspace(d)
+    y = torch.full((T, N), 3.0, dtype=BF16, device="cuda")
+    moe.moe_linear(d, xq, wq, None, r, y, ws, x_scale=xe, w_scale=we)
+    status_ok(ws)
+    _, want, bound = forward_bound(dequantize(xq, xe), dequantize(wq, we, 128), None, r.double(),
+                                   "none", y, BF16)
+    assert_within(y, want, bound, "y")
+
+
+@pytest.mark.parametrize("T,N,K", [(4100, 264, 136), (700, 136, 4104), (700, 4104, 136), (260, 2056, 2056)])
+def test_backward_of_unequal_products(T, N, K):
+    """dx's terms are N, dw's T: one launch holds tiles of very different depth."""
+    x, w = randn(91, T, K), randn(92, N, K, std=K ** -0.5)
+    dy = randn(93, T, N, std=0.5)
+    d = moe.linear_desc(T, N, K, moe.MOE_DTYPE_BF16)
+    ws = moe.alloc_workspace(d)
+    dx, dw = torch.empty_like(x), torch.zeros(N, K, device="cuda")
+    for i in (1, 2):  # dw accumulates
+        moe.moe_linear_backward(d, dy, x, w, None, dx, dw, None, ws, accumulate=True)
+        status_ok(ws)
+        want = dy.double() @ w.double()
+        e = product_bound(dy.double(), w.double().t(), N)
+        assert_within(dx, want, e + (want.abs() + e) * half_step(BF16) + tiny(BF16), "dx")
+        want = i * (dy.double().t() @ x.double())
+        e = i * product_bound(dy.double().t(), x.double().t(), T) + want.abs() * 2.0 ** -23
+        assert_within(dw, want, e, "dw")
+
+
+def test_offsets_past_32_bits():
+    """2^20 rows of 4096 columns: more than 2^31 elements, more than 2^33 bytes."""
+    T, N, K, rows = 1 << 20, 4096, 64, 1024
+    x, w, b = randn(94, rows, K), randn(95, N, K, std=K ** -0.5), randn(96, N)
+    d = moe.linear_desc(T, N, K, moe.MOE_DTYPE_BF16)
+    ws = moe.alloc_workspace(d)
+    y = torch.zeros(T, N, dtype=BF16, device="cuda")
+    moe.moe_linear(d, x.repeat(T // rows, 1), w, b, y, y, ws)
+    status_ok(ws)
+    _, want, bound = forward_bound(x.double(), w.double(), b.double(), None, "none", y, BF16)
+    # the residual's zeros add a rounding to fp32 only
+    assert_within(y[:rows], want, bound + want.abs() * 2.0 ** -24, "the first rows")
+    for i in range(0, T, T // 16):
+        part = y[i:i + T // 16].view(-1, rows, N)
+        assert bool((part == y[:rows]).all()), f"rows from {i}"

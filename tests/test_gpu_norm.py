@@ -203,3 +203,38 @@ def test_captured_in_a_graph_and_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+def test_offsets_past_32_bits():
+    """2^20 rows of 2056 elements: more than 2^31 of them, both directions and codes."""
+    T, H, rows, eps = 1 << 20, 2056, 1024, 1e-5
+    x, w, dy = randn(51, rows, H), randn(52, H), randn(53, rows, H, std=0.1)
+    d = moe.norm_desc(T, H, code(BF16), eps)
+    ws = moe.alloc_workspace(d)
+    many = x.repeat(T // rows, 1)
+    y = torch.empty_like(many)
+    q = torch.empty(T, H, dtype=torch.uint8, device="cuda")
+    e = torch.empty(T, -(-H // 128), dtype=torch.int8, device="cuda")
+    moe.moe_add_rms_norm(d, many, many, w, None, y, q, e)
+    torch.cuda.synchronize()
+    _, want = rms_norm(x, x, w, eps)
+    assert_within(y[:rows], want, want.abs() * (half_step(BF16) + 64 * EPS32) + tiny(BF16), "y")
+    for t in (y, q, e):
+        for i in range(0, T, T // 16):
+            assert bool((t[i:i + T // 16].view(-1, rows, t.shape[1]) == t[:rows]).all())
+    del q, e
+    grads = dy.repeat(T // rows, 1)
+    dw = torch.empty(H, device="cuda")
+    moe.moe_add_rms_norm_backward(d, grads, None, many, w, y, dw, ws)
+    torch.cuda.synchronize()
+    want, want_w = backward_ref(dy, None, x, w, eps)
+    sd, wd, dyd = x.double().cpu(), w.double().cpu(), dy.double().cpu()
+    r = 1.0 / torch.sqrt(sd.square().mean(1, keepdim=True) + eps)
+    n = sd * r
+    mag = r * ((wd * dyd).abs() + n.abs() * (wd * dyd * n).abs().mean(1, keepdim=True))
+    assert_within(y[:rows], want, want.abs() * half_step(BF16) + mag * 64 * EPS32 + tiny(BF16), "dx")
+    for i in range(0, T, T // 16):
+        assert bool((y[i:i + T // 16].view(-1, rows, H) == y[:rows]).all())
+    # a CTA adds at most T / 152 rows, then their sums are added
+    magw = (dyd * n).abs().sum(0) * (T // rows)
+    assert_within(dw, want_w * (T // rows), magw * (64 + T / 152 + 304) * EPS32, "dweight")

@@ -996,9 +996,16 @@ float stage_us(bool e4m3, int bn) {
 // over 32 to 2048 rows, N of 1024 to 8192, K of 1024 to 14336: a stage takes
 // 0.18 us up to 96 columns and 0.28 at 256 (E4M3: 0.30 at 64 and 0.36 at 224), a
 // launch with its first copies and its last epilogue 5.8 us and 0.013 for each
-// column, and half of the time that HBM needs for W is not hidden.  Splitting K
-// in two costs 1.2 us (E4M3: 3.5) and halves a single round's stages: 4096 x
-// 14336 at 512 rows 53.3 -> 42.4 us.
+// column, and half of the time that HBM needs for W is not hidden; a cluster's
+// tiles are at least 0.45 us and 0.0085 for each column apart (their epilogues:
+// 4096 x 4096 x 64 19.3 us in 64 columns, 13.8 in 256).  Splitting K in two costs
+// 1.2 us (E4M3: 3.5) and halves a single round's stages: 4096 x 14336 at 512 rows
+// 53.3 -> 42.4 us.
+//
+// Tried on the same shapes and slower or the same: two pairs of a cluster that
+// share B by multicast (1024 x 4096 x 4096 26.9 us against 25.0: what an SM takes
+// in limits, not L2), eight stages of 24 KB for narrow tiles, 12 or 16 epilogue
+// warps, the residual two chunks ahead in registers.
 PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
   const bool e4m3 = g.dtype == MOE_DTYPE_E4M3, gated = g.epi == kEpiGated;
   const int kb = e4m3 ? Shape8::kb : Shape16::kb;
@@ -1017,8 +1024,9 @@ PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
       if (split == 2 && (tiles > resident[1] || cols < 64)) continue;  // one tile a cluster
       const int64_t rounds = (tiles + resident[split - 1] - 1) / resident[split - 1];
       const float once = e4m3 ? 5.2f + 0.01f * (float)bn : 5.8f + 0.013f * (float)bn;
-      const float us = once + (split == 1 ? 0.f : e4m3 ? 3.5f : 1.2f) +
-                       (float)(rounds * part) * stage_us(e4m3, bn) + 0.5f * hbm;
+      const float tile = (float)part * stage_us(e4m3, bn), drain = 0.45f + 0.0085f * (float)bn;
+      const float us = once + (split == 1 ? 0.f : e4m3 ? 3.5f : 1.2f) + tile +
+                       (float)(rounds - 1) * std::max(tile, drain) + 0.5f * hbm;
       if (p.us == 0.f || us < p.us) {
         p.us = us;
         p.bn = bn;

@@ -14,11 +14,12 @@
 // codes); backward: 3 read, 1 written.  A row lives in the registers of one
 // group of threads (kV chunks of 8 elements a thread), so every tensor is read
 // once, and the mean costs one shuffle reduction and one exchange through
-// shared memory.  With many rows the CTAs stay and walk the rows, and each
-// thread copies its own chunks of the next rows to shared memory meanwhile
-// (cp.async into a ring that no other thread touches): loads stay in flight
-// through the reductions without taking registers.  The arithmetic is done on
-// pairs (f32x2): with one instruction an element it took as long as the bytes.
+// shared memory.  Forward a CTA ends with its row (or few short ones); backward
+// the CTAs stay and walk the rows, adding up dw in registers, and each thread
+// copies its own chunks of the next rows to shared memory meanwhile (cp.async
+// into a ring that no other thread touches): loads stay in flight through the
+// reductions without taking registers.  The arithmetic is done on pairs (f32x2):
+// with one instruction an element it took as long as the bytes.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -29,8 +30,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kNormMaxThreads = 1024;
-constexpr int kNormRowThreads = 512;  // of the CTAs that walk rows
+constexpr int kNormThreads = 512;
 
 // ---------------------------------------------------------- pairs of fp32 --
 
@@ -218,8 +218,7 @@ struct NormArgs {
   uint8_t *q;
   int8_t *scale;
   int64_t x_stride, r_stride, y_stride;
-  int T, H, group, rows;  // threads to a row, rows to a CTA
-  int depth;              // rows of the ring
+  int T, H, group;  // group: threads to a row
   float eps;
 };
 
@@ -262,8 +261,7 @@ __device__ __forceinline__ void store_codes(const NormArgs &a, const pair_t (&y)
 template <typename T, int kV>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)[kV],
                                          const Chunk<T> (&rr)[kV], const Chunk<T> (&rw)[kV],
-                                         int64_t row, int sub, int t, float *part) {
-  const bool live = row < a.T;
+                                         int64_t row, int sub, int t, bool live, float *part) {
   pair_t s[kV][4], sq = make_pair(0.f, 0.f);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
@@ -280,7 +278,7 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)
   }
   const float mine = warp_sum(lo_of(sq) + hi_of(sq));
   const int warps = a.group >> 5;
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mine;
+  if ((t & 31) == 0) part[sub * warps + (t >> 5)] = mine;
   __syncthreads();
   float sum = 0.f;
   for (int i = 0; i < warps; ++i) sum += part[sub * warps + i];
@@ -298,79 +296,32 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)
   }
 }
 
-// Few rows: a CTA (whole warps) to a row.
-template <typename T, int kV>
-__global__ void __launch_bounds__(kNormMaxThreads) add_rms_norm_kernel(const NormArgs a) {
-  __shared__ float part[kNormMaxThreads / 32];
-  const int64_t row = blockIdx.x;
-  const int t = threadIdx.x;
+// blockDim.x threads (whole warps) to a row, kOne: the CTA's only one.  Registers
+// are held down to 40 a thread of two chunks (64 of four): what hides the loads is
+// other CTAs' rows (8192 x 7168 78.4 us with 48, 69.9 with 40).  CTAs that stayed
+// and copied the next rows to shared memory meanwhile took 9.4 us for 1021 x 4104
+// (this 6.9), 44.9 for 8192 x 4096 (40.5), 17.0 for 16384 x 512 (15.1).
+template <typename T, int kV, bool kOne>
+__global__ void __launch_bounds__(kNormThreads, (kV == 2 ? 3 : 2) - (sizeof(T) == 4 ? 1 : 0))
+    add_rms_norm_kernel(const NormArgs a) {
+  __shared__ float part[kNormThreads / 32];
+  const int sub = kOne ? 0 : threadIdx.y, t = threadIdx.x;
+  const int64_t row = kOne ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * blockDim.y + sub;
+  const bool live = kOne || row < a.T;
   const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
   const T *res = static_cast<const T *>(a.residual) + row * a.r_stride;
   pdl_wait();
   Chunk<T> rx[kV], rr[kV], rw[kV];
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
-    rx[v] = load_chunk(x, v, a.group, t, a.H, true);
-    rr[v] = load_chunk(res, v, a.group, t, a.H, a.residual != nullptr);
+    rx[v] = load_chunk(x, v, a.group, t, a.H, live);
+    rr[v] = load_chunk(res, v, a.group, t, a.H, live && a.residual != nullptr);
   }
 #pragma unroll
   for (int v = 0; v < kV; ++v)
     rw[v] = load_chunk(static_cast<const T *>(a.weight), v, a.group, t, a.H, true);
   pdl_launch_dependents();
-  norm_row<T, kV>(a, rx, rr, rw, row, 0, t, part);
-}
-
-// Many rows: CTA b's group g walks rows b * rows + g, + gridDim.x * rows, ...
-// with `depth` - 1 rows on their way to its ring.
-template <typename T, int kV>
-__global__ void __launch_bounds__(kNormRowThreads) add_rms_norm_rows_kernel(const NormArgs a) {
-  __shared__ float part[2][kNormRowThreads / 32];
-  extern __shared__ uint4 s_ring[];
-  const int sub = threadIdx.x / a.group, t = threadIdx.x - sub * a.group;
-  const int threads = blockDim.x;
-  const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
-  const uint32_t chunk = (uint32_t)threads * 16u * (uint32_t)Chunk<T>::kPieces;
-  const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16u;
-  pdl_wait();
-  pdl_launch_dependents();
-  Chunk<T> rw[kV];
-#pragma unroll
-  for (int v = 0; v < kV; ++v)
-    rw[v] = load_chunk(static_cast<const T *>(a.weight), v, a.group, t, a.H, true);
-  auto fill = [&](int64_t row, int slot) {
-    if (row < a.T) {
-#pragma unroll
-      for (int v = 0; v < kV; ++v) {
-        const uint32_t at = ring + (uint32_t)(slot * 2 * kV + v) * chunk;
-        ring_fill(at, x + row * a.x_stride, v, a.group, t, a.H, threads);
-        if (res != nullptr)
-          ring_fill(at + kV * chunk, res + row * a.r_stride, v, a.group, t, a.H, threads);
-      }
-    }
-    ring_commit();
-  };
-  const int64_t step = (int64_t)gridDim.x * a.rows;
-  int64_t row = (int64_t)blockIdx.x * a.rows + sub, ahead = row;
-  for (int i = 0; i + 1 < a.depth; ++i, ahead += step) fill(ahead, i);
-  int slot = 0, next = a.depth - 1, buf = 0;
-  // every group makes the same number of trips (the barrier is the CTA's)
-  for (int64_t r0 = (int64_t)blockIdx.x * a.rows; r0 < a.T; r0 += step, row += step, ahead += step) {
-    fill(ahead, next);  // of depth 1 the row itself
-    ring_wait(a.depth - 1);
-    Chunk<T> rx[kV], rr[kV];
-#pragma unroll
-    for (int v = 0; v < kV; ++v) {
-      const uint32_t at = ring + (uint32_t)(slot * 2 * kV + v) * chunk;
-      rx[v] = ring_read<T>(at, v, a.group, t, a.H, threads, row < a.T);
-      rr[v] = ring_read<T>(at + kV * chunk, v, a.group, t, a.H, threads,
-                           row < a.T && res != nullptr);
-    }
-    // two buffers of partial sums: the next trip writes the other one
-    norm_row<T, kV>(a, rx, rr, rw, row, sub, t, part[buf]);
-    buf ^= 1;
-    slot = slot + 1 == a.depth ? 0 : slot + 1;
-    next = next + 1 == a.depth ? 0 : next + 1;
-  }
+  norm_row<T, kV>(a, rx, rr, rw, row, sub, t, live, part);
 }
 
 struct NormBwdArgs {
@@ -382,13 +333,14 @@ struct NormBwdArgs {
   float eps;
 };
 
-// As add_rms_norm_rows_kernel.  dy n is kept per column in registers, joined
+// CTA b's group g walks rows b * rows + g, + gridDim.x * rows, ... with `depth`
+// - 1 rows on their way to its ring.  dy n is kept per column in registers, joined
 // over the CTA's groups through shared memory at the end and left as one row of
 // partials for the second kernel: a fixed order, so the sums do not change from
 // run to run.
 template <typename T, int kV>
-__global__ void __launch_bounds__(kNormRowThreads) add_rms_norm_bwd_kernel(const NormBwdArgs a) {
-  __shared__ float2 s_part[2][kNormRowThreads / 32];
+__global__ void __launch_bounds__(kNormThreads) add_rms_norm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float2 s_part[2][kNormThreads / 32];
   extern __shared__ uint4 s_ring[];
   // wide or fp32 rows leave no registers for the weight: it is read from L1
   constexpr bool kKeepWeight = kV == 2 && sizeof(T) == 2, kKeepProduct = kV == 2;
@@ -566,39 +518,20 @@ int ring_depth(size_t row_bytes, int per_sm) {
   return d >= 2 ? std::min(d, 4) : (2 * row_bytes <= 200 * 1024 ? 2 : 1);
 }
 
-template <typename T, int kV>
-cudaError_t launch_norm_rows(const NormArgs &a, dim3 grid, dim3 block, size_t smem, cudaStream_t s) {
-  static size_t allowed[64] = {};
-  const cudaError_t e = allow_smem(add_rms_norm_rows_kernel<T, kV>, smem, allowed);
-  return e != cudaSuccess
-             ? e
-             : launch_pdl(add_rms_norm_rows_kernel<T, kV>, grid, block, smem, s, a);
-}
-
 template <typename T>
 cudaError_t norm_forward(NormArgs a, cudaStream_t s) {
   const int nch = a.H / 8;
-  if (a.T <= 2 * num_sms()) {
-    // latency counts: one chunk a thread where 1024 threads hold the row
-    const int v = nch <= kNormMaxThreads ? 1 : 2;
-    a.rows = 1;
-    a.group = round_up((nch + v - 1) / v, 32);
-    const dim3 grid((unsigned)a.T), block((unsigned)a.group);
-    return v == 1 ? launch_pdl(add_rms_norm_kernel<T, 1>, grid, block, 0, s, a)
-                  : launch_pdl(add_rms_norm_kernel<T, 2>, grid, block, 0, s, a);
-  }
-  // Four chunks a thread and three CTAs an SM; two where codes are made, which
-  // wants the registers (8192 x 7168: 73 us of three, 82 of two; to E4M3 66 of
-  // two, 81 of three).
-  a.group = round_up((nch + 3) / 4, 32);
-  a.rows = std::max(1, 256 / a.group);
-  const int per_sm = a.q != nullptr ? 2 : 3;
-  const size_t row_bytes = (size_t)8 * a.group * a.rows * 8 * sizeof(T);
-  a.depth = ring_depth(row_bytes, per_sm);
-  const size_t smem = (size_t)a.depth * row_bytes;
-  const int fit = (int)std::min<size_t>(per_sm, std::max<size_t>(1, 210 * 1024 / smem));
-  const int ctas = std::min((a.T + a.rows - 1) / a.rows, fit * num_sms());
-  return launch_norm_rows<T, 4>(a, dim3((unsigned)ctas), dim3((unsigned)(a.group * a.rows)), smem, s);
+  // Two chunks a thread, four in rows that 512 threads do not hold else, and where
+  // long rows are coded (8192 x 7168 to E4M3: 72.3 us of two, 69.8 of four; 5120
+  // columns 53.1 and 52.0, without codes 50.4 and 50.9).
+  const int v = nch > 2 * kNormThreads || (a.q != nullptr && nch > 640) ? 4 : 2;
+  a.group = round_up((nch + v - 1) / v, 32);
+  // a warp's rows four to a CTA (65536 x 256: 31.6 us, of one 34.4)
+  const int rows = a.group == 32 ? 4 : 1;
+  const dim3 grid((unsigned)((a.T + rows - 1) / rows)), block((unsigned)a.group, (unsigned)rows);
+  if (rows > 1) return launch_pdl(add_rms_norm_kernel<T, 2, false>, grid, block, 0, s, a);
+  return v == 2 ? launch_pdl(add_rms_norm_kernel<T, 2, true>, grid, block, 0, s, a)
+                : launch_pdl(add_rms_norm_kernel<T, 4, true>, grid, block, 0, s, a);
 }
 
 // Threads to a row, rows to a CTA and CTAs of the backward pass: two an SM while
@@ -606,7 +539,7 @@ cudaError_t norm_forward(NormArgs a, cudaStream_t s) {
 // 448 threads do not fit twice: 86 of two, 80 of one).
 void norm_bwd_shape(int T, int H, int sms, int *v, int *group, int *rows, int *per_sm, int *ctas) {
   const int nch = H / 8;
-  *v = nch <= 2 * kNormRowThreads ? 2 : 4;
+  *v = nch <= 2 * kNormThreads ? 2 : 4;
   *group = round_up((nch + *v - 1) / *v, 32);
   *rows = std::max(1, 256 / *group);
   *per_sm = *group * *rows <= 256 ? 2 : 1;
@@ -657,7 +590,7 @@ cudaError_t launch_add_rms_norm(const moe_norm_desc_t &d, const void *x, const v
                                 const void *weight, void *residual_out, void *y, uint8_t *q,
                                 int8_t *scale, cudaStream_t s) {
   NormArgs a = {x, residual, weight, residual_out, y, q, scale, d.x_stride, d.residual_stride,
-                d.y_stride, d.T, d.H, 0, 0, 0, d.eps};
+                d.y_stride, d.T, d.H, 0, d.eps};
   switch (d.dtype) {
     case MOE_DTYPE_BF16: return norm_forward<__nv_bfloat16>(a, s);
     case MOE_DTYPE_FP16: return norm_forward<__half>(a, s);

@@ -42,13 +42,14 @@ cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s);
 // epilogues, in one launch: g[1] and g[2] of equal depth, g[0] of any.
 cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s);
 // Few rows: weight rows as the MMA's M, rows of A as its N, K split over a
-// cluster (dense_small.cu).  K-major operands, no preact or saved, at most
-// kSmallRows rows.
+// cluster (dense_small.cu).  A K-major, B either (MN-major: 16 bits, not gated), no
+// preact or saved, at most kSmallRows rows.
 constexpr int kSmallRows = 1024;
 cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s);
 // What each is estimated to take, in us (0 if it cannot be told).
 float dense_pair_us(const DenseGemm &g);
 float dense_small_us(const DenseGemm &g);
+float dense_multi_us(const DenseGemm *g, int n);
 
 // dz = dy act'(z) in 16 bits (act none: not written) and the column sums of the
 // unrounded dz to dbias (null: none), by way of part [slices][N] and one zero
@@ -153,6 +154,9 @@ __host__ __device__ constexpr uint32_t idesc_16(int dtype, bool a_mn, bool b_mn,
 //             1024 bytes apart (stride), boxes 8192 bytes apart (leading)
 constexpr uint32_t kDescLoK = 1u << 16, kDescLoMn = (8192u >> 4) << 16;
 constexpr uint32_t kDescHiK = (1024u >> 4) | (1u << 14) | (2u << 29), kDescHiMn = kDescHiK;
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  return (uint64_t)kDescHiMn << 32 | kDescLoMn | (saddr & 0x3FFFFu) >> 4;
+}
 
 // 32 lanes x 32 consecutive 32-bit columns; thread i gets lane (base + i).
 // The wait is part of the same statement: no use can move in front of it.

@@ -1185,16 +1185,16 @@ cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s) {
   return pair_call(g, s, nullptr);
 }
 
-cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s) {
-  if (n == 1) return launch_dense_pair(g[0], s);
-  int resident[2];
-  cudaError_t e = resident_clusters<kEpiLinear, true, true, false, true>(resident);
-  if (e != cudaSuccess) return e;
-  const int ncl = resident[0];
-  // Tile width by plan_pair's figures, each product's tiles at their own depth;
-  // a tile takes 3.3 us at least (its epilogue).
-  int bn = 0;
-  double best = 0, cost[3] = {};
+namespace {
+
+// Tile width by plan_pair's figures, each product's tiles at their own depth; a
+// tile takes 3.3 us at least (its epilogue).
+struct MultiPlan {
+  int bn;
+  double us, cost[3];
+};
+MultiPlan plan_multi(const DenseGemm *g, int n, int ncl) {
+  MultiPlan p = {};
   for (int w = Shape16::acc; w >= 64; w -= 32) {
     double c[3], sum = 0, most = 0;
     for (int i = 0; i < n; ++i) {
@@ -1204,12 +1204,34 @@ cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s) {
       most = std::max(most, c[i]);
     }
     const double us = std::max(sum / ncl, most) + 0.5 * most + 0.02 * w;
-    if (bn == 0 || us < best) {
-      best = us;
-      bn = w;
-      for (int i = 0; i < n; ++i) cost[i] = c[i];
+    if (p.bn == 0 || us < p.us) {
+      p.us = us;
+      p.bn = w;
+      for (int i = 0; i < n; ++i) p.cost[i] = c[i];
     }
   }
+  return p;
+}
+
+}  // namespace
+
+float dense_multi_us(const DenseGemm *g, int n) {
+  if (n == 1) return dense_pair_us(g[0]);
+  int resident[2];
+  return resident_clusters<kEpiLinear, true, true, false, true>(resident) == cudaSuccess
+             ? (float)plan_multi(g, n, resident[0]).us
+             : 0.f;
+}
+
+cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s) {
+  if (n == 1) return launch_dense_pair(g[0], s);
+  int resident[2];
+  cudaError_t e = resident_clusters<kEpiLinear, true, true, false, true>(resident);
+  if (e != cudaSuccess) return e;
+  const int ncl = resident[0];
+  const MultiPlan plan = plan_multi(g, n, ncl);
+  const int bn = plan.bn;
+  const double (&cost)[3] = plan.cost;
   PairArgs<true> a = {};
   PairMaps<true> maps;
   bool ok = true;

@@ -135,7 +135,21 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *m, int c0, in
                "r"(c0), "r"(c1), "r"(c2)
                : "memory");
 }
-template <bool kGated, bool kE4m3>
+// W's tile of a stage: kGated 64 gate and 64 up rows; kMn 128 columns of the
+// MN-major W (a gradient's) in two boxes of 64.
+template <bool kGated, bool kMn>
+__device__ __forceinline__ void load_w(void *dst, const CUtensorMap *m, uint64_t *bar, int k, int c0) {
+  if (kGated) {
+    tma_load_3d(dst, m, bar, k, c0, 0);
+  } else if (kMn) {
+    tma_load_2d(dst, m, bar, c0, k);
+    tma_load_2d(static_cast<uint8_t *>(dst) + kWBytes / 2, m, bar, c0 + 64, k);
+  } else {
+    tma_load_2d(dst, m, bar, k, c0);
+  }
+}
+
+template <bool kGated, bool kE4m3, bool kMn>
 __global__ void __launch_bounds__(kThreads)
     dense_small_kernel(const __grid_constant__ SmallMaps maps, const SmallArgs a) {
   constexpr int kCols = kGated ? 64 : 128;  // output columns of a tile
@@ -184,10 +198,14 @@ __global__ void __launch_bounds__(kThreads)
   // slower, 14336 x 4096 21 -> 26 us.)
   if (warp == kTmaWarp && lane == 0)
     for (int kb = k0; kb < min(k1, k0 + a.stages); ++kb) {
-      if (kGated)
+      if (kGated) {
         tma_prefetch_3d(&maps.w, kb * kKb, c0, 0);
-      else
+      } else if (kMn) {
+        tma_prefetch_2d(&maps.w, c0, kb * kKb);
+        tma_prefetch_2d(&maps.w, c0 + 64, kb * kKb);
+      } else {
         tma_prefetch_2d(&maps.w, kb * kKb, c0);
+      }
     }
   tc_fence_before();
   __syncthreads();
@@ -224,10 +242,7 @@ __global__ void __launch_bounds__(kThreads)
         if (elect_one()) {
           mbar_arrive_expect_tx(&full[st], stage_bytes);
           uint8_t *dst = ring + st * stage_bytes;
-          if (kGated)
-            tma_load_3d(dst, &maps.w, &full[st], kb * kKb, c0, 0);
-          else
-            tma_load_2d(dst, &maps.w, &full[st], kb * kKb, c0);
+          load_w<kGated, kMn>(dst, &maps.w, &full[st], kb * kKb, c0);
           tma_load_2d(dst + kWBytes, &maps.x, &full[st], kb * kKb, t0);
         }
         ++issued;
@@ -247,8 +262,10 @@ __global__ void __launch_bounds__(kThreads)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     {
-      const uint32_t idesc = kE4m3 ? idesc_mxf8(128, a.n) : idesc_16(a.dtype, false, false, 128, a.n);
-      const uint64_t w0 = sdesc_k_sw128(smem_u32(ring));
+      const uint32_t idesc = kE4m3 ? idesc_mxf8(128, a.n) : idesc_16(a.dtype, kMn, false, 128, a.n);
+      const uint64_t x0 = sdesc_k_sw128(smem_u32(ring + kWBytes));
+      const uint64_t w0 = kMn ? sdesc_mn_sw128(smem_u32(ring)) : sdesc_k_sw128(smem_u32(ring));
+      constexpr uint32_t kWStep = kMn ? 128 : 2;  // 16 of K, in 16 bytes
       uint32_t st = 0, ph = 0;
       for (int kb = k0; kb < k1; ++kb) {
         if (!mbar_wait_warp(&full[st], ph, &abort_flag, a.status, kStatusTimeoutDense)) break;
@@ -256,7 +273,7 @@ __global__ void __launch_bounds__(kThreads)
             !mbar_wait_warp(&sf_full[st], ph, &abort_flag, a.status, kStatusTimeoutDense))
           break;
         tc_fence_after();
-        const uint64_t wd = w0 + st * (stage_bytes >> 4), xd = wd + (kWBytes >> 4);
+        const uint64_t wd = w0 + st * (stage_bytes >> 4), xd = x0 + st * (stage_bytes >> 4);
         const uint32_t sf = tmem + a.sf_col + st * kSmallSfCols;
         if (elect_one()) {
 #pragma unroll
@@ -265,7 +282,7 @@ __global__ void __launch_bounds__(kThreads)
             if (kE4m3)
               umma_mxf8(tmem, wd + 2 * q, xd + 2 * q, idesc, sf, sf + 4, acc);
             else
-              umma_bf16(tmem, wd + 2 * q, xd + 2 * q, idesc, acc);
+              umma_bf16(tmem, wd + kWStep * q, xd + 2 * q, idesc, acc);
           }
           umma_commit(&empty[st]);
         }
@@ -443,9 +460,9 @@ SmallPlan plan_small(const DenseGemm &g) {
   return p;
 }
 
-template <bool kGated, bool kE4m3>
+template <bool kGated, bool kE4m3, bool kMn>
 cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
-  auto kern = dense_small_kernel<kGated, kE4m3>;
+  auto kern = dense_small_kernel<kGated, kE4m3, kMn>;
   constexpr int kCols = kGated ? 64 : 128, kKb = kE4m3 ? 128 : 64;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -492,6 +509,7 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
   const bool ok =
       (kGated ? map_two(&maps.w, g.dtype, CU_TENSOR_MAP_SWIZZLE_128B, g.b, g.N, g.K, g.ldb,
                         g.ldb * g.N, 64, kKb, 2)
+       : kMn  ? map_2d(&maps.w, g.dtype, CU_TENSOR_MAP_SWIZZLE_128B, g.b, g.K, g.N, g.ldb, kKb, 64)
               : map_2d(&maps.w, g.dtype, CU_TENSOR_MAP_SWIZZLE_128B, g.b, g.N, g.K, g.ldb, 128, kKb)) &&
       map_2d(&maps.x, g.dtype, CU_TENSOR_MAP_SWIZZLE_128B, g.a, g.M, g.K, g.lda, a.n, kKb);
   if (!ok) return cudaErrorInvalidValue;
@@ -525,8 +543,9 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
 float dense_small_us(const DenseGemm &g) { return plan_small(g).us; }
 
 cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s) {
-  if (g.dtype == MOE_DTYPE_E4M3) return launch<false, true>(g, s);
-  return g.epi == kEpiGated ? launch<true, false>(g, s) : launch<false, false>(g, s);
+  if (g.dtype == MOE_DTYPE_E4M3) return launch<false, true, false>(g, s);
+  if (g.epi == kEpiGated) return launch<true, false, false>(g, s);
+  return g.b_mn ? launch<false, false, true>(g, s) : launch<false, false, false>(g, s);
 }
 
 }  // namespace moe

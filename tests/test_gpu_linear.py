@@ -356,3 +356,31 @@ def test_offsets_past_32_bits():
     for i in range(0, T, T // 16):
         part = y[i:i + T // 16].view(-1, rows, N)
         assert bool((part == y[:rows]).all()), f"rows from {i}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T,N,K", [(1, 6336, 400), (16, 4104, 136), (17, 2056, 72), (64, 8200, 264), (33, 5000, 8)])
+def test_backward_of_few_rows_and_many_terms(T, N, K, dtype):
+    """dx of few rows and columns over many terms: the kernel for few rows, W as it lies."""
+    x, w = randn(97, T, K, dtype=dtype), randn(98, N, K, std=K ** -0.5, dtype=dtype)
+    dy = randn(99, T, N + 8, std=0.5, dtype=dtype)[:, :N]
+    d = moe.linear_desc(T, N, K, moe.dtype_of(x), y_stride=N + 8, x_stride=K + 16)
+    ws = moe.alloc_workspace(d)
+    dxw = torch.full((T + 1, K + 16), 7.0, dtype=dtype, device="cuda")
+    xw = torch.zeros(T, K + 16, dtype=dtype, device="cuda")
+    xw[:, :K] = x
+    dx, dw, db = dxw[:T, :K], torch.empty_like(w), torch.empty(N, device="cuda")
+    want = dy.double() @ w.double()
+    e = product_bound(dy.double(), w.double().t(), N)
+    bound = e + (want.abs() + e) * half_step(dtype) + tiny(dtype)
+    wdw = dy.double().t() @ x.double()
+    e = product_bound(dy.double().t(), x.double().t(), T)
+    for only in (False, True):
+        dx.fill_(9.0)
+        moe.moe_linear_backward(d, dy, xw[:, :K], w, None, dx, None if only else dw,
+                                None if only else db, ws)
+        status_ok(ws)
+        assert_within(dx, want, bound, "dx")
+        assert bool((dxw[T:] == 7).all()) and bool((dxw[:, K:] == 7).all())
+    assert_within(dw, wdw, e + (wdw.abs() + e) * half_step(dtype) + tiny(dtype), "dw")
+    assert_within(db, dy.double().sum(0), dy.double().abs().sum(0) * (T + 8) * 2.0 ** -24, "dbias")

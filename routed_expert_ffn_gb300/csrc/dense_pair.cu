@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
     // j of B's block i column 128 i + 32 j + l (32 columns lie in one 128-row
     // block of W).  The MMA thread copies the blocks to TMEM in the order of its
     // products.  One hand-over for eight stages: it takes a release at cluster
-    // scope, which measured 0.85 us (a stage takes 0.25).
+    // scope, which measured 0.85 us (a stage takes 0.32).
     // Loads run one hand-over ahead.
     const int last = (a.p[0].N - 1) >> 7, nkb = a.p[0].nkb, total = a.tiles0;
     uint32_t nx[2][4], nw[2];

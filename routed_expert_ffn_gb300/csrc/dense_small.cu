@@ -7,10 +7,11 @@
 // bandwidth, so K is split over the CTAs of a cluster: each streams its own
 // part of K through a ring of TMA stages into its TMEM accumulator, and the
 // partial tiles are sent through distributed shared memory to the CTA that adds
-// them (each takes some of the rows of X) and added in rank order -- one kernel, no partials in HBM, and the same
-// bits every time.
+// them (each takes some of the rows of X), in rank order -- one kernel, no
+// partials in HBM, and the same bits every time.
 //
-// Gated tiles hold 64 gate and the same 64 up rows of W.  E4M3 operands are
+// Gated tiles hold 64 gate and the same 64 up rows of W.  A gradient's W (dX =
+// dY W) is read as it lies, MN-major.  E4M3 operands are
 // multiplied as they are (kind::mxf8f6f4, block-scaled): the exponent of each
 // 128 x 128 block of W and of each row of X and 128 columns goes to TMEM as
 // the MMA's scale factors.

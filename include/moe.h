@@ -574,7 +574,11 @@ size_t moe_norm_workspace_size(const moe_norm_desc_t *d);
  *                  out, both or neither NULL: per row and block of 128 elements
  *                  the least e with max|y| <= 448 * 2^e (at least -126; 0 for a
  *                  block of zeros), codes = y / 2^e rounded to nearest even;
- *                  the activation form of moe_quantize_fp8's weight blocks
+ *                  the activation form of moe_quantize_fp8's weight blocks.
+ *                  Here y is the fp32 value (s r) weight with r = rsqrtf(mean +
+ *                  eps) and the mean of s^2 rounded once (to 2^-27): a block whose
+ *                  maximum in exact arithmetic is within 2^-21 of 448 * 2^e (3 of 55
+ *                  million measured) may take the exponent on the other side
  * At least one of y and y_q.  Limits: 0 <= T <= 2^20, 8 <= H <= 16384,
  * H % 8 == 0 (MOE_ERR_UNSUPPORTED_SHAPE).  Needs no workspace.
  */

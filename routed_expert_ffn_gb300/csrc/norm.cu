@@ -202,9 +202,38 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// An fp32 sum with what its rounding left.
+struct Kept {
+  float hi, lo;
+};
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// The warp's sum of hi (kTwo: hi + lo), not negative, added in integers: in units of
+// 2^-25 of the largest lane's power of two, so that lanes within a factor of 4 of it
+// lose nothing and the others half a unit.  Two reductions in hardware; shuffles with
+// fp32 additions round at each of five steps (keeping what they round off took 74.4 us
+// of 8192 x 7168 where this takes 69.3).  Sums below 2^-101, whose units are not normal
+// numbers, infinities and NaN take the shuffles.
+template <bool kTwo>
+__device__ __forceinline__ Kept warp_sum_kept(Kept v) {
+  constexpr uint32_t kLeast = 26u << 23;
+  const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v.hi));
+  if (m - kLeast >= 0x7f800000u - kLeast) return {warp_sum(v.hi), 0.f};
+  const int e = 152 - (int)(m >> 23);
+  const int units = __float2int_rn(v.hi * pow2(e)) + (kTwo ? __float2int_rn(v.lo * pow2(e)) : 0);
+  const uint32_t s = __reduce_add_sync(0xffffffffu, (uint32_t)units);
+  const float h = __uint2float_rn(s);
+  return {h * pow2(-e), (float)(int)(s - __float2uint_rn(h)) * pow2(-e)};
+}
+// (hi + lo) / n rounded once; inv_n = 1 / n in fp32.
+__device__ __forceinline__ float mean_of(Kept s, float n, float inv_n) {
+  const float q = s.hi * inv_n;
+  return fabsf(q) < INFINITY ? fmaf(fmaf(-q, n, s.hi) + s.lo, inv_n, q) : q;
+}
+
 // The power-of-two exponent of a block of 8-bit values with absolute maximum
-// `amax`: the least s with amax <= 448 * 2^s (448 = 1.75 * 2^8, the largest
-// E4M3 value), at least -126; 0 for a block of zeros.
+// `amax` (of fp32 values): the least s with amax <= 448 * 2^s (448 = 1.75 * 2^8,
+// the largest E4M3 value), at least -126; 0 for a block of zeros.
 __device__ __forceinline__ int block_exp(float amax) {
   const uint32_t b = __float_as_uint(amax);
   if (b == 0u) return 0;
@@ -219,7 +248,7 @@ struct NormArgs {
   int8_t *scale;
   int64_t x_stride, r_stride, y_stride;
   int T, H, group;  // group: threads to a row
-  float eps;
+  float eps, inv_h;  // inv_h: 1 / H
 };
 
 // y of a chunk as E4M3 codes.  A block of 128 elements lies in 16 neighbouring
@@ -257,11 +286,21 @@ __device__ __forceinline__ void store_codes(const NormArgs &a, const pair_t (&y)
 }
 
 // This thread's chunks of a row, s = x + residual: residual_out and, once the
-// row's mean is known, y and its codes.  `part`: one float for each warp.
-template <typename T, int kV>
+// row's mean is known, y and its codes.  kOne: the row is the whole CTA's, else a
+// warp's.
+//
+// y = (s r) w in fp32, r = rsqrtf(mean + eps).  The exponent of a block is a step
+// of its largest y, and a mean off in its last bit can move y across that step
+// (1 of 55 million blocks of 8192 x 7168 inputs, with plain fp32 sums here).  So
+// the sum over threads keeps what its additions round off, the mean is rounded
+// once, and y has the bits that the same fp32 operations give anywhere: what is
+// left is the threads' own fp32 sums, a few squares each, whose errors are
+// independent and some 2^-28 of the whole.
+template <typename T, int kV, bool kOne>
 __device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)[kV],
                                          const Chunk<T> (&rr)[kV], const Chunk<T> (&rw)[kV],
-                                         int64_t row, int sub, int t, bool live, float *part) {
+                                         int64_t row, int t, bool live) {
+  __shared__ Kept part[kNormThreads / 32];
   pair_t s[kV][4], sq = make_pair(0.f, 0.f);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
@@ -276,13 +315,20 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)
     if (a.residual_out != nullptr && live)
       store_chunk(static_cast<T *>(a.residual_out) + row * a.r_stride, s[v], v, a.group, t, a.H);
   }
-  const float mine = warp_sum(lo_of(sq) + hi_of(sq));
-  const int warps = a.group >> 5;
-  if ((t & 31) == 0) part[sub * warps + (t >> 5)] = mine;
+  // A warp's row, too, by way of shared memory: with its sum left in registers 65536 x
+  // 256 takes 34.6 us, so 33.2 (31.8 with fp32 additions that keep nothing; of long
+  // coded rows 8192 x 7168 65.9 and 64.4, 5120 columns 45.7 and 47.3).
+  const int first = kOne ? 0 : threadIdx.y, lane = t & 31;
+  Kept sum = warp_sum_kept<false>({lo_of(sq) + hi_of(sq), 0.f});
+  if (lane == 0) part[first + (t >> 5)] = sum;
   __syncthreads();
-  float sum = 0.f;
-  for (int i = 0; i < warps; ++i) sum += part[sub * warps + i];
-  const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
+  if (kOne) {
+    sum = lane < a.group >> 5 ? part[lane] : Kept{0.f, 0.f};
+    sum = warp_sum_kept<true>(sum);
+  } else {
+    sum = part[first];
+  }
+  const float rstd = rsqrtf(mean_of(sum, (float)a.H, a.inv_h) + a.eps);
   const pair_t r2 = make_pair(rstd, rstd);
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
@@ -296,17 +342,17 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)
   }
 }
 
-// blockDim.x threads (whole warps) to a row, kOne: the CTA's only one.  Registers
-// are held down to 40 a thread of two chunks (64 of four): what hides the loads is
-// other CTAs' rows (8192 x 7168 78.4 us with 48, 69.9 with 40).  CTAs that stayed
-// and copied the next rows to shared memory meanwhile took 9.4 us for 1021 x 4104
-// (this 6.9), 44.9 for 8192 x 4096 (40.5), 17.0 for 16384 x 512 (15.1).
+// blockDim.x threads (whole warps) to a row, kOne: the CTA's only one, else a warp's.
+// Registers are held down to 40 a thread of two chunks (64 of four): what hides the
+// loads is other CTAs' rows (8192 x 7168 78.4 us with 48, 69.9 with 40).  CTAs that
+// stayed and copied the next rows to shared memory meanwhile took 9.4 us for 1021 x
+// 4104 (this 7.0), 44.9 for 8192 x 4096 (40.5), 17.0 for 16384 x 512 (15.0).
 template <typename T, int kV, bool kOne>
 __global__ void __launch_bounds__(kNormThreads, (kV == 2 ? 3 : 2) - (sizeof(T) == 4 ? 1 : 0))
     add_rms_norm_kernel(const NormArgs a) {
-  __shared__ float part[kNormThreads / 32];
-  const int sub = kOne ? 0 : threadIdx.y, t = threadIdx.x;
-  const int64_t row = kOne ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * blockDim.y + sub;
+  const int t = threadIdx.x;
+  const int64_t row =
+      kOne ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = kOne || row < a.T;
   const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
   const T *res = static_cast<const T *>(a.residual) + row * a.r_stride;
@@ -321,7 +367,7 @@ __global__ void __launch_bounds__(kNormThreads, (kV == 2 ? 3 : 2) - (sizeof(T) =
   for (int v = 0; v < kV; ++v)
     rw[v] = load_chunk(static_cast<const T *>(a.weight), v, a.group, t, a.H, true);
   pdl_launch_dependents();
-  norm_row<T, kV>(a, rx, rr, rw, row, sub, t, live, part);
+  norm_row<T, kV, kOne>(a, rx, rr, rw, row, t, live);
 }
 
 struct NormBwdArgs {
@@ -590,7 +636,7 @@ cudaError_t launch_add_rms_norm(const moe_norm_desc_t &d, const void *x, const v
                                 const void *weight, void *residual_out, void *y, uint8_t *q,
                                 int8_t *scale, cudaStream_t s) {
   NormArgs a = {x, residual, weight, residual_out, y, q, scale, d.x_stride, d.residual_stride,
-                d.y_stride, d.T, d.H, 0, d.eps};
+                d.y_stride, d.T, d.H, 0, d.eps, 1.0f / (float)d.H};
   switch (d.dtype) {
     case MOE_DTYPE_BF16: return norm_forward<__nv_bfloat16>(a, s);
     case MOE_DTYPE_FP16: return norm_forward<__half>(a, s);

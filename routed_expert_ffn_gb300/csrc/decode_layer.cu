@@ -1336,14 +1336,9 @@ cudaError_t launch_decode(const moe_layer_desc_t &d, const DecodeWeights &w,
   a.s2 = w.s2;
   a.s13_sh = w.s13s;
   a.s2_sh = w.s2s;
-  static bool configured[64] = {};
-  if (!configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(decode_layer_kernel<kFp8>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kDSmemBytes);
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
+  static std::atomic<bool> allowed[64];
+  const cudaError_t e = allow_smem(decode_layer_kernel<kFp8>, kDSmemBytes, allowed);
+  if (e != cudaSuccess) return e;
   return launch_cooperative(decode_layer_kernel<kFp8>, dim3(num_sms()),
                             dim3(kFp8 ? kDThreads8 : kDThreads), kDSmemBytes, s, maps, a);
 }

@@ -1045,15 +1045,15 @@ PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
 template <int kEpi, bool kAMn, bool kBMn, bool kE4m3, bool kMulti>
 cudaError_t resident_clusters(int (&out)[2]) {
   auto kern = dense_pair_kernel<kEpi, kAMn, kBMn, kE4m3, kMulti>;
-  static int resident[64][2] = {};
+  static std::atomic<int> resident[64][2];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (resident[dev][0] == 0) {
     constexpr size_t kBytes = smem_bytes<kEpi, kE4m3>();
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+    static std::atomic<bool> allowed[64];
+    cudaError_t e = allow_smem(kern, kBytes, allowed);
     if (e != cudaSuccess) return e;
-    for (int p = 2; p >= 1; --p) {
+    for (int p = 2; p >= 1; --p) {  // of one pair last: the one that says both are there
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -35,6 +35,10 @@ constexpr uint32_t kSmallSfCols = 8;     // scale-factor columns of a stage
 constexpr uint32_t kWBytes = 128 * 128;  // 128 rows of 128 bytes of K
 constexpr int kChunk = 64;               // the most rows of X a tile
 constexpr int kMaxSplit = 8;             // portable cluster size
+constexpr uint32_t kRingRoom = 102u * 1024u;  // of a CTA: two to an SM
+// and behind the ring up to 16 rows' partial tiles (more rows' fit in its place)
+constexpr size_t kMostSmem = 1024 + kRingRoom + 16 * 512;
+static_assert(2 * kChunk * 512 <= kRingRoom, "partial tiles in the ring's place");
 
 struct SmallMaps {
   CUtensorMap w, x;
@@ -465,8 +469,6 @@ template <bool kGated, bool kE4m3, bool kMn>
 cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
   auto kern = dense_small_kernel<kGated, kE4m3, kMn>;
   constexpr int kCols = kGated ? 64 : 128, kKb = kE4m3 ? 128 : 64;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   const SmallPlan plan = plan_small(g);
 
   SmallArgs a = {};
@@ -477,7 +479,7 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
   a.split = plan.split;
   const uint32_t stage = kWBytes + (uint32_t)a.n * 128u;
   // Two CTAs share an SM: one streams while the other adds and stores.
-  a.stages = std::min<int>(kMaxStages, (int)(102u * 1024u / stage));
+  a.stages = std::min<int>(kMaxStages, (int)(kRingRoom / stage));
   uint32_t cols = (uint32_t)a.n;
   a.sf_col = cols;
   if (kE4m3) cols += (uint32_t)a.stages * kSmallSfCols;
@@ -515,13 +517,10 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
       map_2d(&maps.x, g.dtype, CU_TENSOR_MAP_SWIZZLE_128B, g.a, g.M, g.K, g.lda, a.n, kKb);
   if (!ok) return cudaErrorInvalidValue;
 
-  static size_t configured[64] = {};
-  if (smem > configured[dev]) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = smem;
-  }
+  if (smem > kMostSmem) return cudaErrorInvalidValue;
+  static std::atomic<bool> allowed[64];
+  const cudaError_t e = allow_smem(kern, kMostSmem, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -885,13 +885,9 @@ cudaError_t launch_gemm(const moe_layer_desc_t &d, const void *w, const void *w_
 
   const size_t smem = C::smem_bytes(nseg);
   auto kern = expert_gemm_kernel<kGateUp>;
-  static size_t configured[64] = {};  // per device
-  if (smem > configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = smem;
-  }
+  static std::atomic<bool> allowed[64];
+  const cudaError_t e = allow_smem(kern, C::smem_bytes(kMaxE + 1), allowed);
+  if (e != cudaSuccess) return e;
   // one CTA per SM: the device-side plan decides the tiles (and split-K
   // pieces); CTAs without work leave at once
   const int grid = num_sms();

@@ -619,14 +619,9 @@ cudaError_t launch_expert_gemm_fp8(bool gate_up, const moe_layer_desc_t &d, cons
   if (!fp8_maps(key, &m)) return cudaErrorInvalidValue;
   const size_t smem = fp8_smem_bytes(nseg);
   auto kern = gate_up ? expert_gemm_fp8_kernel<true> : expert_gemm_fp8_kernel<false>;
-  static size_t configured[2][64] = {};
-  const int g = gate_up ? 1 : 0;
-  if (smem > configured[g][dev]) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    configured[g][dev] = smem;
-  }
+  static std::atomic<bool> allowed[2][64];
+  const cudaError_t e = allow_smem(kern, fp8_smem_bytes(kMaxE + 1), allowed[gate_up ? 1 : 0]);
+  if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(num_sms()), dim3(kFThreads), smem, s, m.ma, m.msh, m.mb, w_scale,
                     shared ? w_sh_scale : w_scale, plan, nseg, d.E, key.K, key.rows, Na, w_perm,
                     static_cast<uint16_t *>(out), status);

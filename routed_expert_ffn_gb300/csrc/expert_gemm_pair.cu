@@ -416,8 +416,8 @@ cudaError_t launch_expert_gemm_pair(bool gate_up, const CUtensorMap &a, const CU
   auto kern = gate_up ? expert_gemm_pair_kernel<true> : expert_gemm_pair_kernel<false>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  static size_t configured[2][64] = {};
-  static int clusters[2][64] = {};
+  static std::atomic<bool> allowed[2][64];
+  static std::atomic<int> clusters[2][64];
   const int g = gate_up ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -431,20 +431,15 @@ cudaError_t launch_expert_gemm_pair(bool gate_up, const CUtensorMap &a, const CU
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  if (smem > configured[g][dev]) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    configured[g][dev] = smem;
-    clusters[g][dev] = 0;
-  }
+  cudaError_t e = allow_smem(kern, pair_smem_bytes(kMaxE + 1), allowed[g]);
+  if (e != cudaSuccess) return e;
   if (clusters[g][dev] == 0) {
     // as many pairs as can be resident at once (one CTA per SM): the
     // persistent tile loop assumes every cluster runs from the start
     cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2));
     cfg.numAttrs = 1;
     int n = 0;
-    cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     clusters[g][dev] = std::min(n, num_sms() / 2);

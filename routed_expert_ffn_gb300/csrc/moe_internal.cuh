@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/moe.h"
@@ -354,6 +355,21 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// Opts a kernel in to `most` bytes of dynamic shared memory, the most that any of its
+// launches takes: the attribute is the kernel's, not a launch's, and setting it lowers
+// it, too, so with each call's own size a host thread could take away what another's
+// launch needs.  `done`: the kernel's own record, per device.
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kern)(KArgs...), size_t most, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {

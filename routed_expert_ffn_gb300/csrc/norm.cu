@@ -544,24 +544,13 @@ __global__ void __launch_bounds__(1024)
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
-// Opts a kernel in to `bytes` of dynamic shared memory; `allowed`: the kernel's
-// own record of what it has, per device.
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes, size_t (&allowed)[64]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (bytes <= allowed[dev]) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) allowed[dev] = bytes;
-  return e;
-}
+constexpr size_t kRingRoom = 200 * 1024;
 
 // Rows of a ring: up to four where `per_sm` CTAs of an SM have room for at least
 // two, else two of a CTA that has the SM to itself, or one.
 int ring_depth(size_t row_bytes, int per_sm) {
-  const int d = (int)((size_t)(200 / per_sm * 1024) / row_bytes);
-  return d >= 2 ? std::min(d, 4) : (2 * row_bytes <= 200 * 1024 ? 2 : 1);
+  const int d = (int)(kRingRoom / per_sm / row_bytes);
+  return d >= 2 ? std::min(d, 4) : (2 * row_bytes <= kRingRoom ? 2 : 1);
 }
 
 template <typename T>
@@ -595,8 +584,9 @@ void norm_bwd_shape(int T, int H, int sms, int *v, int *group, int *rows, int *p
 template <typename T, int kV>
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, dim3 grid, dim3 block, size_t smem,
                             cudaStream_t s) {
-  static size_t allowed[64] = {};
-  const cudaError_t e = allow_smem(add_rms_norm_bwd_kernel<T, kV>, smem, allowed);
+  if (smem > kRingRoom) return cudaErrorInvalidValue;
+  static std::atomic<bool> allowed[64];
+  const cudaError_t e = allow_smem(add_rms_norm_bwd_kernel<T, kV>, kRingRoom, allowed);
   return e != cudaSuccess
              ? e
              : launch_pdl(add_rms_norm_bwd_kernel<T, kV>, grid, block, smem, s, a);

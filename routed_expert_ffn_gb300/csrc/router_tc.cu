@@ -280,16 +280,9 @@ cudaError_t launch_router_logits(const __nv_bfloat16 *x, const float *w_router, 
     const cuuint32_t box128[2] = {(cuuint32_t)kBK, (cuuint32_t)kRBN};
     if (!encode_bf16_map(&mx128, x, 2, dims, strides, box128)) return cudaErrorInvalidValue;
   }
-  static bool configured[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!configured[dev]) {
-    e = cudaFuncSetAttribute(router_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kRSmem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
+  static std::atomic<bool> allowed[64];
+  e = allow_smem(router_tc_kernel, kRSmem, allowed);
+  if (e != cudaSuccess) return e;
   const int nkb = H / kBK;
   const int per = (nkb + splits - 1) / splits;
   dim3 grid((E + kBM - 1) / kBM, (T + kRBN - 1) / kRBN, splits);

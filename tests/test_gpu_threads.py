@@ -1,5 +1,8 @@
 """Calls from other host threads than the first (needs a GB300)."""
 
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -85,3 +88,12 @@ def test_a_layer_from_a_new_thread():
         torch.cuda.synchronize()
         out.append((y, ws, tensors, x))  # (kept: the second round has buffers of its own)
     assert torch.equal(out[0][0], out[1][0])
+
+
+def test_first_calls_of_every_kernel_from_many_threads():
+    """With sizes that take different amounts of shared memory; in a process of its own, because
+    only a kernel's first calls set how much it may have."""
+    worker = os.path.join(os.path.dirname(os.path.abspath(__file__)), "threads_worker.py")
+    p = subprocess.run([sys.executable, worker], capture_output=True, text=True, timeout=600)
+    assert p.returncode == 0, (p.stdout + p.stderr)[-3000:]
+    assert p.stdout.strip().endswith("ok")

@@ -318,15 +318,15 @@ __device__ __forceinline__ void norm_row(const NormArgs &a, const Chunk<T> (&rx)
   // A warp's row, too, by way of shared memory: with its sum left in registers 65536 x
   // 256 takes 34.6 us, so 33.2 (31.8 with fp32 additions that keep nothing; of long
   // coded rows 8192 x 7168 65.9 and 64.4, 5120 columns 45.7 and 47.3).
-  const int first = kOne ? 0 : threadIdx.y, lane = t & 31;
+  const int mine = kOne ? t >> 5 : threadIdx.y, lane = t & 31;
   Kept sum = warp_sum_kept<false>({lo_of(sq) + hi_of(sq), 0.f});
-  if (lane == 0) part[first + (t >> 5)] = sum;
+  if (lane == 0) part[mine] = sum;
   __syncthreads();
   if (kOne) {
     sum = lane < a.group >> 5 ? part[lane] : Kept{0.f, 0.f};
     sum = warp_sum_kept<true>(sum);
   } else {
-    sum = part[first];
+    sum = part[mine];
   }
   const float rstd = rsqrtf(mean_of(sum, (float)a.H, a.inv_h) + a.eps);
   const pair_t r2 = make_pair(rstd, rstd);

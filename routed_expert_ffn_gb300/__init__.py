@@ -411,6 +411,8 @@ def moe_layer_forward_fp8(d: LayerDesc, w: LayerWeightsFp8, x, y, ws, stream=Non
 
 # ---------------------------------------------- dense operators --
 # Rows may be strided (the descriptor's *_stride, in elements); everything else is contiguous.
+# Tensors of another element type, or smaller than the descriptor says, are a ValueError (larger
+# ones are not: a buffer for more rows may serve fewer); plain addresses are taken as they are.
 
 def dtype_of(t) -> int:
     """The MOE_DTYPE_* of a tensor (uint8 counts as E4M3 codes)."""
@@ -423,17 +425,59 @@ def dtype_of(t) -> int:
         raise ValueError(f"unsupported element type {name}") from None
 
 
-def _rows(t, stride: int, cols: int) -> Optional[int]:
-    """The pointer of a [T, cols] tensor whose rows are ``stride`` elements apart (0: cols)."""
+_EXPONENTS = -1  # int8 block exponents, beside the MOE_DTYPE_* in _ACCEPTED
+
+
+class _Accepted(dict):
+    """The torch types that hold MOE_DTYPE_* elements (E4M3 codes: float8_e4m3fn or any byte).
+    Codes that are none, which the library refuses, go with every type."""
+
+    def __missing__(self, code):
+        import torch
+        every = [t for t in vars(torch).values() if isinstance(t, torch.dtype)]
+        self[code] = frozenset({
+            MOE_DTYPE_BF16: [torch.bfloat16], MOE_DTYPE_FP16: [torch.float16],
+            MOE_DTYPE_FP32: [torch.float32], _EXPONENTS: [torch.int8],
+            MOE_DTYPE_E4M3: [torch.float8_e4m3fn, torch.uint8, torch.int8]}.get(code, every))
+        return self[code]
+
+
+_ACCEPTED = _Accepted()
+
+
+def _rows(t, stride: int, cols: int, rows: int = 0, code: int = None) -> Optional[int]:
+    """The pointer of a [rows, cols] tensor (or one of more rows) of MOE_DTYPE_* ``code`` whose
+    rows are ``stride`` elements apart (0: cols)."""
     if t is None or isinstance(t, int):
         return t
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    s = t.stride()
-    if len(s) == 2 and t.size(1) == cols and (s[0] == (stride or cols) or t.size(0) <= 1) and (
-            s[1] == 1 or cols == 1):
-        return t.data_ptr()
-    raise ValueError("expected a [T, cols] tensor with rows at the descriptor's stride")
+    n, s = t.shape, t.stride()
+    if not (len(n) == 2 and n[1] == cols and (s[0] == (stride or cols) or n[0] <= 1) and (
+            s[1] == 1 or cols == 1)):
+        raise ValueError("expected a [T, cols] tensor with rows at the descriptor's stride")
+    if n[0] < rows:
+        raise ValueError(f"expected {rows} rows, got {n[0]}")
+    if t.dtype not in _ACCEPTED[code]:
+        raise ValueError(f"{t.dtype} is not the descriptor's element type")
+    return t.data_ptr()
+
+
+def _flat(t, count: int, code: int) -> Optional[int]:
+    """The pointer of a contiguous tensor of at least ``count`` elements of MOE_DTYPE_* ``code``."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.numel() < count:
+        raise ValueError(f"expected {count} elements, got {t.numel()}")
+    if t.dtype not in _ACCEPTED[code]:
+        raise ValueError(f"{t.dtype} is not the element type of this argument")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
 
 
 def norm_desc(T: int, H: int, dtype: int, eps: float = 1e-6, x_stride: int = 0,
@@ -449,20 +493,23 @@ def moe_add_rms_norm(d: NormDesc, x, residual, weight, residual_out, y, y_q=None
                      stream=None):
     """s = x + residual; residual_out = s; y (and / or E4M3 codes y_q with exponents
     scale_exp) = weight * s / sqrt(mean(s^2) + eps)."""
+    T, H, dt, rs = d.T, d.H, d.dtype, d.residual_stride
     _check("moe_add_rms_norm", library().moe_add_rms_norm(
-        ctypes.byref(d), _rows(x, d.x_stride, d.H), _rows(residual, d.residual_stride, d.H),
-        _ptr(weight), _rows(residual_out, d.residual_stride, d.H), _rows(y, d.y_stride, d.H),
-        _ptr(y_q), _ptr(scale_exp), _stream(stream)))
+        ctypes.byref(d), _rows(x, d.x_stride, H, T, dt), _rows(residual, rs, H, T, dt),
+        _flat(weight, H, dt), _rows(residual_out, rs, H, T, dt), _rows(y, d.y_stride, H, T, dt),
+        _flat(y_q, T * H, MOE_DTYPE_E4M3), _flat(scale_exp, T * _blocks(H), _EXPONENTS),
+        _stream(stream)))
 
 
 def moe_add_rms_norm_backward(d: NormDesc, dy, dresidual, sum, weight, dx, dweight, ws,
                               stream=None):
     """dx (of x and of residual) and dweight (fp32) of moe_add_rms_norm; ``sum`` is its
     residual_out, ``dresidual`` the gradient of that (or None)."""
+    T, H, dt, rs = d.T, d.H, d.dtype, d.residual_stride
     _check("moe_add_rms_norm_backward", library().moe_add_rms_norm_backward(
-        ctypes.byref(d), _rows(dy, d.y_stride, d.H), _rows(dresidual, d.residual_stride, d.H),
-        _rows(sum, d.residual_stride, d.H), _ptr(weight), _rows(dx, d.x_stride, d.H),
-        _ptr(dweight), _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(d), _rows(dy, d.y_stride, H, T, dt), _rows(dresidual, rs, H, T, dt),
+        _rows(sum, rs, H, T, dt), _flat(weight, H, dt), _rows(dx, d.x_stride, H, T, dt),
+        _flat(dweight, H, MOE_DTYPE_FP32), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def linear_desc(T: int, N: int, K: int, dtype: int, act="none", out_dtype: int = None,
@@ -483,10 +530,13 @@ def moe_linear(d: LinearDesc, x, w, bias, residual, y, ws, preact=None, x_scale=
                w_scale=None, stream=None):
     """y = act(x w^T + bias) + residual (``preact``: x w^T + bias in fp32 as well); E4M3 codes
     come with their block exponents ``x_scale`` and ``w_scale``."""
+    T, N, K, dt, out = d.T, d.N, d.K, d.dtype, d.out_dtype
     _check("moe_linear", library().moe_linear(
-        ctypes.byref(d), _rows(x, d.x_stride, d.K), _ptr(x_scale), _ptr(w), _ptr(w_scale),
-        _ptr(bias), _rows(residual, d.residual_stride, d.N), _ptr(preact),
-        _rows(y, d.y_stride, d.N), _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(d), _rows(x, d.x_stride, K, T, dt),
+        _flat(x_scale, T * _blocks(K), _EXPONENTS), _flat(w, N * K, dt),
+        _flat(w_scale, _blocks(N) * _blocks(K), _EXPONENTS), _flat(bias, N, out),
+        _rows(residual, d.residual_stride, N, T, out), _flat(preact, T * N, MOE_DTYPE_FP32),
+        _rows(y, d.y_stride, N, T, out), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def _grad_dtype(d, *grads) -> int:
@@ -500,10 +550,14 @@ def _grad_dtype(d, *grads) -> int:
 def moe_linear_backward(d: LinearDesc, dy, x, w, preact, dx, dw, dbias, ws,
                         accumulate: bool = False, stream=None):
     """dx, dw (in the type of x or fp32) and dbias (fp32) of moe_linear; any of them may be None."""
+    T, N, K, dt = d.T, d.N, d.K, d.dtype
+    dw_dtype = _grad_dtype(d, dw)
     _check("moe_linear_backward", library().moe_linear_backward(
-        ctypes.byref(d), _rows(dy, d.y_stride, d.N), _rows(x, d.x_stride, d.K), _ptr(w),
-        _ptr(preact) if d.act != MOE_ACT_NONE else None, _rows(dx, d.x_stride, d.K), _ptr(dw),
-        _grad_dtype(d, dw), _ptr(dbias), 1 if accumulate else 0, _ptr(ws), _nbytes(ws),
+        ctypes.byref(d), _rows(dy, d.y_stride, N, T, dt), _rows(x, d.x_stride, K, T, dt),
+        _flat(w, N * K, dt),
+        _flat(preact, T * N, MOE_DTYPE_FP32) if d.act != MOE_ACT_NONE else None,
+        _rows(dx, d.x_stride, K, T, dt), _flat(dw, N * K, dw_dtype), dw_dtype,
+        _flat(dbias, N, MOE_DTYPE_FP32), 1 if accumulate else 0, _ptr(ws), _nbytes(ws),
         _stream(stream)))
 
 
@@ -518,18 +572,23 @@ def moe_gated_ffn_workspace_size(d: FfnDesc) -> int:
 def moe_gated_ffn(d: FfnDesc, x, w13, w2, residual, saved, y, ws, stream=None):
     """y = (SiLU(x Wg^T) * (x Wu^T)) W2^T + residual; ``saved`` ([T,2I] fp32 or None) is what
     moe_gated_ffn_backward needs of it."""
+    TH, HI, dt = d.T * d.H, d.H * d.I, d.dtype
     _check("moe_gated_ffn", library().moe_gated_ffn(
-        ctypes.byref(d), _ptr(x), _ptr(w13), _ptr(w2), _ptr(residual), _ptr(saved), _ptr(y),
+        ctypes.byref(d), _flat(x, TH, dt), _flat(w13, 2 * HI, dt), _flat(w2, HI, dt),
+        _flat(residual, TH, dt), _flat(saved, 2 * d.T * d.I, MOE_DTYPE_FP32), _flat(y, TH, dt),
         _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_gated_ffn_backward(d: FfnDesc, dy, x, w13, w2, saved, dx, dw13, dw2, ws,
                            accumulate: bool = False, stream=None):
     """dx, dw13 and dw2 (in the type of x, or both in fp32) of moe_gated_ffn; any may be None."""
+    TH, HI, dt = d.T * d.H, d.H * d.I, d.dtype
+    dw_dtype = _grad_dtype(d, dw13, dw2)
     _check("moe_gated_ffn_backward", library().moe_gated_ffn_backward(
-        ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(w13), _ptr(w2), _ptr(saved), _ptr(dx), _ptr(dw13),
-        _ptr(dw2), _grad_dtype(d, dw13, dw2), 1 if accumulate else 0, _ptr(ws), _nbytes(ws),
-        _stream(stream)))
+        ctypes.byref(d), _flat(dy, TH, dt), _flat(x, TH, dt), _flat(w13, 2 * HI, dt),
+        _flat(w2, HI, dt), _flat(saved, 2 * d.T * d.I, MOE_DTYPE_FP32), _flat(dx, TH, dt),
+        _flat(dw13, 2 * HI, dw_dtype), _flat(dw2, HI, dw_dtype), dw_dtype, 1 if accumulate else 0,
+        _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def workspace_view(ws, layout: Dict[str, int], name: str, dtype, shape):

@@ -536,6 +536,9 @@ moe_status_t moe_reshard_tp_to_ep_unpack(int32_t E_local, int32_t H, int32_t I, 
  *   rows come out as zero (or unchanged when accumulating).
  * - Strides are in elements between consecutive rows, multiples of 8 (16 for
  *   MOE_DTYPE_E4M3 rows); 0 means dense rows.
+ * - Outputs share no memory with inputs or with each other but where an argument
+ *   says so.  Equal addresses that would be written while they are read are
+ *   MOE_ERR_INVALID_ARG; other overlaps are not looked for.
  * - Workspaces: one buffer of the operator's *_workspace_size(desc) bytes,
  *   256-byte aligned, initialised once with moe_workspace_init(); read its
  *   status word with moe_get_device_status(): bit 8 (MOE_ERR_TIMEOUT) is set

@@ -3,6 +3,8 @@
 // argument are in include/moe.h.
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "dense.cuh"
 
 namespace moe {
@@ -15,6 +17,14 @@ moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE
 moe_status_t check_ws(const void *ws, size_t ws_bytes, size_t need) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
   return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
+// Whether `out` is at the address of one of `others` that the call still reads, or
+// writes too (null: no argument).
+bool lies_on(const void *out, std::initializer_list<const void *> others) {
+  for (const void *p : others)
+    if (out != nullptr && out == p) return true;
+  return false;
 }
 
 // A row stride in elements: 0 (dense) becomes `cols`; otherwise at least
@@ -194,6 +204,8 @@ moe_status_t moe_add_rms_norm(const moe_norm_desc_t *in, const void *x, const vo
   // in place means row for row
   if (residual_out == x && d.residual_stride != d.x_stride) return MOE_ERR_INVALID_ARG;
   if (y == x && d.y_stride != d.x_stride) return MOE_ERR_INVALID_ARG;
+  if (y != nullptr && y == residual && d.y_stride != d.residual_stride) return MOE_ERR_INVALID_ARG;
+  if (lies_on(y_q, {x, residual, residual_out, y})) return MOE_ERR_INVALID_ARG;
   if ((st = check_device()) != MOE_OK) return st;
   return cuda_status(launch_add_rms_norm(d, x, residual, weight, residual_out, y,
                                          static_cast<uint8_t *>(y_q), scale_exp,
@@ -247,7 +259,10 @@ moe_status_t moe_linear(const moe_linear_desc_t *in, const void *x, const int8_t
   if ((x_scale != nullptr) != e4m3 || (w_scale != nullptr) != e4m3) return MOE_ERR_INVALID_ARG;
   if (e4m3 && preact != nullptr) return MOE_ERR_INVALID_ARG;
   if (residual == y && d.residual_stride != d.y_stride) return MOE_ERR_INVALID_ARG;
-  if (y == x || y == w) return MOE_ERR_INVALID_ARG;
+  if (y == x || y == w || lies_on(preact, {x, w, bias, y})) return MOE_ERR_INVALID_ARG;
+  if (preact != nullptr && preact == residual &&
+      (d.out_dtype != MOE_DTYPE_FP32 || d.residual_stride != d.N))
+    return MOE_ERR_INVALID_ARG;
   if ((st = check_device()) != MOE_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   DenseGemm g = product(d.T, d.N, d.K, d.dtype, x, d.x_stride, false, w, d.K, false, y, d.y_stride,
@@ -281,6 +296,11 @@ moe_status_t moe_linear_backward(const moe_linear_desc_t *in, const void *dy, co
       return MOE_ERR_INVALID_ARG;
     if ((dx != nullptr && !ok_ptr(w)) || (dw != nullptr && !ok_ptr(x))) return MOE_ERR_INVALID_ARG;
     if (dx != nullptr && (dx == dy || dx == x || dx == w)) return MOE_ERR_INVALID_ARG;
+    // dx and dw are of one launch, after that of dbias; with an activation neither reads dy
+    const void *w_read = dx != nullptr ? w : nullptr, *x_read = dw != nullptr ? x : nullptr;
+    if (lies_on(dw, {x, w_read, dx, act ? nullptr : dy}) ||
+        lies_on(dbias, {dy, preact, x_read, w_read, dx, dw}))
+      return MOE_ERR_INVALID_ARG;
   }
   if ((st = check_device()) != MOE_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
@@ -325,6 +345,7 @@ moe_status_t moe_gated_ffn(const moe_ffn_desc_t *d, const void *x, const void *w
       !ok_ptr(y))
     return MOE_ERR_INVALID_ARG;
   if (y == x || y == w13 || y == w2) return MOE_ERR_INVALID_ARG;
+  if (lies_on(saved, {x, w13, w2, residual, y})) return MOE_ERR_INVALID_ARG;
   if ((st = check_device()) != MOE_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   DenseGemm up = product(d->T, d->I, d->H, d->dtype, x, d->H, false, w13, d->H, false,
@@ -356,6 +377,11 @@ moe_status_t moe_gated_ffn_backward(const moe_ffn_desc_t *d, const void *dy, con
     if ((dx != nullptr && !ok_ptr(w13)) || (dw13 != nullptr && !ok_ptr(x)))
       return MOE_ERR_INVALID_ARG;
     if (dx != nullptr && (dx == dy || dx == x || dx == w13 || dx == w2)) return MOE_ERR_INVALID_ARG;
+    // the three are of one launch, which reads neither w2 nor saved
+    const void *w13_read = dx != nullptr ? w13 : nullptr;
+    if (lies_on(dw13, {x, w13_read, dw2 != nullptr ? dy : nullptr, dx, dw2}) ||
+        lies_on(dw2, {dy, w13_read, dw13 != nullptr ? x : nullptr, dx}))
+      return MOE_ERR_INVALID_ARG;
   }
   if ((st = check_device()) != MOE_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;

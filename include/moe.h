@@ -644,6 +644,9 @@ size_t moe_linear_workspace_size(const moe_linear_desc_t *d);
  *             moe_linear_backward needs where act is not MOE_ACT_NONE
  *             (not with MOE_DTYPE_E4M3)
  *   y         [T,N] out
+ * Activations are good to a few fp32 steps of their value (and of their
+ * exponential's argument) where y is fp32, to 2^-18 of z before a rounding to
+ * 16 bits.
  * Limits: 0 <= T <= 2^20, 8 <= N, K <= 2^18, both multiples of 8 (K of 16
  * for MOE_DTYPE_E4M3).
  */
@@ -656,7 +659,8 @@ moe_status_t moe_linear(const moe_linear_desc_t *d, const void *x, const int8_t 
  * moe_linear_backward -- with z = preact and dz = dy act'(z):
  *   dx = dz w,   dw = dz^T x,   dbias = sum over rows of dz
  * (the gradient of residual is dy itself).  dz is rounded once to the 16-bit
- * type, the tensor cores' operand; dbias sums it unrounded.
+ * type, the tensor cores' operand; dbias sums it unrounded (slopes are good to
+ * 2^-18).
  *   dy      [T,N] in, of type dtype, rows y_stride apart
  *   preact  [T,N] fp32 in; NULL where act is MOE_ACT_NONE
  *   dx      [T,K] out, of type dtype, rows x_stride apart, or NULL

@@ -79,36 +79,47 @@ __device__ __forceinline__ float2 unpack16(int dtype, uint32_t w) {
 constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluC1 = 0.044715f;
 
-// the approximate division: 2 ulp, and 0 where 1 + e^-z overflows
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// The approximate division: 2 ulp, and 0 where 1 + e^-z overflows.  Unless kExact, the
+// approximate exponential too, whose error grows with |z| (2^-22 of the result at 0,
+// 2^-19 at 16): enough for results that are rounded to 16 bits next.
+template <bool kExact = false>
+__device__ __forceinline__ float sigmoid(float z) {
+  return __fdividef(1.0f, 1.0f + (kExact ? expf(-z) : __expf(-z)));
+}
 
+// kExact: to a few fp32 steps for any z, for fp32 results.  2048 x 8192 x 1024 with
+// SiLU takes 36.4 us so and 28.0 without, with GELU 78.7 and 44.8.
+template <bool kExact>
 __device__ __forceinline__ float activate(int act, float z) {
   switch (act) {
     // comparisons that let a NaN through
     case MOE_ACT_RELU: return z < 0.f ? 0.f : z;
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case MOE_ACT_GELU:
+      // 1 + erf v = erfc(-v), where nothing cancels far below zero
+      return 0.5f * z *
+             (kExact ? erfcf(z * -0.7071067811865476f) : 1.0f + erff(z * 0.7071067811865476f));
     case MOE_ACT_GELU_TANH: {
       // 1/2 (1 + tanh v) = sigmoid(2 v)
-      return z * sigmoid(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
+      return z * sigmoid<kExact>(2.0f * kGeluC0 * (z + kGeluC1 * z * z * z));
     }
-    case MOE_ACT_SILU: return z * sigmoid(z);
+    case MOE_ACT_SILU: return z * sigmoid<kExact>(z);
     default: return z;
   }
 }
 
 // All of an array, the choice made once.
-template <int kAct, int kN>
+template <bool kExact, int kAct, int kN>
 __device__ __forceinline__ void activate_as(float (&f)[kN]) {
 #pragma unroll
-  for (int i = 0; i < kN; ++i) f[i] = activate(kAct, f[i]);
+  for (int i = 0; i < kN; ++i) f[i] = activate<kExact>(kAct, f[i]);
 }
-template <int kN>
+template <bool kExact, int kN>
 __device__ __forceinline__ void activate_all(int act, float (&f)[kN]) {
   switch (act) {
-    case MOE_ACT_RELU: return activate_as<MOE_ACT_RELU>(f);
-    case MOE_ACT_GELU: return activate_as<MOE_ACT_GELU>(f);
-    case MOE_ACT_GELU_TANH: return activate_as<MOE_ACT_GELU_TANH>(f);
-    case MOE_ACT_SILU: return activate_as<MOE_ACT_SILU>(f);
+    case MOE_ACT_RELU: return activate_as<kExact, MOE_ACT_RELU>(f);
+    case MOE_ACT_GELU: return activate_as<kExact, MOE_ACT_GELU>(f);
+    case MOE_ACT_GELU_TANH: return activate_as<kExact, MOE_ACT_GELU_TANH>(f);
+    case MOE_ACT_SILU: return activate_as<kExact, MOE_ACT_SILU>(f);
     default: return;
   }
 }

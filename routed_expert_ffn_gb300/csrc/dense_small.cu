@@ -415,7 +415,10 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < 8; ++i) f[i] = f[i] * sigmoid(f[i]) * up[i];
       } else {
         if (a.bias != nullptr) b.add_to(f, a.out_dtype);
-        activate_all(a.act, f);
+        if (a.out_dtype == MOE_DTYPE_FP32)
+          activate_all<true>(a.act, f);
+        else
+          activate_all<false>(a.act, f);
       }
       if (a.residual != nullptr) r.add_to(f, a.out_dtype);
       store8(f, a.d, (int64_t)(t0 + first + t) * a.ldd + c, a.out_dtype);

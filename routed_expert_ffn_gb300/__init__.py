@@ -235,7 +235,9 @@ def alloc_workspace(d, device="cuda"):
     """A zero-initialised workspace tensor (uint8) for the calls made with ``d``: a layer's
     descriptor (moe_workspace_size(d) bytes) or a dense operator's (its own *_workspace_size)."""
     import torch
-    fn = _WORKSPACE_SIZE[type(d)]
+    fn = next((f for c, f in _WORKSPACE_SIZE.items() if isinstance(d, c)), None)
+    if fn is None:
+        raise TypeError(f"{type(d).__name__} is no descriptor")
     n = int(getattr(library(), fn)(ctypes.byref(d)))
     if n == 0:
         raise MoeError(fn, MOE_ERR_UNSUPPORTED_SHAPE)

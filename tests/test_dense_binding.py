@@ -119,3 +119,13 @@ def test_a_row_less_or_another_type_is_refused(lib, name, arg):
         call(fn, desc(), a)
     assert not lib.calls
 
+
+
+def test_workspace_of_a_derived_descriptor():
+    """A program's own class over a descriptor is one, as it was before the dense operators."""
+    class Mine(moe.LayerDesc):
+        pass
+    with pytest.raises(moe.MoeError):  # a bad shape, not an unknown class
+        moe.alloc_workspace(Mine(-1, 256, 8, 2, 128, moe.MOE_GATE_SOFTMAX_TOPK_RENORM, 0))
+    with pytest.raises(TypeError):
+        moe.alloc_workspace(object())

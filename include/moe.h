@@ -625,6 +625,22 @@ typedef struct {
   int64_t y_stride;         /* rows of y (and dy) */
 } moe_linear_desc_t;
 
+/* The kernels of moe_linear: one reads W once for each (up to 64) rows of x, one
+ * takes tiles of 256 rows on pairs of SMs. */
+enum { MOE_LINEAR_FEW_ROWS = 0, MOE_LINEAR_TILES = 1 };
+typedef struct {
+  int32_t kernel;                /* MOE_LINEAR_* */
+  int32_t tile_rows, tile_cols;  /* rows of x and columns of y of a tile */
+  int32_t split;                 /* parts of K, each worked on apart */
+} moe_linear_plan_t;
+
+/*
+ * moe_linear_plan -- how moe_linear runs a descriptor on the current device (with
+ * or without a preact), by its estimated times.  Launches nothing; T >= 1.
+ */
+moe_status_t moe_linear_plan(const moe_linear_desc_t *d, int32_t with_preact,
+                             moe_linear_plan_t *plan);
+
 /* Bytes of the workspace of both calls; 0 for an invalid descriptor. */
 size_t moe_linear_workspace_size(const moe_linear_desc_t *d);
 

@@ -102,6 +102,15 @@ class LinearDesc(ctypes.Structure):
                 ("y_stride", ctypes.c_int64)]
 
 
+MOE_LINEAR_FEW_ROWS = 0
+MOE_LINEAR_TILES = 1
+
+
+class LinearPlan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("tile_rows", ctypes.c_int32),
+                ("tile_cols", ctypes.c_int32), ("split", ctypes.c_int32)]
+
+
 class FfnDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
@@ -145,6 +154,7 @@ def library() -> ctypes.CDLL:
         "moe_add_rms_norm": ([ctypes.POINTER(NormDesc), P, P, P, P, P, P, P, P], I32),
         "moe_add_rms_norm_backward": ([ctypes.POINTER(NormDesc), P, P, P, P, P, P, P, S, P], I32),
         "moe_linear_workspace_size": ([ctypes.POINTER(LinearDesc)], S),
+        "moe_linear_plan": ([ctypes.POINTER(LinearDesc), I32, ctypes.POINTER(LinearPlan)], I32),
         "moe_linear": ([ctypes.POINTER(LinearDesc), P, P, P, P, P, P, P, P, P, S, P], I32),
         "moe_linear_backward": ([ctypes.POINTER(LinearDesc), P, P, P, P, P, P, I32, P, I32, P, S,
                                  P], I32),
@@ -526,6 +536,14 @@ def linear_desc(T: int, N: int, K: int, dtype: int, act="none", out_dtype: int =
 
 def moe_linear_workspace_size(d: LinearDesc) -> int:
     return int(library().moe_linear_workspace_size(ctypes.byref(d)))
+
+
+def moe_linear_plan(d: LinearDesc, with_preact: bool = False) -> LinearPlan:
+    """How moe_linear runs ``d`` on the current device (kernel, tile, parts of K)."""
+    plan = LinearPlan()
+    _check("moe_linear_plan", library().moe_linear_plan(ctypes.byref(d), 1 if with_preact else 0,
+                                                        ctypes.byref(plan)))
+    return plan
 
 
 def moe_linear(d: LinearDesc, x, w, bias, residual, y, ws, preact=None, x_scale=None,

@@ -135,11 +135,12 @@ DenseGemm product(int M, int N, int K, int dtype, const void *a, int64_t lda, bo
 // tiled one wants 256 rows for each 64 to 256 columns.  4096 x 4096 (us, few
 // rows against tiled): 32 rows 9.6 and 14.1, 128 rows 14.9 and 14.8, 192 rows
 // 19.0 and 14.7.  preact and saved are stored by the tiled kernel only.
+bool by_few_rows(const DenseGemm &g) {
+  return g.M <= kSmallRows && g.preact == nullptr && g.saved == nullptr &&
+         dense_small_us(g) <= dense_pair_us(g);
+}
 cudaError_t forward(const DenseGemm &g, cudaStream_t s) {
-  if (g.M <= kSmallRows && g.preact == nullptr && g.saved == nullptr &&
-      dense_small_us(g) <= dense_pair_us(g))
-    return launch_dense_small(g, s);
-  return launch_dense_pair(g, s);
+  return by_few_rows(g) ? launch_dense_small(g, s) : launch_dense_pair(g, s);
 }
 
 constexpr int kGradSmallRows = 64;
@@ -240,6 +241,28 @@ moe_status_t moe_add_rms_norm_backward(const moe_norm_desc_t *in, const void *dy
 size_t moe_linear_workspace_size(const moe_linear_desc_t *in) {
   moe_linear_desc_t d;
   return linear_desc(in, &d) == MOE_OK ? linear_ws(d).total : 0;
+}
+
+moe_status_t moe_linear_plan(const moe_linear_desc_t *in, int32_t with_preact,
+                             moe_linear_plan_t *plan) {
+  moe_linear_desc_t d;
+  moe_status_t st = linear_desc(in, &d);
+  if (st != MOE_OK) return st;
+  if (plan == nullptr || d.T == 0) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device()) != MOE_OK) return st;
+  DenseGemm g = product(d.T, d.N, d.K, d.dtype, nullptr, d.x_stride, false, nullptr, d.K, false,
+                        nullptr, d.y_stride, d.out_dtype, nullptr);
+  g.act = d.act;
+  float preact;
+  if (with_preact) g.preact = &preact;
+  const bool few = by_few_rows(g);
+  const DensePlan p = few ? dense_small_plan(g) : dense_pair_plan(g);
+  if (p.us == 0.f) return MOE_ERR_CUDA;
+  plan->kernel = few ? MOE_LINEAR_FEW_ROWS : MOE_LINEAR_TILES;
+  plan->tile_rows = p.rows;
+  plan->tile_cols = p.cols;
+  plan->split = p.split;
+  return MOE_OK;
 }
 
 moe_status_t moe_linear(const moe_linear_desc_t *in, const void *x, const int8_t *x_scale,

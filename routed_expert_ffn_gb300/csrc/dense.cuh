@@ -46,9 +46,16 @@ cudaError_t launch_dense_multi(const DenseGemm *g, int n, cudaStream_t s);
 // preact or saved, at most kSmallRows rows.
 constexpr int kSmallRows = 1024;
 cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s);
-// What each is estimated to take, in us (0 if it cannot be told).
-float dense_pair_us(const DenseGemm &g);
-float dense_small_us(const DenseGemm &g);
+// Tiles of rows x cols, K split in `split`, and what that is estimated to take, in us
+// (0 if it cannot be told).
+struct DensePlan {
+  int rows, cols, split;
+  float us;
+};
+DensePlan dense_pair_plan(const DenseGemm &g);
+DensePlan dense_small_plan(const DenseGemm &g);
+inline float dense_pair_us(const DenseGemm &g) { return dense_pair_plan(g).us; }
+inline float dense_small_us(const DenseGemm &g) { return dense_small_plan(g).us; }
 float dense_multi_us(const DenseGemm *g, int n);
 
 // dz = dy act'(z) in 16 bits (act none: not written) and the column sums of the

@@ -1122,15 +1122,15 @@ cudaError_t start(const PairMaps<kMulti> &maps, const PairArgs<kMulti> &a, int c
                             a);
 }
 
-// `us` not null: only the estimated time.
+// `out` not null: only the plan.
 template <int kEpi, bool kAMn, bool kBMn, bool kE4m3 = false, bool kExact = false>
-cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
+cudaError_t launch(const DenseGemm &g, cudaStream_t s, DensePlan *out) {
   int resident[2];
   cudaError_t e = resident_clusters<kEpi, kAMn, kBMn, kE4m3, false, kExact>(resident);
   if (e != cudaSuccess) return e;
   const PairPlan plan = plan_pair(g, resident);
-  if (us != nullptr) {
-    *us = plan.us;
+  if (out != nullptr) {
+    *out = {kTileM, plan.cols, plan.split, plan.us};
     return cudaSuccess;
   }
 
@@ -1166,27 +1166,27 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s, float *us) {
   return start<kEpi, kAMn, kBMn, kE4m3, false, kExact>(maps, a, plan.clusters, s);
 }
 
-cudaError_t pair_call(const DenseGemm &g, cudaStream_t s, float *us) {
+cudaError_t pair_call(const DenseGemm &g, cudaStream_t s, DensePlan *out) {
   const bool exact = g.act != MOE_ACT_NONE && g.out_dtype == MOE_DTYPE_FP32;
   if (g.dtype == MOE_DTYPE_E4M3)
-    return exact ? launch<kEpiLinear, false, false, true, true>(g, s, us)
-                 : launch<kEpiLinear, false, false, true>(g, s, us);
+    return exact ? launch<kEpiLinear, false, false, true, true>(g, s, out)
+                 : launch<kEpiLinear, false, false, true>(g, s, out);
   switch (g.epi) {
-    case kEpiGated: return launch<kEpiGated, false, false>(g, s, us);
-    case kEpiGatedGrad: return launch<kEpiGatedGrad, false, true>(g, s, us);
+    case kEpiGated: return launch<kEpiGated, false, false>(g, s, out);
+    case kEpiGatedGrad: return launch<kEpiGatedGrad, false, true>(g, s, out);
     default:
-      if (g.a_mn) return launch<kEpiLinear, true, true>(g, s, us);
-      if (g.b_mn) return launch<kEpiLinear, false, true>(g, s, us);
-      return exact ? launch<kEpiLinear, false, false, false, true>(g, s, us)
-                   : launch<kEpiLinear, false, false>(g, s, us);
+      if (g.a_mn) return launch<kEpiLinear, true, true>(g, s, out);
+      if (g.b_mn) return launch<kEpiLinear, false, true>(g, s, out);
+      return exact ? launch<kEpiLinear, false, false, false, true>(g, s, out)
+                   : launch<kEpiLinear, false, false>(g, s, out);
   }
 }
 
 }  // namespace
 
-float dense_pair_us(const DenseGemm &g) {
-  float us = 0.f;
-  return pair_call(g, nullptr, &us) == cudaSuccess ? us : 0.f;
+DensePlan dense_pair_plan(const DenseGemm &g) {
+  DensePlan p = {};
+  return pair_call(g, nullptr, &p) == cudaSuccess ? p : DensePlan{};
 }
 
 cudaError_t launch_dense_pair(const DenseGemm &g, cudaStream_t s) {

@@ -543,7 +543,10 @@ cudaError_t launch(const DenseGemm &g, cudaStream_t s) {
 
 }  // namespace
 
-float dense_small_us(const DenseGemm &g) { return plan_small(g).us; }
+DensePlan dense_small_plan(const DenseGemm &g) {
+  const SmallPlan p = plan_small(g);
+  return {p.n, g.epi == kEpiGated ? 64 : 128, p.split, p.us};
+}
 
 cudaError_t launch_dense_small(const DenseGemm &g, cudaStream_t s) {
   if (g.dtype == MOE_DTYPE_E4M3) return launch<false, true, false>(g, s);

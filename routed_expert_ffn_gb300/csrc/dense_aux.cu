@@ -2,7 +2,9 @@
 //
 // act_grad: dz = dy act'(z), rounded once to the 16-bit type the gradient
 // products take, with the column sums of the unrounded dz for the bias.
-// Bound: HBM (dy and z read, dz written).  A CTA takes 128 columns (a lane 4
+// Bound: HBM (dy and z read, dz written), of which it draws 60%: a thread's next
+// loads start when those before are used (2047 x 4096 with GELU by tanh 14 to 17 us,
+// 67 MB).  A CTA takes 128 columns (a lane 4
 // of them: 16 bytes of z, 8 of dy) and one slice of the rows, four rows a
 // thread in flight.  A slice's column sums go to the workspace; the last CTA
 // of the columns adds the slices in order, so the sums do not change from run

@@ -207,22 +207,6 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The cluster's barrier in two halves.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// `bytes` of this CTA's shared memory to another's, counted on that CTA's barrier.
-__device__ __forceinline__ void bulk_send(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
 
 struct Tile {
   int p, m0, j;  // product, first row, column tile
@@ -1018,7 +1002,9 @@ PairPlan plan_pair(const DenseGemm &g, const int (&resident)[2]) {
   p.mt = (g.M + kTileM - 1) / kTileM;
   const int mt = p.mt;
   for (int split = 1; split <= 2; ++split) {
-    const int part = split == 1 ? nkb : (nkb + 15) / 16 * 8;  // E4M3: whole groups of scales
+    // The first part in whole groups of eight stages, which E4M3's scale factors come
+    // in (16 bits could split evenly: 33 stages are 24 and 9 so).
+    const int part = split == 1 ? nkb : (nkb + 15) / 16 * 8;
     if (split == 2 && part >= nkb) continue;
     for (int bn = e4m3 ? Shape8::acc : Shape16::acc; bn >= 64; bn -= gated ? 64 : 32) {
       const int cols = gated ? bn / 2 : bn;

@@ -3,7 +3,9 @@
 //
 // Bound: the bytes of W from HBM.  W's rows are the MMA's M (128 a tile), the
 // rows of X its N (16 to 64), so a tile of W flows through the tensor core
-// once for all rows of X.  There are too few tiles of W to draw the whole
+// once for up to 64 rows of X; each further 64 read it again, from L2 (the caller's
+// estimates send batches of up to 1024 rows here where few columns leave the other
+// kernel's tiles too few).  There are too few tiles of W to draw the whole
 // bandwidth, so K is split over the CTAs of a cluster: each streams its own
 // part of K through a ring of TMA stages into its TMEM accumulator, and the
 // partial tiles are sent through distributed shared memory to the CTA that adds
@@ -100,23 +102,6 @@ __device__ __forceinline__ void store8(const float (&f)[8], void *p, int64_t off
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-// `bytes` of this CTA's shared memory to another's, counted on that CTA's barrier.
-__device__ __forceinline__ void bulk_send(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "r"(smem_u32(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
-// The cluster's barrier in two halves.  Arrivals release what was written
-// before (to any shared memory of the cluster), the wait acquires it.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // f[i] = sum over the ranks, in rank order, of 8 floats of their partial tiles
 __device__ __forceinline__ void add_parts(float (&f)[8], const float *p, int split, int stride) {

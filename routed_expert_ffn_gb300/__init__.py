@@ -206,7 +206,8 @@ def _current_stream() -> int:
         _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
     else:
         # 0.2 us instead of 3 for the Stream object and its handle
-        device = torch.cuda.current_device
+        torch.cuda.current_device()  # sets torch's CUDA side up; from then on without asking for it
+        device = torch._C._cuda_getDevice
         _current_stream = lambda: raw(device())  # noqa: E731
     return _current_stream()
 
@@ -464,12 +465,12 @@ def _rows(t, stride: int, cols: int, rows: int = 0, code: int = None) -> Optiona
         return t
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    n, s = t.shape, t.stride()
-    if not (len(n) == 2 and n[1] == cols and (s[0] == (stride or cols) or n[0] <= 1) and (
-            s[1] == 1 or cols == 1)):
+    n, c = t.shape  # (a ValueError, too, unless there are two)
+    step, one = t.stride()
+    if c != cols or (step != (stride or cols) and n > 1) or (one != 1 and cols != 1):
         raise ValueError("expected a [T, cols] tensor with rows at the descriptor's stride")
-    if n[0] < rows:
-        raise ValueError(f"expected {rows} rows, got {n[0]}")
+    if n < rows:
+        raise ValueError(f"expected {rows} rows, got {n}")
     if t.dtype not in _ACCEPTED[code]:
         raise ValueError(f"{t.dtype} is not the descriptor's element type")
     return t.data_ptr()

@@ -1,7 +1,8 @@
 // The row-wise pass of the dense operators' gradients.
 //
 // act_grad: dz = dy act'(z), rounded once to the 16-bit type the gradient
-// products take, with the column sums of the unrounded dz for the bias.
+// products take (more bits would take each product twice; bf16 gradients end 0.0023
+// off in the 2-norm, with their own rounding alone 0.0017), with the column sums of the unrounded dz for the bias.
 // Bound: HBM (dy and z read, dz written), of which it draws 60%: a thread's next
 // loads start when those before are used (2047 x 4096 with GELU by tanh 14 to 17 us,
 // 67 MB).  A CTA takes 128 columns (a lane 4

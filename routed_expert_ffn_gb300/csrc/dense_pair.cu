@@ -901,7 +901,11 @@ __global__ void __launch_bounds__(Shape<kEpi, kE4m3>::threads, 1)
           put16(p, lane, a.dtype, v);
           send_2d(&map.d, p, lane, c, row0);
         } else {
-          // dh = acc;  s = sigmoid(g):  h = g s u, dg = dh u s (1 + g (1 - s)), du = dh g s
+          // dh = acc;  s = sigmoid(g):  h = g s u, dg = dh u s (1 + g (1 - s)), du = dh g s.
+          // All three in 16 bits: they are the next products' operands, and keeping
+          // more bits would take each product twice (high and low parts).  bf16
+          // gradients end 0.0023 to 0.0025 off in the 2-norm, with the rounding of
+          // the result alone 0.0016 to 0.0017.
           uint32_t wh[16], wg[16], wu[16];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {

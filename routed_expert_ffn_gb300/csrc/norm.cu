@@ -13,7 +13,7 @@
 // Bound: HBM.  Forward: 3 row tensors read and written plus y (or its 8-bit
 // codes); backward: 3 read, 1 written.  A row lives in the registers of one
 // group of threads (kV chunks of 8 elements a thread), so every tensor is read
-// once, and the mean costs one shuffle reduction and one exchange through
+// once, and the mean costs a reduction in each warp and one exchange through
 // shared memory.  Forward a CTA ends with its row (or few short ones); backward
 // the CTAs stay and walk the rows, adding up dw in registers, and each thread
 // copies its own chunks of the next rows to shared memory meanwhile (cp.async

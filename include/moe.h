@@ -733,6 +733,63 @@ moe_status_t moe_gated_ffn_backward(const moe_ffn_desc_t *d, const void *dy, con
                                     void *dw13, void *dw2, int32_t dw_dtype, int32_t accumulate,
                                     void *workspace, size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The experts' matrix products on their own: the product of each expert's rows with
+ * its matrix and its gradients, for training and for layers whose activation is not
+ * moe_grouped_swiglu_ffn's.
+ *
+ * Rows [offsets[e], offsets[e+1]) of the row tensors are expert e's, as
+ * moe_build_dispatch lays them out; an expert may have none.  The conventions of the
+ * dense operators hold.  In addition:
+ * - offsets are [E+1] int32 on the device, 0 <= offsets[0], none below the one before
+ *   it, offsets[E] <= R.  Offsets that are not so set bit 3 of the status word
+ *   (MOE_ERR_DEVICE_CHECK); nothing is computed then.
+ * - Rows before offsets[0] and from offsets[E] on take part in no product; of the
+ *   outputs they are left as they were.
+ */
+typedef struct {
+  int32_t R;         /* rows of x and y */
+  int32_t E;         /* experts: matrices of w */
+  int32_t N, K;      /* output columns, input columns */
+  int32_t dtype;     /* of x, w and the gradients of rows: BF16 or FP16 */
+  int32_t out_dtype; /* of y: dtype or FP32 */
+  int64_t x_stride;  /* rows of x (and dx) */
+  int64_t y_stride;  /* rows of y (and dy) */
+} moe_grouped_desc_t;
+
+/* Bytes of the workspace of every call with this descriptor; 0 for an invalid one. */
+size_t moe_grouped_linear_workspace_size(const moe_grouped_desc_t *d);
+
+/*
+ * moe_grouped_linear -- y_p = W_e x_p for every row p of every expert e
+ * ("MoE推理优化全景指南", section "Expert GEMM 为什么经常不够大": one scheduled GEMM
+ * over [m_i, hidden] @ W_i for all experts).
+ *   x        [R,K] in
+ *   offsets  [E+1] int32 in
+ *   w        [E,N,K] in, dense
+ *   y        [R,N] out; fp32 sums rounded once
+ * Limits: 0 <= R <= 2^24, 1 <= E <= 512, 8 <= N, K <= 2^18, both multiples of 8
+ * (MOE_ERR_UNSUPPORTED_SHAPE).
+ */
+moe_status_t moe_grouped_linear(const moe_grouped_desc_t *d, const void *x, const int32_t *offsets,
+                                const void *w, void *y, void *workspace, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/*
+ * moe_grouped_linear_backward -- for every row p of every expert e
+ *   dx_p = W_e^T dy_p,   dW_e = sum over e's rows p of dy_p x_p^T
+ *   dy     [R,N] in, of type dtype, rows y_stride apart
+ *   dx     [R,K] out, of type dtype, rows x_stride apart, or NULL
+ *   dw     [E,N,K] out of type dw_dtype (dtype or FP32), dense, or NULL
+ *   accumulate  1: dw is added to what it holds, 0: written (zeros for an expert
+ *          without rows)
+ */
+moe_status_t moe_grouped_linear_backward(const moe_grouped_desc_t *d, const void *dy, const void *x,
+                                         const int32_t *offsets, const void *w, void *dx, void *dw,
+                                         int32_t dw_dtype, int32_t accumulate, void *workspace,
+                                         size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -116,6 +116,12 @@ class FfnDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class GroupedDesc(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -162,6 +168,10 @@ def library() -> ctypes.CDLL:
         "moe_gated_ffn": ([ctypes.POINTER(FfnDesc), P, P, P, P, P, P, P, S, P], I32),
         "moe_gated_ffn_backward": ([ctypes.POINTER(FfnDesc), P, P, P, P, P, P, P, P, I32, I32, P,
                                     S, P], I32),
+        "moe_grouped_linear_workspace_size": ([ctypes.POINTER(GroupedDesc)], S),
+        "moe_grouped_linear": ([ctypes.POINTER(GroupedDesc), P, P, P, P, P, S, P], I32),
+        "moe_grouped_linear_backward": ([ctypes.POINTER(GroupedDesc), P, P, P, P, P, P, I32, I32, P,
+                                         S, P], I32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -239,7 +249,8 @@ def moe_workspace_layout(d: LayerDesc) -> Dict[str, int]:
 
 _WORKSPACE_SIZE = {LayerDesc: "moe_workspace_size", NormDesc: "moe_norm_workspace_size",
                    LinearDesc: "moe_linear_workspace_size",
-                   FfnDesc: "moe_gated_ffn_workspace_size"}
+                   FfnDesc: "moe_gated_ffn_workspace_size",
+                   GroupedDesc: "moe_grouped_linear_workspace_size"}
 
 
 def alloc_workspace(d, device="cuda"):
@@ -439,6 +450,7 @@ def dtype_of(t) -> int:
 
 
 _EXPONENTS = -1  # int8 block exponents, beside the MOE_DTYPE_* in _ACCEPTED
+_INT32 = -2      # offsets
 
 
 class _Accepted(dict):
@@ -451,6 +463,7 @@ class _Accepted(dict):
         self[code] = frozenset({
             MOE_DTYPE_BF16: [torch.bfloat16], MOE_DTYPE_FP16: [torch.float16],
             MOE_DTYPE_FP32: [torch.float32], _EXPONENTS: [torch.int8],
+            _INT32: [torch.int32],
             MOE_DTYPE_E4M3: [torch.float8_e4m3fn, torch.uint8, torch.int8]}.get(code, every))
         return self[code]
 
@@ -610,6 +623,39 @@ def moe_gated_ffn_backward(d: FfnDesc, dy, x, w13, w2, saved, dx, dw13, dw2, ws,
         _flat(w2, HI, dt), _flat(saved, 2 * d.T * d.I, MOE_DTYPE_FP32), _flat(dx, TH, dt),
         _flat(dw13, 2 * HI, dw_dtype), _flat(dw2, HI, dw_dtype), dw_dtype, 1 if accumulate else 0,
         _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+# ---------------------------------------------- the experts' products --
+# As the dense operators; offsets are int32 tensors of E + 1 elements (moe_build_dispatch's).
+
+def grouped_desc(R: int, E: int, N: int, K: int, dtype: int, out_dtype: int = None,
+                 x_stride: int = 0, y_stride: int = 0) -> GroupedDesc:
+    return GroupedDesc(R, E, N, K, dtype, dtype if out_dtype is None else out_dtype, x_stride,
+                       y_stride)
+
+
+def moe_grouped_linear_workspace_size(d: GroupedDesc) -> int:
+    return int(library().moe_grouped_linear_workspace_size(ctypes.byref(d)))
+
+
+def moe_grouped_linear(d: GroupedDesc, x, offsets, w, y, ws, stream=None):
+    """y_p = W_e x_p for the rows p in [offsets[e], offsets[e+1]) of each expert e."""
+    _check("moe_grouped_linear", library().moe_grouped_linear(
+        ctypes.byref(d), _rows(x, d.x_stride, d.K, d.R, d.dtype), _flat(offsets, d.E + 1, _INT32),
+        _flat(w, d.E * d.N * d.K, d.dtype), _rows(y, d.y_stride, d.N, d.R, d.out_dtype), _ptr(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def moe_grouped_linear_backward(d: GroupedDesc, dy, x, offsets, w, dx, dw, ws,
+                                accumulate: bool = False, stream=None):
+    """dx and dw (in the type of x or fp32) of moe_grouped_linear; either may be None."""
+    dw_dtype, count = _grad_dtype(d, dw), d.E * d.N * d.K
+    _check("moe_grouped_linear_backward", library().moe_grouped_linear_backward(
+        ctypes.byref(d), _rows(dy, d.y_stride, d.N, d.R, d.dtype),
+        _rows(x, d.x_stride, d.K, d.R, d.dtype), _flat(offsets, d.E + 1, _INT32),
+        _flat(w, count, d.dtype), _rows(dx, d.x_stride, d.K, d.R, d.dtype),
+        _flat(dw, count, dw_dtype), dw_dtype, 1 if accumulate else 0, _ptr(ws), _nbytes(ws),
+        _stream(stream)))
 
 
 def workspace_view(ws, layout: Dict[str, int], name: str, dtype, shape):

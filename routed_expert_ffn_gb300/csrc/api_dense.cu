@@ -3,53 +3,12 @@
 // argument are in include/moe.h.
 #include <stdint.h>
 
-#include <initializer_list>
-
+#include "api_util.cuh"
 #include "dense.cuh"
 
 namespace moe {
 
-namespace {
-
-moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-// A workspace of at least `need` bytes, aligned to 256.
-moe_status_t check_ws(const void *ws, size_t ws_bytes, size_t need) {
-  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
-  return ws_bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
-}
-
-// Whether `out` is at the address of one of `others` that the call still reads, or
-// writes too (null: no argument).
-bool lies_on(const void *out, std::initializer_list<const void *> others) {
-  for (const void *p : others)
-    if (out != nullptr && out == p) return true;
-  return false;
-}
-
-// A row stride in elements: 0 (dense) becomes `cols`; otherwise at least
-// `cols` and a multiple of `mult`.
-bool fix_stride(int64_t *stride, int64_t cols, int mult) {
-  if (*stride == 0) *stride = cols;
-  return *stride >= cols && *stride % mult == 0 && *stride < ((int64_t)1 << 36);
-}
-
-// A validated copy of the descriptor with its strides filled in.
-moe_status_t norm_desc(const moe_norm_desc_t *in, moe_norm_desc_t *d) {
-  if (in == nullptr) return MOE_ERR_INVALID_ARG;
-  *d = *in;
-  if (d->dtype != MOE_DTYPE_BF16 && d->dtype != MOE_DTYPE_FP16 && d->dtype != MOE_DTYPE_FP32)
-    return MOE_ERR_INVALID_ARG;
-  if (!(d->eps >= 0.f)) return MOE_ERR_INVALID_ARG;
-  if (d->T < 0 || d->T > kMaxT || d->H < 8 || d->H > 16384 || d->H % 8 != 0)
-    return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (!fix_stride(&d->x_stride, d->H, 8) || !fix_stride(&d->residual_stride, d->H, 8) ||
-      !fix_stride(&d->y_stride, d->H, 8))
-    return MOE_ERR_UNSUPPORTED_SHAPE;
-  return MOE_OK;
-}
-
-moe_status_t linear_desc(const moe_linear_desc_t *in, moe_linear_desc_t *d) {
+moe_status_t check_linear_desc(const moe_linear_desc_t *in, moe_linear_desc_t *d) {
   if (in == nullptr) return MOE_ERR_INVALID_ARG;
   *d = *in;
   const bool e4m3 = d->dtype == MOE_DTYPE_E4M3;
@@ -68,7 +27,22 @@ moe_status_t linear_desc(const moe_linear_desc_t *in, moe_linear_desc_t *d) {
   return MOE_OK;
 }
 
-size_t pad(size_t n) { return (n + 1023) / 1024 * 1024; }
+namespace {
+
+// A validated copy of the descriptor with its strides filled in.
+moe_status_t norm_desc(const moe_norm_desc_t *in, moe_norm_desc_t *d) {
+  if (in == nullptr) return MOE_ERR_INVALID_ARG;
+  *d = *in;
+  if (d->dtype != MOE_DTYPE_BF16 && d->dtype != MOE_DTYPE_FP16 && d->dtype != MOE_DTYPE_FP32)
+    return MOE_ERR_INVALID_ARG;
+  if (!(d->eps >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (d->T < 0 || d->T > kMaxT || d->H < 8 || d->H > 16384 || d->H % 8 != 0)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!fix_stride(&d->x_stride, d->H, 8) || !fix_stride(&d->residual_stride, d->H, 8) ||
+      !fix_stride(&d->y_stride, d->H, 8))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
 
 // After the status block: dz and the column partials of the gradient.
 struct LinearWs {
@@ -103,8 +77,6 @@ FfnWs ffn_ws(const moe_ffn_desc_t &d) {
   w.total = w.dgu + pad((size_t)d.T * d.I * 4);
   return w;
 }
-
-uint8_t *at(void *ws, size_t off) { return static_cast<uint8_t *>(ws) + off; }
 
 // D[M,N] = A B with fp32 accumulators: the fields every product shares.
 DenseGemm product(int M, int N, int K, int dtype, const void *a, int64_t lda, bool a_mn,
@@ -168,12 +140,6 @@ DenseGemm weight_grad(int M, int N, int T, int dtype, const void *a, int64_t lda
     g.ldr = N;
   }
   return g;
-}
-
-// The gradient of a weight over no rows: zeros, or what is accumulated.
-cudaError_t no_rows(void *dw, int64_t n, int dw_dtype, int accumulate, cudaStream_t s) {
-  if (dw == nullptr || accumulate) return cudaSuccess;
-  return cudaMemsetAsync(dw, 0, (size_t)n * (dw_dtype == MOE_DTYPE_FP32 ? 4 : 2), s);
 }
 
 }  // namespace
@@ -240,13 +206,13 @@ moe_status_t moe_add_rms_norm_backward(const moe_norm_desc_t *in, const void *dy
 
 size_t moe_linear_workspace_size(const moe_linear_desc_t *in) {
   moe_linear_desc_t d;
-  return linear_desc(in, &d) == MOE_OK ? linear_ws(d).total : 0;
+  return check_linear_desc(in, &d) == MOE_OK ? linear_ws(d).total : 0;
 }
 
 moe_status_t moe_linear_plan(const moe_linear_desc_t *in, int32_t with_preact,
                              moe_linear_plan_t *plan) {
   moe_linear_desc_t d;
-  moe_status_t st = linear_desc(in, &d);
+  moe_status_t st = check_linear_desc(in, &d);
   if (st != MOE_OK) return st;
   if (plan == nullptr || d.T == 0) return MOE_ERR_INVALID_ARG;
   if ((st = check_device()) != MOE_OK) return st;
@@ -270,7 +236,7 @@ moe_status_t moe_linear(const moe_linear_desc_t *in, const void *x, const int8_t
                         const void *residual, float *preact, void *y, void *workspace,
                         size_t ws_bytes, moe_stream_t stream) {
   moe_linear_desc_t d;
-  moe_status_t st = linear_desc(in, &d);
+  moe_status_t st = check_linear_desc(in, &d);
   if (st != MOE_OK) return st;
   const LinearWs L = linear_ws(d);
   if ((st = check_ws(workspace, ws_bytes, L.total)) != MOE_OK) return st;
@@ -305,7 +271,7 @@ moe_status_t moe_linear_backward(const moe_linear_desc_t *in, const void *dy, co
                                  int32_t dw_dtype, float *dbias, int32_t accumulate,
                                  void *workspace, size_t ws_bytes, moe_stream_t stream) {
   moe_linear_desc_t d;
-  moe_status_t st = linear_desc(in, &d);
+  moe_status_t st = check_linear_desc(in, &d);
   if (st != MOE_OK) return st;
   if (d.dtype == MOE_DTYPE_E4M3) return MOE_ERR_INVALID_ARG;
   if (dw_dtype != d.dtype && dw_dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;

@@ -1,0 +1,132 @@
+// C ABI of the experts' ragged products: argument validation and the sequence of
+// launches of each call.  Declarations and the meaning of every argument are in
+// include/moe.h.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "api_util.cuh"
+#include "grouped.cuh"
+
+namespace moe {
+
+namespace {
+
+// A validated copy of the descriptor with its strides filled in.
+moe_status_t grouped_desc(const moe_grouped_desc_t *in, moe_grouped_desc_t *d) {
+  if (in == nullptr) return MOE_ERR_INVALID_ARG;
+  *d = *in;
+  if (d->dtype != MOE_DTYPE_BF16 && d->dtype != MOE_DTYPE_FP16) return MOE_ERR_INVALID_ARG;
+  if (d->out_dtype != d->dtype && d->out_dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
+  const int32_t most = 1 << 18;
+  if (d->R < 0 || d->R > kMaxAssign || d->E < 1 || d->E > kMaxE || d->N < 8 || d->N > most ||
+      d->N % 8 != 0 || d->K < 8 || d->K > most || d->K % 8 != 0)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!fix_stride(&d->x_stride, d->K, 8) || !fix_stride(&d->y_stride, d->N, 8))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+// After the status block: the weight gradient's tensor maps, then partial sums.
+struct GroupedWs {
+  size_t maps, part, total;
+};
+GroupedWs grouped_ws(const moe_grouped_desc_t &d) {
+  GroupedWs w;
+  w.maps = kStatusPad;
+  w.part = w.maps + pad(grouped_map_bytes(d.E));
+  w.total = w.part + pad(grouped_part_bytes(d.R));
+  return w;
+}
+
+GroupedGemm grouped_product(const moe_grouped_desc_t &d, const int32_t *offsets, const void *x,
+                            const void *w, const void *dy, void *out, int out_dtype,
+                            void *workspace) {
+  const GroupedWs L = grouped_ws(d);
+  GroupedGemm g = {};
+  g.R = d.R;
+  g.E = d.E;
+  g.N = d.N;
+  g.K = d.K;
+  g.dtype = d.dtype;
+  g.out_dtype = out_dtype;
+  g.offsets = offsets;
+  g.x = x;
+  g.w = w;
+  g.dy = dy;
+  g.ldx = d.x_stride;
+  g.ldy = d.y_stride;
+  g.d = out;
+  g.part = reinterpret_cast<float *>(at(workspace, L.part));
+  g.maps = reinterpret_cast<CUtensorMap *>(at(workspace, L.maps));
+  g.status = static_cast<uint32_t *>(workspace);
+  return g;
+}
+
+bool ok_offsets(const int32_t *p) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_grouped_linear_workspace_size(const moe_grouped_desc_t *in) {
+  moe_grouped_desc_t d;
+  return grouped_desc(in, &d) == MOE_OK ? grouped_ws(d).total : 0;
+}
+
+moe_status_t moe_grouped_linear(const moe_grouped_desc_t *in, const void *x, const int32_t *offsets,
+                                const void *w, void *y, void *workspace, size_t ws_bytes,
+                                moe_stream_t stream) {
+  moe_grouped_desc_t d;
+  moe_status_t st = grouped_desc(in, &d);
+  if (st != MOE_OK) return st;
+  if ((st = check_ws(workspace, ws_bytes, grouped_ws(d).total)) != MOE_OK) return st;
+  if (!ok_offsets(offsets)) return MOE_ERR_INVALID_ARG;
+  if (d.R == 0) return MOE_OK;  // empty tensors may have no address
+  if (!ok_ptr(x) || !ok_ptr(w) || !ok_ptr(y)) return MOE_ERR_INVALID_ARG;
+  if (lies_on(y, {x, w, offsets})) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device()) != MOE_OK) return st;
+  const GroupedGemm g = grouped_product(d, offsets, x, w, nullptr, y, d.out_dtype, workspace);
+  return cuda_status(launch_grouped_rows(g, false, (cudaStream_t)stream));
+}
+
+moe_status_t moe_grouped_linear_backward(const moe_grouped_desc_t *in, const void *dy,
+                                         const void *x, const int32_t *offsets, const void *w,
+                                         void *dx, void *dw, int32_t dw_dtype, int32_t accumulate,
+                                         void *workspace, size_t ws_bytes, moe_stream_t stream) {
+  moe_grouped_desc_t d;
+  moe_status_t st = grouped_desc(in, &d);
+  if (st != MOE_OK) return st;
+  if (dw_dtype != d.dtype && dw_dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(workspace, ws_bytes, grouped_ws(d).total)) != MOE_OK) return st;
+  if (!ok_offsets(offsets) || !ok_opt(dw)) return MOE_ERR_INVALID_ARG;
+  if (d.R > 0) {
+    if (!ok_ptr(dy) || !ok_opt(dx)) return MOE_ERR_INVALID_ARG;
+    if ((dx != nullptr && !ok_ptr(w)) || (dw != nullptr && !ok_ptr(x))) return MOE_ERR_INVALID_ARG;
+    const void *w_read = dx != nullptr ? w : nullptr, *x_read = dw != nullptr ? x : nullptr;
+    if (lies_on(dx, {dy, x_read, w, offsets}) || lies_on(dw, {dy, x, w_read, dx, offsets}))
+      return MOE_ERR_INVALID_ARG;
+  }
+  if ((st = check_device()) != MOE_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (d.R == 0)
+    return cuda_status(no_rows(dw, (int64_t)d.E * d.N * d.K, dw_dtype, accumulate, s));
+  cudaError_t e = cudaSuccess;
+  if (dx != nullptr)
+    e = launch_grouped_rows(grouped_product(d, offsets, x, w, dy, dx, d.dtype, workspace), true, s);
+  if (e == cudaSuccess && dw != nullptr) {
+    GroupedGemm g = grouped_product(d, offsets, x, w, dy, dw, dw_dtype, workspace);
+    g.accumulate = accumulate;
+    e = launch_grouped_weight_grad(g, s);
+  }
+  return cuda_status(e);
+}
+
+}  // extern "C"

@@ -790,6 +790,52 @@ moe_status_t moe_grouped_linear_backward(const moe_grouped_desc_t *d, const void
                                          int32_t dw_dtype, int32_t accumulate, void *workspace,
                                          size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * Weights in 4 bits ("MoE推理优化全景指南", section "量化与 offload 并非独立开关",
+ * "专家权重量化"; the scale layout is the implementation's choice).  `group` (32, 64 or
+ * 128) successive columns of a row share a scale of the type of the activations; two codes
+ * to a byte, the even column's in the low half.  A weight is (code - 8) * scale, and
+ * the products below take it as that: neither is rounded on the way.
+ *   q      [...,N,K/2] bytes
+ *   scale  [...,N,ceil(K/group)]; the last group of a row may be short
+ * K is a multiple of 32.
+ */
+
+/*
+ * moe_quantize_int4 -- 4-bit codes of w [rows,K] (for [E,N,K] rows = E*N):
+ *   scale = max |w| of the group / 7, rounded to the type of w
+ *   code  = 8 + w / scale rounded to nearest even, at least 0 and at most 15
+ * (8 throughout where the scale is 0, infinite or NaN).
+ *   w       [rows,K] in, of type dtype (BF16 or FP16), dense
+ *   q, scale  out
+ *   values  [rows,K] out or NULL, of type dtype: what the codes stand for,
+ *           rounded (training with the rounding in the forward); may be w
+ * Limits: 0 <= rows <= 2^27, 32 <= K <= 2^18.
+ */
+moe_status_t moe_quantize_int4(const void *w, int32_t dtype, int64_t rows, int32_t K, int32_t group,
+                               void *q, void *scale, void *values, moe_stream_t stream);
+
+/*
+ * moe_linear_int4 -- moe_linear, y = act(x w^T + bias) + residual, with w in 4 bits.
+ *   d       as moe_linear's, dtype BF16 or FP16; the workspace too
+ *   scale   [N,ceil(K/group)] of type dtype
+ * Other arguments as moe_linear.  Made for few rows: W is read once for each 16.
+ */
+moe_status_t moe_linear_int4(const moe_linear_desc_t *d, int32_t group, const void *x,
+                             const void *q, const void *scale, const void *bias,
+                             const void *residual, void *y, void *workspace, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/*
+ * moe_grouped_linear_int4 -- moe_grouped_linear with the experts' matrices in 4 bits.
+ *   q       [E,N,K/2], scale [E,N,ceil(K/group)] of type dtype
+ * Other arguments as moe_grouped_linear; R <= 2^20.
+ */
+moe_status_t moe_grouped_linear_int4(const moe_grouped_desc_t *d, int32_t group, const void *x,
+                                     const int32_t *offsets, const void *q, const void *scale,
+                                     void *y, void *workspace, size_t ws_bytes,
+                                     moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -170,6 +170,9 @@ def library() -> ctypes.CDLL:
                                     S, P], I32),
         "moe_grouped_linear_workspace_size": ([ctypes.POINTER(GroupedDesc)], S),
         "moe_grouped_linear": ([ctypes.POINTER(GroupedDesc), P, P, P, P, P, S, P], I32),
+        "moe_quantize_int4": ([P, I32, ctypes.c_int64, I32, I32, P, P, P, P], I32),
+        "moe_linear_int4": ([ctypes.POINTER(LinearDesc), I32, P, P, P, P, P, P, P, S, P], I32),
+        "moe_grouped_linear_int4": ([ctypes.POINTER(GroupedDesc), I32, P, P, P, P, P, P, S, P], I32),
         "moe_grouped_linear_backward": ([ctypes.POINTER(GroupedDesc), P, P, P, P, P, P, I32, I32, P,
                                          S, P], I32),
     }
@@ -656,6 +659,42 @@ def moe_grouped_linear_backward(d: GroupedDesc, dy, x, offsets, w, dx, dw, ws,
         _flat(w, count, d.dtype), _rows(dx, d.x_stride, d.K, d.R, d.dtype),
         _flat(dw, count, dw_dtype), dw_dtype, 1 if accumulate else 0, _ptr(ws), _nbytes(ws),
         _stream(stream)))
+
+
+def _groups(K: int, group: int) -> int:
+    return -(-K // group) if group > 0 else 0
+
+
+def moe_quantize_int4(w, rows: int, K: int, group: int, q, scale, values=None, dtype: int = None,
+                      stream=None):
+    """4-bit codes q [rows,K/2] (two to a byte) and scales [rows,ceil(K/group)] of w [rows,K];
+    ``values``: what the codes stand for ([rows,K], or None).  ``dtype``: of a plain address."""
+    if dtype is None:
+        dtype = MOE_DTYPE_BF16 if isinstance(w, int) else dtype_of(w)
+    _check("moe_quantize_int4", library().moe_quantize_int4(
+        _flat(w, rows * K, dtype), dtype, rows, K, group, _flat(q, rows * K // 2, MOE_DTYPE_E4M3),
+        _flat(scale, rows * _groups(K, group), dtype), _flat(values, rows * K, dtype),
+        _stream(stream)))
+
+
+def moe_linear_int4(d: LinearDesc, group: int, x, q, scale, bias, residual, y, ws, stream=None):
+    """moe_linear with w in 4 bits: codes q [N,K/2] and scales [N,ceil(K/group)]."""
+    T, N, K, dt, out = d.T, d.N, d.K, d.dtype, d.out_dtype
+    _check("moe_linear_int4", library().moe_linear_int4(
+        ctypes.byref(d), group, _rows(x, d.x_stride, K, T, dt),
+        _flat(q, N * K // 2, MOE_DTYPE_E4M3), _flat(scale, N * _groups(K, group), dt),
+        _flat(bias, N, out), _rows(residual, d.residual_stride, N, T, out),
+        _rows(y, d.y_stride, N, T, out), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_grouped_linear_int4(d: GroupedDesc, group: int, x, offsets, q, scale, y, ws, stream=None):
+    """moe_grouped_linear with w in 4 bits: codes q [E,N,K/2] and scales [E,N,ceil(K/group)]."""
+    EN = d.E * d.N
+    _check("moe_grouped_linear_int4", library().moe_grouped_linear_int4(
+        ctypes.byref(d), group, _rows(x, d.x_stride, d.K, d.R, d.dtype),
+        _flat(offsets, d.E + 1, _INT32), _flat(q, EN * d.K // 2, MOE_DTYPE_E4M3),
+        _flat(scale, EN * _groups(d.K, group), d.dtype),
+        _rows(y, d.y_stride, d.N, d.R, d.out_dtype), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def workspace_view(ws, layout: Dict[str, int], name: str, dtype, shape):

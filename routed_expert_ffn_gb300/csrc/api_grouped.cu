@@ -7,6 +7,7 @@
 
 #include "api_util.cuh"
 #include "grouped.cuh"
+#include "int4.cuh"
 
 namespace moe {
 
@@ -62,6 +63,8 @@ GroupedGemm grouped_product(const moe_grouped_desc_t &d, const int32_t *offsets,
   g.status = static_cast<uint32_t *>(workspace);
   return g;
 }
+
+bool ok_group(int32_t group) { return group == 32 || group == 64 || group == 128; }
 
 bool ok_offsets(const int32_t *p) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
@@ -127,6 +130,96 @@ moe_status_t moe_grouped_linear_backward(const moe_grouped_desc_t *in, const voi
     e = launch_grouped_weight_grad(g, s);
   }
   return cuda_status(e);
+}
+
+moe_status_t moe_quantize_int4(const void *w, int32_t dtype, int64_t rows, int32_t K, int32_t group,
+                               void *q, void *scale, void *values, moe_stream_t stream) {
+  if ((dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) || !ok_group(group))
+    return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || rows > ((int64_t)1 << 27) || K < 32 || K > 1 << 18 || K % 32 != 0)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return MOE_OK;  // empty tensors may have no address
+  if (!ok_ptr(w) || !ok_ptr(q) || !ok_ptr(scale) || !ok_opt(values)) return MOE_ERR_INVALID_ARG;
+  // values may be w: a thread writes what it alone has read
+  if (lies_on(q, {w, scale, values}) || lies_on(scale, {w, values})) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_device();
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_int4(w, dtype, rows, K, group, static_cast<uint8_t *>(q), scale,
+                                          values, (cudaStream_t)stream));
+}
+
+moe_status_t moe_linear_int4(const moe_linear_desc_t *in, int32_t group, const void *x,
+                             const void *q, const void *scale, const void *bias,
+                             const void *residual, void *y, void *workspace, size_t ws_bytes,
+                             moe_stream_t stream) {
+  moe_linear_desc_t d;
+  moe_status_t st = check_linear_desc(in, &d);
+  if (st != MOE_OK) return st;
+  if (d.dtype == MOE_DTYPE_E4M3 || !ok_group(group)) return MOE_ERR_INVALID_ARG;
+  if (d.K % 32 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((st = check_ws(workspace, ws_bytes, moe_linear_workspace_size(in))) != MOE_OK) return st;
+  if (d.T == 0) return MOE_OK;  // empty tensors may have no address
+  if (!ok_ptr(x) || !ok_ptr(q) || !ok_ptr(scale) || !ok_opt(bias) || !ok_opt(residual) ||
+      !ok_ptr(y))
+    return MOE_ERR_INVALID_ARG;
+  if (residual == y && d.residual_stride != d.y_stride) return MOE_ERR_INVALID_ARG;
+  if (lies_on(y, {x, q, scale, bias})) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device()) != MOE_OK) return st;
+  Int4Gemm g = {};
+  g.T = d.T;
+  g.E = 1;
+  g.N = d.N;
+  g.K = d.K;
+  g.group = group;
+  g.dtype = d.dtype;
+  g.out_dtype = d.out_dtype;
+  g.act = d.act;
+  g.x = x;
+  g.q = static_cast<const uint8_t *>(q);
+  g.scale = scale;
+  g.bias = bias;
+  g.residual = residual;
+  g.y = y;
+  g.ldx = d.x_stride;
+  g.ldr = d.residual_stride;
+  g.ldy = d.y_stride;
+  g.status = static_cast<uint32_t *>(workspace);
+  return cuda_status(launch_int4_small(g, (cudaStream_t)stream));
+}
+
+moe_status_t moe_grouped_linear_int4(const moe_grouped_desc_t *in, int32_t group, const void *x,
+                                     const int32_t *offsets, const void *q, const void *scale,
+                                     void *y, void *workspace, size_t ws_bytes,
+                                     moe_stream_t stream) {
+  moe_grouped_desc_t d;
+  moe_status_t st = grouped_desc(in, &d);
+  if (st != MOE_OK) return st;
+  if (!ok_group(group)) return MOE_ERR_INVALID_ARG;
+  if (d.K % 32 != 0 || d.R > kMaxT) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((st = check_ws(workspace, ws_bytes, grouped_ws(d).total)) != MOE_OK) return st;
+  if (!ok_offsets(offsets)) return MOE_ERR_INVALID_ARG;
+  if (d.R == 0) return MOE_OK;  // empty tensors may have no address
+  if (!ok_ptr(x) || !ok_ptr(q) || !ok_ptr(scale) || !ok_ptr(y)) return MOE_ERR_INVALID_ARG;
+  if (lies_on(y, {x, q, scale, offsets})) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device()) != MOE_OK) return st;
+  Int4Gemm g = {};
+  g.T = d.R;
+  g.E = d.E;
+  g.N = d.N;
+  g.K = d.K;
+  g.group = group;
+  g.dtype = d.dtype;
+  g.out_dtype = d.out_dtype;
+  g.act = MOE_ACT_NONE;
+  g.offsets = offsets;
+  g.x = x;
+  g.q = static_cast<const uint8_t *>(q);
+  g.scale = scale;
+  g.y = y;
+  g.ldx = d.x_stride;
+  g.ldy = d.y_stride;
+  g.status = static_cast<uint32_t *>(workspace);
+  return cuda_status(launch_int4_small(g, (cudaStream_t)stream));
 }
 
 }  // extern "C"

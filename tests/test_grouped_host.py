@@ -71,3 +71,48 @@ def test_tensors(lib):  # noqa: F811
         moe.moe_grouped_linear(d, X, off[:3], W, Y, ws(), stream=0)
     with pytest.raises(ValueError):
         moe.moe_grouped_linear(d, X, off.long(), W, Y, ws(), stream=0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(group=16), INVALID), (dict(group=0), INVALID), (dict(group=256), INVALID),
+    (dict(rows=-1), SHAPE), (dict(rows=(1 << 27) + 1), SHAPE), (dict(K=48), SHAPE),
+    (dict(K=0), SHAPE), (dict(K=(1 << 18) + 32), SHAPE), (dict(dtype=moe.MOE_DTYPE_FP32), INVALID),
+    (dict(w=None), INVALID), (dict(w=W + 8), INVALID), (dict(q=None), INVALID),
+    (dict(q=W), INVALID), (dict(scale=None), INVALID), (dict(scale=W), INVALID),
+    (dict(values=Y + 4), INVALID), (dict(values=X), INVALID), (dict(q=DX, scale=DX), INVALID)])
+def test_quantize_int4(lib, kw, want):  # noqa: F811
+    a = {**dict(w=W, rows=4, K=64, group=32, q=X, scale=Y, values=DW, dtype=BF16), **kw}
+    assert status(moe.moe_quantize_int4, **a) == want
+
+
+def test_linear_int4(lib):  # noqa: F811
+    f, d = moe.moe_linear_int4, moe.linear_desc(4, 512, 256, BF16)
+    q, s, b, r = DY, DX, DW, OFF
+    for group in (0, 16, 96, 256, -32):
+        assert status(f, d, group, X, q, s, b, r, Y, ws()) == INVALID
+    for kw, want in ((dict(K=264), SHAPE), (dict(dtype=moe.MOE_DTYPE_E4M3), INVALID),
+                     (dict(T=-1), SHAPE), (dict(N=260), SHAPE), (dict(act=9), INVALID)):
+        e = moe.linear_desc(**{**dict(T=4, N=512, K=256, dtype=BF16), **kw})
+        assert status(f, e, 32, X, q, s, b, r, Y, ws()) == want, kw
+    for bad in ((None, q, s, b, r, Y), (X, None, s, b, r, Y), (X, q, None, b, r, Y),
+                (X, q, s, b, r, None), (X + 2, q, s, b, r, Y), (X, q + 4, s, b, r, Y),
+                (X, q, s + 2, b, r, Y), (X, q, s, b + 2, r, Y), (X, q, s, b, r + 8, Y),
+                (X, q, s, b, r, X), (X, q, s, b, r, q), (X, q, s, b, r, s), (X, q, s, b, r, b)):
+        assert status(f, d, 32, *bad, ws()) == INVALID, bad
+    assert status(f, d, 32, X, q, s, b, r, Y, ws(64)) == SMALL
+    t = moe.linear_desc(4, 512, 256, BF16, y_stride=520)
+    assert status(f, t, 32, X, q, s, b, Y, Y, ws()) == INVALID  # in place, other rows
+
+
+def test_grouped_linear_int4(lib):  # noqa: F811
+    f, d = moe.moe_grouped_linear_int4, moe.grouped_desc(4, 3, 512, 256, BF16)
+    for group in (0, 48, 512):
+        assert status(f, d, group, X, OFF, W, DW, Y, ws()) == INVALID
+    for kw, want in ((dict(K=264), SHAPE), (dict(R=(1 << 20) + 1), SHAPE), (dict(E=0), SHAPE)):
+        e = moe.grouped_desc(**{**dict(R=4, E=3, N=512, K=256, dtype=BF16), **kw})
+        assert status(f, e, 32, X, OFF, W, DW, Y, ws()) == want
+    for bad in ((None, OFF, W, DW, Y), (X, None, W, DW, Y), (X, OFF, None, DW, Y),
+                (X, OFF, W, None, Y), (X, OFF, W, DW, None), (X, OFF, W + 8, DW, Y),
+                (X, OFF, W, DW, X), (X, OFF, W, DW, W), (X, OFF, W, DW, DW), (X, OFF, W, DW, OFF)):
+        assert status(f, d, 64, *bad, ws()) == INVALID, bad
+    assert status(f, d, 64, X, OFF, W, DW, Y, ws(512)) == SMALL

@@ -3,8 +3,11 @@
 // argument are in include/moe.h.
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "api_util.cuh"
 #include "dense.cuh"
+#include "int4.cuh"
 
 namespace moe {
 
@@ -44,7 +47,8 @@ moe_status_t norm_desc(const moe_norm_desc_t *in, moe_norm_desc_t *d) {
   return MOE_OK;
 }
 
-// After the status block: dz and the column partials of the gradient.
+// After the status block: dz and the column partials of the gradient, or the partial
+// sums of the product with 4-bit weights.
 struct LinearWs {
   size_t dz, part, total;
 };
@@ -53,7 +57,8 @@ LinearWs linear_ws(const moe_linear_desc_t &d) {
   w.dz = w.part = w.total = kStatusPad;
   if (d.dtype == MOE_DTYPE_E4M3) return w;  // no gradient
   w.part += d.act == MOE_ACT_NONE ? 0 : pad((size_t)d.T * d.N * 2);
-  w.total = w.part + pad((size_t)act_grad_slices(d.T, d.N) * d.N * 4);
+  w.total = std::max(w.part + pad((size_t)act_grad_slices(d.T, d.N) * d.N * 4),
+                     kStatusPad + pad(int4_part_bytes(d.T)));
   return w;
 }
 

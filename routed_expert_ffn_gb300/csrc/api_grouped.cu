@@ -2,6 +2,7 @@
 // launches of each call.  Declarations and the meaning of every argument are in
 // include/moe.h.
 #include <stdint.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -36,7 +37,7 @@ GroupedWs grouped_ws(const moe_grouped_desc_t &d) {
   GroupedWs w;
   w.maps = kStatusPad;
   w.part = w.maps + pad(grouped_map_bytes(d.E));
-  w.total = w.part + pad(grouped_part_bytes(d.R));
+  w.total = w.part + pad(std::max(grouped_part_bytes(d.R), int4_part_bytes(d.R)));
   return w;
 }
 
@@ -65,6 +66,11 @@ GroupedGemm grouped_product(const moe_grouped_desc_t &d, const int32_t *offsets,
 }
 
 bool ok_group(int32_t group) { return group == 32 || group == 64 || group == 128; }
+
+cudaError_t launch_int4(const Int4Gemm &g, cudaStream_t s) {
+  const char *p = getenv("I4");
+  return p != nullptr && *p == 's' ? launch_int4_small(g, s) : launch_int4_tc(g, s);
+}
 
 bool ok_offsets(const int32_t *p) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
@@ -183,8 +189,9 @@ moe_status_t moe_linear_int4(const moe_linear_desc_t *in, int32_t group, const v
   g.ldx = d.x_stride;
   g.ldr = d.residual_stride;
   g.ldy = d.y_stride;
+  g.part = reinterpret_cast<float *>(at(workspace, kStatusPad));
   g.status = static_cast<uint32_t *>(workspace);
-  return cuda_status(launch_int4_small(g, (cudaStream_t)stream));
+  return cuda_status(launch_int4(g, (cudaStream_t)stream));
 }
 
 moe_status_t moe_grouped_linear_int4(const moe_grouped_desc_t *in, int32_t group, const void *x,
@@ -218,8 +225,9 @@ moe_status_t moe_grouped_linear_int4(const moe_grouped_desc_t *in, int32_t group
   g.y = y;
   g.ldx = d.x_stride;
   g.ldy = d.y_stride;
+  g.part = reinterpret_cast<float *>(at(workspace, grouped_ws(d).part));
   g.status = static_cast<uint32_t *>(workspace);
-  return cuda_status(launch_int4_small(g, (cudaStream_t)stream));
+  return cuda_status(launch_int4(g, (cudaStream_t)stream));
 }
 
 }  // extern "C"

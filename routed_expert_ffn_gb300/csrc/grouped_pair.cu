@@ -27,6 +27,7 @@
 // warp 8 TMA, warp 9 TMEM allocation and, in the even CTA, the MMAs.  Every wait is
 // bounded; on expiry the CTA latches the status bit and leaves its loops.
 #include <algorithm>
+#include <type_traits>
 
 #include "grouped.cuh"
 #include "pair_tile.cuh"
@@ -89,85 +90,30 @@ struct GroupedArgs {
   uint32_t *counters, *status;
 };
 
-struct Work {
-  int e;
-  int a0;      // first of M
-  int b0;      // first row, or column of dW
-  int n;       // rows, or columns, of the tile
-  int k0, k1;  // stages
-  int parts, part, tile;
-};
+typedef RowSchedule<kTileN, 32, kTileM, kMaxParts, kMinPart> RowTiles;
 
-__device__ __forceinline__ int row_tiles(int m) { return (m + kTileN - 1) / kTileN; }
-
-// The tiles of a launch as a cluster sees them.
-template <int kMode>
-struct Schedule {
-  const int32_t *seg, *first;  // [E+1] offsets and tile prefix sums (shared memory)
+// The weight gradient's tiles: whole ones, in turn.
+struct WeightTiles {
+  const int32_t *seg, *first;
   int E, mt, nt, bn, N, nkb;
-  int total, rem, units, cid, ncl;  // rem: tiles dealt out in stages, `units` to a cluster
-  int lo, hi, pieces;               // of this cluster
+  int total, cid, ncl;
+  static constexpr int pieces = 0;
 
-  __device__ __forceinline__ void start() {
-    total = first[E];
-    rem = 0;
-    pieces = 0;
-    if (kMode == kWeightGrad) return;
-    rem = total % ncl;
-    if (rem == 0) return;
-    units = max((rem * nkb + ncl - 1) / ncl, max((nkb + kMaxParts - 1) / kMaxParts, min(kMinPart, nkb)));
-    if (nkb - units < kMinPart) units = nkb;
-    lo = min(rem * nkb, cid * units);
-    hi = min(rem * nkb, lo + units);
-    if (hi > lo) pieces = (hi - 1) / nkb - lo / nkb + 1;
-  }
-  // Where cluster c keeps its partial sums of tile t.
-  __device__ __forceinline__ int slot(int c, int t) const { return 2 * c + t - c * units / nkb; }
-  __device__ __forceinline__ int first_cluster(int t) const { return t * nkb / units; }
-
+  __device__ __forceinline__ void start() { total = first[E]; }
   __device__ __forceinline__ bool at(int i, Work *w) const {
-    int tile;
+    const int tile = i * ncl + cid;
+    if (tile >= total) return false;
+    const int e = expert_of(first, E, tile);
+    const int at = tile - first[e], m = at / nt, n = at - m * nt;
+    w->e = e;
+    w->tile = tile;
     w->part = 0;
     w->parts = 1;
-    if (i < pieces) {
-      tile = lo / nkb + i;
-      w->k0 = max(lo - tile * nkb, 0);
-      w->k1 = min(hi - tile * nkb, nkb);
-      const int c = first_cluster(tile);
-      w->part = cid - c;
-      w->parts = ((tile + 1) * nkb - 1) / units - c + 1;
-    } else {
-      tile = rem + (i - pieces) * ncl + cid;
-      if (tile >= total) return false;
-      w->k0 = 0;
-      w->k1 = nkb;
-    }
-    w->tile = tile;
-    int l = 0, r = E;  // first[l] <= tile < first[r]
-    while (r - l > 1) {
-      const int mid = (l + r) >> 1;
-      if (first[mid] <= tile)
-        l = mid;
-      else
-        r = mid;
-    }
-    const int at = tile - first[l], m = seg[l + 1] - seg[l];
-    w->e = l;
-    if (kMode == kWeightGrad) {
-      const int i = at / nt, j = at - i * nt;
-      w->a0 = i * kTileM;
-      w->b0 = j * bn;
-      w->n = min(bn, N - w->b0);
-      w->k1 = (m + kBK - 1) / kBK;
-    } else {
-      // the row tiles of one stretch of the matrix follow each other: they run together
-      const int rt = row_tiles(m);
-      const int j = at / rt, i = at - j * rt;
-      const int per = ((m + rt - 1) / rt + 31) & ~31;  // (rt - 1) per < m, as per <= 256
-      w->a0 = j * kTileM;
-      w->b0 = seg[l] + i * per;
-      w->n = min(per, m - i * per);
-    }
+    w->a0 = m * kTileM;
+    w->b0 = n * bn;
+    w->n = min(bn, N - w->b0);
+    w->k0 = 0;
+    w->k1 = (seg[e + 1] - seg[e] + kBK - 1) / kBK;
     return true;
   }
 };
@@ -260,52 +206,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  bool good = true;
-  for (int i = threadIdx.x; i <= a.E; i += kThreads) {
-    const int o = __ldg(a.offsets + i), before = i > 0 ? __ldg(a.offsets + i - 1) : 0;
-    seg[i] = o;
-    good = good && before >= 0 && o >= before && o <= a.R;
-  }
-  good = __syncthreads_and(good);
-  if (warp == 0) {
-    // tiles of each expert -> prefix sums, a run of experts to a lane
-    auto tiles = [&](int e) {
-      const int m = seg[e + 1] - seg[e];
-      if (kWeights) return m > 0 || !a.accumulate ? a.mt * a.nt : 0;
-      return row_tiles(m) * a.mt;
-    };
-    const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
-    int sum = 0;
-    if (good)
-      for (int e = e0; e < e1; ++e) sum += tiles(e);
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    int run = incl - sum;
-    for (int e = e0; e < e1; ++e) {
-      first[e] = run;
-      if (good) run += tiles(e);
-    }
-    if (lane == 31) first[a.E] = incl;
-    if (!good && lane == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusBadOffsets);
-  }
+  make_tables(a.offsets, a.E, a.R, seg, first, a.status, [&](int m) {
+    if (kWeights) return m > 0 || !a.accumulate ? a.mt * a.nt : 0;
+    return RowTiles::row_tiles(m) * a.mt;
+  });
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  Schedule<kMode> sch;
+  typename std::conditional<kWeights, WeightTiles, RowTiles>::type sch;
   sch.seg = seg;
   sch.first = first;
   sch.E = a.E;
   sch.mt = a.mt;
-  sch.nt = a.nt;
-  sch.bn = a.bn;
-  sch.N = a.N;
   sch.nkb = a.nkb;
+  if constexpr (kWeights) {
+    sch.nt = a.nt;
+    sch.bn = a.bn;
+    sch.N = a.N;
+  }
   sch.cid = blockIdx.x >> 1;
   sch.ncl = gridDim.x >> 1;
   sch.start();
@@ -447,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + buf * kTileN;
       const int m0 = w.a0 + (int)rank * kBM + quad * 32;
-      if (kWeights) {
+      if constexpr (kWeights) {
         const bool wide = a.out_dtype == MOE_DTYPE_FP32;
         const int cend = m0 < a.M ? w.n : 0;
         for (int c = turn; c < cend; c += 64) {
@@ -476,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *mine = nullptr;
         bool last = true;
         auto place = [&](int part, int c) {
-          const int s = sch.slot(sch.first_cluster(w.tile) + part, w.tile);
+          const int s = sch.slot(sch.first_worker(w.tile) + part, w.tile);
           return a.part + ((size_t)(s * 2 + (int)rank) * a.part_chunks + c / 32) * (kBM * 32) +
                  quad * 1024 + lane * 4;
         };

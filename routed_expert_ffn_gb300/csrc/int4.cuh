@@ -21,10 +21,13 @@ struct Int4Gemm {
   const void *bias, *residual;
   void *y;
   int64_t ldx, ldr, ldy;
+  float *part;  // int4_part_bytes(T): partial sums of split tiles
   uint32_t *status;
 };
 
 cudaError_t launch_int4_small(const Int4Gemm &g, cudaStream_t s);
+cudaError_t launch_int4_tc(const Int4Gemm &g, cudaStream_t s);
+size_t int4_part_bytes(int T);
 
 // codes, scales and (not null) the values that they stand for, of w [rows][K].
 cudaError_t launch_quantize_int4(const void *w, int dtype, int64_t rows, int K, int group,

@@ -48,7 +48,7 @@ moe_status_t norm_desc(const moe_norm_desc_t *in, moe_norm_desc_t *d) {
 }
 
 // After the status block: dz and the column partials of the gradient, or the partial
-// sums of the product with 4-bit weights.
+// sums and rows of the product with 4-bit weights.
 struct LinearWs {
   size_t dz, part, total;
 };
@@ -58,7 +58,7 @@ LinearWs linear_ws(const moe_linear_desc_t &d) {
   if (d.dtype == MOE_DTYPE_E4M3) return w;  // no gradient
   w.part += d.act == MOE_ACT_NONE ? 0 : pad((size_t)d.T * d.N * 2);
   w.total = std::max(w.part + pad((size_t)act_grad_slices(d.T, d.N) * d.N * 4),
-                     kStatusPad + pad(int4_part_bytes(d.T)));
+                     kStatusPad + pad(int4_part_bytes(d.T)) + pad(int4_rows_bytes(d.T, d.K)));
   return w;
 }
 

@@ -2,7 +2,6 @@
 // launches of each call.  Declarations and the meaning of every argument are in
 // include/moe.h.
 #include <stdint.h>
-#include <stdlib.h>
 
 #include <algorithm>
 
@@ -29,15 +28,17 @@ moe_status_t grouped_desc(const moe_grouped_desc_t *in, moe_grouped_desc_t *d) {
   return MOE_OK;
 }
 
-// After the status block: the weight gradient's tensor maps, then partial sums.
+// After the status block: the weight gradient's tensor maps, then partial sums, then the
+// rows of the products with 4-bit weights.
 struct GroupedWs {
-  size_t maps, part, total;
+  size_t maps, part, rows, total;
 };
 GroupedWs grouped_ws(const moe_grouped_desc_t &d) {
   GroupedWs w;
   w.maps = kStatusPad;
   w.part = w.maps + pad(grouped_map_bytes(d.E));
-  w.total = w.part + pad(std::max(grouped_part_bytes(d.R), int4_part_bytes(d.R)));
+  w.rows = w.part + pad(std::max(grouped_part_bytes(d.R), int4_part_bytes(d.R)));
+  w.total = w.rows + pad(int4_rows_bytes(d.R, d.K));
   return w;
 }
 
@@ -67,9 +68,23 @@ GroupedGemm grouped_product(const moe_grouped_desc_t &d, const int32_t *offsets,
 
 bool ok_group(int32_t group) { return group == 32 || group == 64 || group == 128; }
 
-cudaError_t launch_int4(const Int4Gemm &g, cudaStream_t s) {
-  const char *p = getenv("I4");
-  return p != nullptr && *p == 's' ? launch_int4_small(g, s) : launch_int4_tc(g, s);
+// `rows`: int4_rows_bytes of the workspace.  Up to eight rows of one matrix by the kernel
+// that multiplies where it unpacks, others by way of tcgen05: 14336 x 4096 with 8 rows 14.7
+// and 19.1 us, 114688 x 4096 53 and 74, 14336 x 4096 with 16 rows 25 and 18.7.
+cudaError_t launch_int4(Int4Gemm g, void *rows, cudaStream_t s) {
+  const bool small = g.offsets == nullptr && g.T <= kInt4SmallRows;
+  if (small && int4_staged(g)) return launch_int4_small(g, s);
+  float *factor = reinterpret_cast<float *>(at(rows, (size_t)std::min(g.T, kInt4Rows) * int4_pitch(g.K) * 2));
+  g.xr = rows;
+  g.factor = factor;
+  g.part_bytes = int4_part_bytes(g.T);
+  cudaError_t e = cudaSuccess;
+  for (g.first = 0; g.first < g.T && e == cudaSuccess; g.first += kInt4Rows) {
+    e = launch_int4_rows(static_cast<const uint16_t *>(g.x) + g.first * g.ldx, g.ldx, g.dtype,
+                         std::min(kInt4Rows, g.T - g.first), g.K, rows, factor, s);
+    if (e == cudaSuccess) e = small ? launch_int4_small(g, s) : launch_int4_tc(g, s);
+  }
+  return e;
 }
 
 bool ok_offsets(const int32_t *p) {
@@ -191,7 +206,8 @@ moe_status_t moe_linear_int4(const moe_linear_desc_t *in, int32_t group, const v
   g.ldy = d.y_stride;
   g.part = reinterpret_cast<float *>(at(workspace, kStatusPad));
   g.status = static_cast<uint32_t *>(workspace);
-  return cuda_status(launch_int4(g, (cudaStream_t)stream));
+  void *rows = at(workspace, kStatusPad + pad(int4_part_bytes(d.T)));
+  return cuda_status(launch_int4(g, rows, (cudaStream_t)stream));
 }
 
 moe_status_t moe_grouped_linear_int4(const moe_grouped_desc_t *in, int32_t group, const void *x,
@@ -227,7 +243,7 @@ moe_status_t moe_grouped_linear_int4(const moe_grouped_desc_t *in, int32_t group
   g.ldy = d.y_stride;
   g.part = reinterpret_cast<float *>(at(workspace, grouped_ws(d).part));
   g.status = static_cast<uint32_t *>(workspace);
-  return cuda_status(launch_int4(g, (cudaStream_t)stream));
+  return cuda_status(launch_int4(g, at(workspace, grouped_ws(d).rows), (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -48,12 +48,13 @@ __device__ __forceinline__ int expert_of(const int32_t *first, int E, int tile) 
   return l;
 }
 
-// The offsets (null: all T rows of one matrix) to seg [E+1], and the prefix sums of
+// The offsets (null: all T rows of one matrix), as far as they lie in rows [low, high), to seg [E+1], and the prefix sums of
 // tiles(rows of an expert) to first [E+1], in shared memory; by all threads of the
 // block, which meet afterwards.  Offsets that do not hold make no tiles, and a status bit.
 template <typename Tiles>
-__device__ __forceinline__ void make_tables(const int32_t *offsets, int E, int T, int32_t *seg,
-                                            int32_t *first, uint32_t *status, Tiles tiles) {
+__device__ __forceinline__ void make_tables(const int32_t *offsets, int E, int T, int low, int high,
+                                            int32_t *seg, int32_t *first, uint32_t *status,
+                                            Tiles tiles) {
   bool good = true;
   for (int i = threadIdx.x; i <= E; i += blockDim.x) {
     int o = i == 0 ? 0 : T;
@@ -62,7 +63,7 @@ __device__ __forceinline__ void make_tables(const int32_t *offsets, int E, int T
       o = __ldg(offsets + i);
       good = good && before >= 0 && o >= before && o <= T;
     }
-    seg[i] = o;
+    seg[i] = min(max(o, low), high);
   }
   good = __syncthreads_and(good);
   if (threadIdx.x < 32) {

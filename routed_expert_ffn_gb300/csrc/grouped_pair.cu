@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  make_tables(a.offsets, a.E, a.R, seg, first, a.status, [&](int m) {
+  make_tables(a.offsets, a.E, a.R, 0, a.R, seg, first, a.status, [&](int m) {
     if (kWeights) return m > 0 || !a.accumulate ? a.mt * a.nt : 0;
     return RowTiles::row_tiles(m) * a.mt;
   });

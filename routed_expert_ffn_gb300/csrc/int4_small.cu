@@ -1,27 +1,26 @@
-// Products with 4-bit weights and few rows (decode): y = act(x W^T + bias) + residual of
-// one matrix, or y_p = W_e x_p for the rows p of each expert e.
+// Products with 4-bit weights and up to eight rows (decode): y = act(x W^T + bias) + residual.
 //
-// Bound: HBM, which reads half a byte for each weight; next to it the instructions
-// that unpack the codes (a word of eight takes three shifts, four LOP3 and four
-// subtractions), so every weight is unpacked once for all rows of a pass.
+// Bound: HBM, which reads half a byte for each weight; next to it the instructions that
+// unpack the codes, nine for a word of eight (int4.cuh).  Every weight is unpacked once
+// for all rows and multiplied in the warp that loaded it, by mma.sync (16 rows of W by 16
+// of depth by 8 rows of x, two clocks): a way through TMEM would only add to it
+// (int4_tc.cu).  A group's sum is scaled in fp32 when it is complete: neither codes nor
+// scales are rounded.
 //
-// Two codes become the two halves of a 32-bit register: masked, and given the
-// exponent under which their bits count ones (bf16 128 + code, fp16 1024 + code); less
-// 128 + 8 that is code - 8, exactly.  They are the A operand of mma.sync (16 rows of W
-// by 16 of depth), x is B (8 rows of x): with one to 16 rows the tensor cores of
-// tcgen05 would wait for the unpacking all the same, and its operands would have to
-// go through shared or tensor memory.  A group's sum is scaled in fp32 when it is
-// complete: neither codes nor scales are rounded.
+// Which k an operand element is does not matter as long as A and B agree.  A warp takes 16
+// rows of W by chunks of 128 columns, a quad of lanes a row of W: nibbles j and j + 4 of
+// a word, and x's elements j and j + 4 of the same eight, go together.  Each MMA must see
+// one group alone: the lanes of a quad take words so that it does.
 //
-// Which k an operand element is does not matter as long as A and B agree.  A lane
-// takes 16 bytes of a row as they lie (32 codes): lane t of a quad those at
-// 32 t of a chunk of 128; word i of them, nibbles j and j + 4, pairs with x's elements
-// j and j + 4 of the same eight.  Groups of 32 or 64 end inside a chunk: the
-// lanes of a quad exchange words so that each MMA sees one group alone.
+// One CTA of 16 warps on each SM.  It takes tiles of 16 kWarpRows rows of W: the warps that
+// share rows split the depth by chunks and add their sums through shared memory.  Each warp
+// has kAhead chunks of codes (8 KB) on their way to a ring of its own in shared memory, across
+// tiles as well, the first of them before it looks at x; with loads to registers, four
+// chunks ahead, 114688 x 4096 with 8 rows took 59 us instead of 53.
 //
-// A CTA takes tiles of 16 kWarpRows rows of W: warps split the depth by chunks, each
-// with kAhead chunks of codes in flight in registers, across tiles as well, and
-// add their sums through shared memory.
+// x is taken as int4_rows.cu makes it (fp16, a power of two for each row).  Where the rows
+// fit, kStaged, every CTA makes them for itself while its first codes are under way, which
+// saves a launch.
 #include <algorithm>
 
 #include "int4.cuh"
@@ -30,88 +29,32 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAhead = 4;
+constexpr int kAhead = 8;  // chunks of codes under way for a warp
 constexpr int kChunk = 128;
+constexpr int kRows = kInt4SmallRows;
+constexpr size_t kStagedBytes = 72 << 10;
+constexpr uint32_t kRingBytes = kWarps * kAhead * 1024;
 
 struct SmallArgs {
-  const int32_t *offsets;
-  int T, E, N, K;
-  int row_blocks;  // tiles of a matrix
-  int chunks, groups;
+  int T, N, K;
+  int tiles;
+  int chunks, groups, pitch;
   int dtype, out_dtype, act;
-  const uint8_t *x;
+  const uint8_t *x;  // kStaged: x itself, else the rows made
+  const float *factor;
   const uint8_t *q;
   const uint16_t *scale;
   const void *bias, *residual;
   void *y;
   int64_t ldx, ldr, ldy;
-  uint32_t *status;
 };
 
-template <bool kFp16>
-__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
-  uint32_t d;
-  if (kFp16)
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// Nibbles j and j + 4 of a word as two numbers: (j = 0..3) of p[j].
-template <bool kFp16>
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t (&p)[4]) {
-  constexpr uint32_t kOne = kFp16 ? 0x64006400u : 0x43004300u;   // 1024 or 128, twice
-  constexpr uint32_t kZero = kFp16 ? 0x64086408u : 0x43084308u;  // 8 more
-#pragma unroll
-  for (int j = 0; j < 4; ++j) p[j] = minus<kFp16>((w >> (4 * j) & 0x000f000fu) | kOne, kZero);
-}
-template <bool kFp16>
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-  if (kFp16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
-  return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
+__device__ __forceinline__ void copy_codes(uint32_t to, const uint8_t *from) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
-// Words of a quad's four lanes exchanged so that word i of every lane is of one group
-// (kGroup 32: of group i; 64: words 0 and 1 of group 0, 2 and 3 of group 1).
-template <int kGroup>
-__device__ __forceinline__ void regroup(uint4 &v, int t) {
-  if (kGroup == 128) return;
-  // lanes t and t ^ 2 exchange two words
-  {
-    const bool high = (t & 2) != 0;
-    const uint32_t a = __shfl_xor_sync(0xffffffffu, high ? v.x : v.z, 2);
-    const uint32_t b = __shfl_xor_sync(0xffffffffu, high ? v.y : v.w, 2);
-    v = high ? make_uint4(a, b, v.z, v.w) : make_uint4(v.x, v.y, a, b);
-  }
-  if (kGroup == 32) {
-    // and lanes t and t ^ 1 one of each two
-    const bool odd = (t & 1) != 0;
-    const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
-    const uint32_t b = __shfl_xor_sync(0xffffffffu, odd ? v.z : v.w, 1);
-    v = odd ? make_uint4(a, v.y, b, v.w) : make_uint4(v.x, a, v.z, b);
-  }
-}
 // The first of the eight k in a chunk that word i of lane t stands for after regroup.
 template <int kGroup>
 __device__ __forceinline__ int k_of(int t, int i) {
@@ -124,288 +67,309 @@ __device__ __forceinline__ int k_of(int t, int i) {
   return 32 * i + 8 * t;  // group i, its word t
 }
 
-// One tile: 16 rows of W for each of kWarpRows warps, up to 8 kN rows of x.
-struct SmallTile {
-  int e, n0, row0, rows;
-};
+// Bytes of a staged row: four pieces of 64 bytes (word i of lanes 0 to 3) for each chunk,
+// and 64 more, so that two rows' pieces lie in different banks.
+__host__ __device__ constexpr int staged_pitch(int chunks) { return chunks * 256 + 64; }
 
-template <int kN, int kWarpRows>
-struct SmallTiles {
-  const int32_t *seg, *first;  // [E+1] (shared memory); null: one matrix
-  int E, T, row_blocks, total;
-  __device__ __forceinline__ SmallTile at(int tile) const {
-    SmallTile t;
-    int l = 0, begin = 0, end = T, base = 0;
-    if (seg != nullptr) {
-      int r = E;
-      while (r - l > 1) {
-        const int mid = (l + r) >> 1;
-        if (first[mid] <= tile)
-          l = mid;
-        else
-          r = mid;
-      }
-      begin = seg[l];
-      end = seg[l + 1];
-      base = first[l];
-    }
-    // the passes over one stretch of W follow each other
-    const int passes = (end - begin + 8 * kN - 1) / (8 * kN);
-    const int at = tile - base, block = at / passes, pass = at - block * passes;
-    t.e = l;
-    t.n0 = block * 16 * kWarpRows;
-    t.row0 = begin + pass * 8 * kN;
-    t.rows = min(8 * kN, end - t.row0);
-    return t;
+// The T rows of x to shared memory as launch_int4_rows makes them, in that order; their
+// factors to `factor`.  The warps share the rows evenly.
+template <int kGroup>
+__device__ __forceinline__ void stage_rows(const SmallArgs &a, uint8_t *to, float *factor,
+                                           float *most) {
+  const int per = a.T == 1 ? kWarps : (a.T == 2 ? kWarps / 2 : (a.T <= 4 ? kWarps / 4 : kWarps / 8));
+  const int warp = threadIdx.x >> 5, r = warp / per, first = warp % per * 32 + (threadIdx.x & 31);
+  const bool mine = r < a.T;
+  const uint4 *row = reinterpret_cast<const uint4 *>(a.x + (int64_t)(mine ? r : 0) * a.ldx * 2);
+  float up = 1.f;
+  if (a.dtype == MOE_DTYPE_BF16) {
+    float m = 0.f;
+    if (mine)
+#pragma unroll 4
+      for (int c = first; c < a.K / 8; c += per * 32) m = fmaxf(m, finite_max_bf16(__ldg(row + c)));
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    if ((threadIdx.x & 31) == 0) most[warp] = m;
+    __syncthreads();
+    for (int i = 0; i < per; ++i) m = fmaxf(m, most[warp / per * per + i]);
+    const RowFactor f = row_factor(m);
+    up = f.up;
+    if (mine && first == 0) factor[r] = f.back;
+  } else if (mine && first == 0) {
+    factor[r] = 1.f;
   }
-};
+  if (!mine) return;
+  to += r * staged_pitch(a.chunks);
+#pragma unroll 4
+  for (int p = first; p < a.chunks * 16; p += per * 32) {
+    const int c = p >> 4, i = (p >> 2) & 3, t = p & 3;
+    const int k = c * kChunk + k_of<kGroup>(t, i);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (k < a.K) v = __ldg(row + k / 8);
+    *reinterpret_cast<uint4 *>(to + c * 256 + i * 64 + t * 16) = row_piece(v, a.dtype, up);
+  }
+}
 
-// The tile's sums of all warps, then everything after them, rounded once.
-template <int kN, int kWarpRows>
-__device__ __noinline__ void finish(const SmallArgs &a, const SmallTile &t, const float *red) {
-  constexpr int kCols = 16 * kWarpRows, kRows = 8 * kN, kSplit = kWarps / kWarpRows;
-  for (int i = threadIdx.x; i < kCols * kRows; i += kThreads) {
-    const int c = i % kCols, r = i / kCols;
-    if (r >= t.rows || t.n0 + c >= a.N) continue;
+// y of the column n of W and the row `row` of x.
+__device__ __forceinline__ void store(const SmallArgs &a, float v, int n, int64_t row) {
+  const bool wide = a.out_dtype == MOE_DTYPE_FP32;
+  auto load = [&](const void *p, int64_t at) {
+    return wide ? static_cast<const float *>(p)[at]
+                : unpack16(a.out_dtype, static_cast<const uint16_t *>(p)[at]).x;
+  };
+  if (a.bias != nullptr) v += load(a.bias, n);
+  if (a.act != MOE_ACT_NONE) v = wide ? activate<true>(a.act, v) : activate<false>(a.act, v);
+  if (a.residual != nullptr) v += load(a.residual, row * a.ldr + n);
+  if (wide)
+    static_cast<float *>(a.y)[row * a.ldy + n] = v;
+  else
+    static_cast<uint16_t *>(a.y)[row * a.ldy + n] = (uint16_t)pack16(a.out_dtype, v, 0.f);
+}
+
+// Sums of columns [from, from + cols) of the tile at n0, everything after them, and the
+// rounding, by `threads` threads; a function of its own, as it is not worth a copy in each
+// place.
+template <int kWarpRows>
+__device__ __noinline__ void finish(const SmallArgs &a, int n0, const float *red,
+                                    const float *factors, int from, int cols, int thread,
+                                    int threads) {
+  constexpr int kCols = 16 * kWarpRows, kSplit = kWarps / kWarpRows;
+  for (int j = thread; j < cols * a.T; j += threads) {
+    const int c = from + j % cols, r = j / cols, n = n0 + c;
     float v = 0.f;
 #pragma unroll
     for (int s = 0; s < kSplit; ++s) v += red[(s * kRows + r) * (kCols + 1) + c];
-    const int n = t.n0 + c;
-    const int64_t row = t.row0 + r;
-    auto load = [&](const void *p, int64_t at) {
-      if (a.out_dtype == MOE_DTYPE_FP32) return static_cast<const float *>(p)[at];
-      return unpack16(a.out_dtype, static_cast<const uint16_t *>(p)[at]).x;
-    };
-    if (a.bias != nullptr) v += load(a.bias, n);
-    if (a.act != MOE_ACT_NONE)
-      v = a.out_dtype == MOE_DTYPE_FP32 ? activate<true>(a.act, v) : activate<false>(a.act, v);
-    if (a.residual != nullptr) v += load(a.residual, row * a.ldr + n);
-    if (a.out_dtype == MOE_DTYPE_FP32)
-      static_cast<float *>(a.y)[row * a.ldy + n] = v;
-    else
-      static_cast<uint16_t *>(a.y)[row * a.ldy + n] = (uint16_t)pack16(a.out_dtype, v, 0.f);
+    if (n < a.N) store(a, v * factors[r], n, r);
   }
 }
 
-template <bool kFp16, int kGroup, int kN, int kWarpRows>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int kGroup, int kWarpRows, bool kStaged>
+__global__ void __launch_bounds__(kThreads, 1)
     int4_small_kernel(const __grid_constant__ SmallArgs a) {
-  constexpr int kCols = 16 * kWarpRows, kRows = 8 * kN, kSplit = kWarps / kWarpRows;
-  constexpr int kRed = kSplit * kRows * (kCols + 1);
-  __shared__ float red[2][kRed];
-  extern __shared__ int32_t tables[];  // offsets: [E+1] and tile prefix sums
+  constexpr int kCols = 16 * kWarpRows, kSplit = kWarps / kWarpRows;
+  __shared__ float red[2][kWarps * kRows * 17];
+  __shared__ float most[kWarps], factors[kRows];
+  extern __shared__ __align__(16) uint8_t dyn[];  // the warps' rings, then x (kStaged)
+  uint8_t *staged = dyn + kRingBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int wr = warp % kWarpRows, part = warp / kWarpRows;
-  pdl_wait();
+  // not kStaged: the launch before this one made the rows of x, and waited for all before
+  // it, so that the codes are there
+  if (kStaged) pdl_wait();
   pdl_launch_dependents();
 
-  SmallTiles<kN, kWarpRows> tiles;
-  tiles.E = a.E;
-  tiles.T = a.T;
-  tiles.row_blocks = a.row_blocks;
-  tiles.seg = nullptr;
-  tiles.first = nullptr;
-  if (a.offsets != nullptr) {
-    int32_t *seg = tables, *first = tables + a.E + 1;
-    bool good = true;
-    for (int i = threadIdx.x; i <= a.E; i += kThreads) {
-      const int o = __ldg(a.offsets + i), before = i > 0 ? __ldg(a.offsets + i - 1) : 0;
-      seg[i] = o;
-      good = good && before >= 0 && o >= before && o <= a.T;
+  // this warp's chunks of a tile, [c0, c0 + count)
+  const int per = (a.chunks + kSplit - 1) / kSplit, c0 = part * per;
+  const int count = max(0, min(per, a.chunks - c0));
+  // In a chunk that K ends in, a lane past K keeps any codes: x is zero there.
+  const bool skips = count > 0 && c0 + count == a.chunks && a.K - (a.chunks - 1) * kChunk <= 32 * t;
+
+  // Codes on their way, across tiles: row g of this warp's 16 and, `down` bytes on, row g + 8.
+  // A lane's 16 bytes lie in the ring where a quad's words can be read without bank conflicts.
+  const uint32_t ring = smem_u32(dyn) + warp * (kAhead * 1024);
+  const uint32_t put = ring + (g * 4 + (t ^ ((g >> 1) & 3))) * 16;
+  int ask_tile = blockIdx.x, to_ask = 0;
+  uint32_t ask_slot = 0;
+  const uint8_t *q = nullptr;
+  int down = 0;
+  auto ask = [&]() {
+    if (to_ask == 0 && count > 0 && ask_tile < a.tiles) {
+      const int n = ask_tile * kCols + 16 * wr + g;
+      const int n0 = min(n, a.N - 1), n1 = min(n + 8, a.N - 1);
+      q = a.q + (int64_t)n0 * (a.K >> 1) + c0 * (kChunk / 2) + 16 * t;
+      down = (n1 - n0) * (a.K >> 1);
+      to_ask = count;
+      ask_tile += gridDim.x;
     }
-    good = __syncthreads_and(good);
-    if (warp == 0) {
-      auto count = [&](int e) { return (seg[e + 1] - seg[e] + kRows - 1) / kRows * a.row_blocks; };
-      const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
-      int sum = 0;
-      if (good)
-        for (int e = e0; e < e1; ++e) sum += count(e);
-      int incl = sum;
+    if (to_ask > 0) {
+      if (to_ask > 1 || !skips) {
+        copy_codes(put + ask_slot, q);
+        copy_codes(put + ask_slot + 512, q + down);
+      }
+      q += kChunk / 2;
+      --to_ask;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ask_slot = (ask_slot + 1024) & (kAhead * 1024 - 1);
+  };
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      int run = incl - sum;
-      for (int e = e0; e < e1; ++e) {
-        first[e] = run;
-        if (good) run += count(e);
-      }
-      if (lane == 31) first[a.E] = incl;
-      if (!good && lane == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusBadOffsets);
+  for (int j = 0; j < kAhead; ++j) ask();
+
+  // Scales, eight groups at a time, one such block ahead: lane l holds four of row l / 2.
+  constexpr int kBlock = 8 * kGroup / kChunk;  // chunks: 8, 4 or 2
+  int scale_tile = blockIdx.x, scale_at = 0;   // group of the warp's range
+  const int range = count > 0 ? min(count * (kChunk / kGroup), a.groups - c0 * (kChunk / kGroup)) : 0;
+  const uint16_t *sc = nullptr;
+  uint32_t next[4] = {};  // (as they come: whatever is done with them waits for them)
+  auto ask_scales = [&]() {
+    if (scale_tile >= a.tiles || range == 0) return;
+    if (scale_at == 0)
+      sc = a.scale + (int64_t)min(scale_tile * kCols + 16 * wr + (lane >> 1), a.N - 1) * a.groups +
+           c0 * (kChunk / kGroup) + (lane & 1) * 4;
+    const int have = range - scale_at - (lane & 1) * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      next[k] = 0;
+      if (k < have) next[k] = __ldg(sc + k);
     }
-    __syncthreads();
-    tiles.seg = seg;
-    tiles.first = first;
-    tiles.total = first[a.E];
+    sc += 8;
+    scale_at += 8;
+    if (scale_at >= range) {
+      scale_at = 0;
+      scale_tile += gridDim.x;
+    }
+  };
+  ask_scales();
+
+  if (kStaged) {
+    stage_rows<kGroup>(a, staged, factors, most);
   } else {
-    tiles.total = (a.T + kRows - 1) / kRows * a.row_blocks;
+    pdl_wait();
+    if (threadIdx.x < a.T) factors[threadIdx.x] = a.factor[threadIdx.x];
   }
+  __syncthreads();
 
-  // this warp's chunks of a tile: part, part + kSplit, ...
-  const int count = part < a.chunks ? (a.chunks - part + kSplit - 1) / kSplit : 0;
-
-  // Where the next codes to be asked for lie.
-  struct Item {
-    uint4 q0, q1;
-    uint32_t s0, s1;
-  };
-  int ahead_tile = blockIdx.x, ahead_i = 0;
-  const uint8_t *q0 = nullptr, *q1 = nullptr;
-  const uint16_t *s0 = nullptr, *s1 = nullptr;
-  auto aim = [&]() {
-    if (ahead_tile >= tiles.total) return;
-    const SmallTile w = tiles.at(ahead_tile);
-    const int n = w.n0 + 16 * wr + g;
-    const int64_t r0 = (int64_t)w.e * a.N + min(n, a.N - 1);
-    const int64_t r1 = (int64_t)w.e * a.N + min(n + 8, a.N - 1);
-    q0 = a.q + r0 * (a.K >> 1) + 16 * t;
-    q1 = a.q + r1 * (a.K >> 1) + 16 * t;
-    s0 = a.scale + r0 * a.groups;
-    s1 = a.scale + r1 * a.groups;
-  };
-  auto ask = [&](Item &it) {
-    if (ahead_tile >= tiles.total) return;
-    const int c = part + ahead_i * kSplit;
-    it.q0 = it.q1 = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-    if (c * kChunk + 32 * t < a.K) {
-      it.q0 = load_codes(q0 + (int64_t)c * (kChunk / 2));
-      it.q1 = load_codes(q1 + (int64_t)c * (kChunk / 2));
-    }
-    const int group = c * (kChunk / kGroup) + (kGroup == 128 ? 0 : (kGroup == 64 ? t >> 1 : t));
-    it.s0 = it.s1 = 0;
-    if (group < a.groups) {
-      it.s0 = __ldg(s0 + group);
-      it.s1 = __ldg(s1 + group);
-    }
-    if (++ahead_i == count) {
-      ahead_i = 0;
-      ahead_tile += gridDim.x;
-      aim();
-    }
-  };
-
-  Item item[kAhead];
-  if (count > 0) {
-    aim();
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) ask(item[j]);
-  }
-  float sum[kN][4];
-#pragma unroll
-  for (int n = 0; n < kN; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
+  const Unpack unpack;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   int tile = blockIdx.x, i = 0;
-  uint32_t turn = 0;
-  SmallTile w = {};
-  if (tile < tiles.total) w = tiles.at(tile);
+  uint32_t turn = 0, slot = 0;
+  // this lane's row of x, from this warp's first chunk on; past the last row the sums are not
+  // used: row 0 will do
+  const int row = g < a.T ? g : 0;
+  const uint8_t *const x0 = kStaged ? staged + row * staged_pitch(a.chunks) + t * 16 + c0 * 256
+                                    : a.x + ((int64_t)row * a.pitch + c0 * kChunk) * 2;
+  const uint8_t *xp = x0;
 
-  // The warp's sums to shared memory; the last warp's arrival completes the tile.
+  // The tile's sums: of this warp alone, or of all that share its rows.
   auto close = [&]() {
     float *to = red[turn] + part * kRows * (kCols + 1) + 16 * wr;
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        to[(8 * n + 2 * t + (k & 1)) * (kCols + 1) + g + 8 * (k >> 1)] = sum[n][k];
-        sum[n][k] = 0.f;
-      }
+    for (int k = 0; k < 4; ++k) {
+      to[(2 * t + (k & 1)) * (kCols + 1) + g + 8 * (k >> 1)] = sum[k];
+      sum[k] = 0.f;
     }
-    __syncthreads();
-    finish<kN, kWarpRows>(a, w, red[turn]);
+    if (kSplit == 1) {
+      __syncwarp();
+      finish<kWarpRows>(a, tile * kCols, red[turn], factors, 16 * wr, 16, lane, 32);
+    } else {
+      __syncthreads();
+      finish<kWarpRows>(a, tile * kCols, red[turn], factors, 0, kCols, threadIdx.x, kThreads);
+    }
     turn ^= 1u;  // the other buffer was read before everybody arrived here
     tile += gridDim.x;
-    if (tile < tiles.total) w = tiles.at(tile);
+    xp = x0;
   };
 
   if (count == 0) {
-    while (tile < tiles.total) close();
+    while (tile < a.tiles) close();
     return;
   }
-  while (tile < tiles.total) {
+  while (tile < a.tiles) {
+    float scales[4];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (tile >= tiles.total) break;
-      const int c = part + i * kSplit;
-      const uint8_t *xp[kN];
+    for (int k = 0; k < 4; ++k) scales[k] = unpack16(a.dtype, next[k]).x;
+    ask_scales();
+    const int have = count - i;  // chunks of the tile from here on
 #pragma unroll
-      for (int n = 0; n < kN; ++n)
-        xp[n] = 8 * n + g < w.rows
-                    ? a.x + ((int64_t)(w.row0 + 8 * n + g) * a.ldx + (int64_t)c * kChunk) * 2
-                    : nullptr;
-      uint4 c0 = item[j].q0, c1 = item[j].q1;
-      const uint32_t sc0 = item[j].s0, sc1 = item[j].s1;
-      regroup<kGroup>(c0, t);
-      regroup<kGroup>(c1, t);
-      ask(item[j]);
-      float part_sum[kN][4];
+    for (int j = 0; j < kBlock; ++j) {
+      if (j < have) {
+        uint4 xv[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4; ++k)
+          xv[k] = kStaged ? *reinterpret_cast<const uint4 *>(xp + k * 64)
+                          : __ldg(reinterpret_cast<const uint4 *>(xp + k_of<kGroup>(t, k) * 2));
+        xp += 256;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncwarp();
+        uint32_t c[2][4];
+        const uint8_t *codes = dyn + warp * (kAhead * 1024) + slot;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t *row = codes + h * 512 + g * 64;
+          const int turned = (g >> 1) & 3;
+          if constexpr (kGroup == 128) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + ((t ^ turned) << 4));
+            c[h][0] = v.x;
+            c[h][1] = v.y;
+            c[h][2] = v.z;
+            c[h][3] = v.w;
+          } else if constexpr (kGroup == 64) {
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(
+                  row + ((((t & 1) | k) ^ turned) << 4) + (t & 2) * 4);
+              c[h][k] = v.x;
+              c[h][k + 1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              c[h][k] = *reinterpret_cast<const uint32_t *>(row + ((k ^ turned) << 4) + t * 4);
+          }
+        }
+        slot = (slot + 1024) & (kAhead * 1024 - 1);
+        // (eight products of one chain after the other would be waited for)
+        constexpr int kChains = kGroup == 128 ? 2 : 1;
         constexpr int kWords = kGroup / 32;  // words to a group
-        if (k % kWords == 0) {
+        float group_sum[kChains][4];
 #pragma unroll
-          for (int n = 0; n < kN; ++n)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) part_sum[n][m] = 0.f;
-        }
-        uint32_t p0[4], p1[4];
-        unpack<kFp16>(word(c0, k), p0);
-        unpack<kFp16>(word(c1, k), p1);
-        const int at = k_of<kGroup>(t, k);
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (xp[n] != nullptr && c * kChunk + at < a.K)
-            v = __ldg(reinterpret_cast<const uint4 *>(xp[n] + at * 2));
-          mma<kFp16>(part_sum[n], p0[0], p1[0], p0[1], p1[1], __byte_perm(v.x, v.z, 0x5410),
-                     __byte_perm(v.x, v.z, 0x7632));
-          mma<kFp16>(part_sum[n], p0[2], p1[2], p0[3], p1[3], __byte_perm(v.y, v.w, 0x5410),
-                     __byte_perm(v.y, v.w, 0x7632));
-        }
-        if (k % kWords == kWords - 1) {
-          // lane t (of its quad) holds the scale of the group that its own codes are of
-          uint32_t u0 = sc0, u1 = sc1;
-          if (kGroup != 128) {
-            const int from = (lane & ~3) | (kGroup == 64 ? (k & 2) : k);
-            u0 = __shfl_sync(0xffffffffu, sc0, from);
-            u1 = __shfl_sync(0xffffffffu, sc1, from);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t p0[4], p1[4];
+          unpack(c[0][k], p0);
+          unpack(c[1][k], p1);
+          if (k % kWords == 0) {
+            mma_first(group_sum[0], p0[0], p1[0], p0[1], p1[1], xv[k].x, xv[k].y);
+            if (kChains == 2)
+              mma_first(group_sum[kChains - 1], p0[2], p1[2], p0[3], p1[3], xv[k].z, xv[k].w);
+            else
+              mma(group_sum[0], p0[2], p1[2], p0[3], p1[3], xv[k].z, xv[k].w);
+          } else {
+            mma(group_sum[0], p0[0], p1[0], p0[1], p1[1], xv[k].x, xv[k].y);
+            mma(group_sum[kChains - 1], p0[2], p1[2], p0[3], p1[3], xv[k].z, xv[k].w);
           }
-          const float f0 = unpack16(kFp16 ? MOE_DTYPE_FP16 : MOE_DTYPE_BF16, u0).x;
-          const float f1 = unpack16(kFp16 ? MOE_DTYPE_FP16 : MOE_DTYPE_BF16, u1).x;
+          if (k % kWords == kWords - 1) {
+            const int gr = j * (kChunk / kGroup) + k / kWords;  // of the block's eight
+            const float f0 = __shfl_sync(0xffffffffu, scales[gr % 4], g * 2 + gr / 4);
+            const float f1 = __shfl_sync(0xffffffffu, scales[gr % 4], g * 2 + 16 + gr / 4);
 #pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            sum[n][0] = fmaf(f0, part_sum[n][0], sum[n][0]);
-            sum[n][1] = fmaf(f0, part_sum[n][1], sum[n][1]);
-            sum[n][2] = fmaf(f1, part_sum[n][2], sum[n][2]);
-            sum[n][3] = fmaf(f1, part_sum[n][3], sum[n][3]);
+            for (int m = 0; m < 4; ++m) {
+              float v = group_sum[0][m];
+              if (kChains == 2) v += group_sum[kChains - 1][m];
+              sum[m] = fmaf(m < 2 ? f0 : f1, v, sum[m]);
+            }
           }
         }
-      }
-      if (++i == count) {
-        i = 0;
-        close();
+        __syncwarp();  // (the words of this slot are read)
+        ask();
       }
     }
+    i += kBlock;
+    if (i >= count) {
+      i = 0;
+      close();
+    }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <bool kFp16, int kGroup, int kN, int kWarpRows>
+template <int kGroup, int kWarpRows, bool kStaged>
 cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
+  auto kern = int4_small_kernel<kGroup, kWarpRows, kStaged>;
+  static std::atomic<bool> allowed[64];
+  const cudaError_t e = allow_smem(kern, kRingBytes + kStagedBytes, allowed);
+  if (e != cudaSuccess) return e;
   SmallArgs a = {};
-  a.offsets = g.offsets;
   a.T = g.T;
-  a.E = g.E;
   a.N = g.N;
   a.K = g.K;
-  a.row_blocks = (g.N + 16 * kWarpRows - 1) / (16 * kWarpRows);
+  a.tiles = (g.N + 16 * kWarpRows - 1) / (16 * kWarpRows);
   a.chunks = (g.K + kChunk - 1) / kChunk;
   a.groups = (g.K + kGroup - 1) / kGroup;
+  a.pitch = int4_pitch(g.K);
   a.dtype = g.dtype;
   a.out_dtype = g.out_dtype;
   a.act = g.act;
-  a.x = static_cast<const uint8_t *>(g.x);
+  a.x = static_cast<const uint8_t *>(kStaged ? g.x : g.xr);
+  a.factor = g.factor;
   a.q = g.q;
   a.scale = static_cast<const uint16_t *>(g.scale);
   a.bias = g.bias;
@@ -414,31 +378,53 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
   a.ldx = g.ldx;
   a.ldr = g.ldr;
   a.ldy = g.ldy;
-  a.status = g.status;
-  const int64_t passes = g.offsets != nullptr ? (int64_t)std::min(g.E, g.T) + g.T / (8 * kN)
-                                              : (g.T + 8 * kN - 1) / (8 * kN);
-  const int64_t most = passes * a.row_blocks;
-  const size_t smem = g.offsets != nullptr ? (size_t)2 * (g.E + 1) * 4 : 0;
-  return launch_pdl(int4_small_kernel<kFp16, kGroup, kN, kWarpRows>,
-                    dim3((unsigned)std::min<int64_t>(most, 2 * (int64_t)num_sms())), dim3(kThreads),
-                    smem, s, a);
+  const size_t smem = kRingBytes + (kStaged ? (size_t)g.T * staged_pitch(a.chunks) : 0);
+  return launch_pdl(kern, dim3((unsigned)std::min(a.tiles, num_sms())), dim3(kThreads), smem, s, a);
 }
 
-template <bool kFp16, int kGroup>
-cudaError_t by_rows(const Int4Gemm &g, cudaStream_t s) {
-  const bool one = g.T <= 8 * g.E;
-  return one ? start<kFp16, kGroup, 1, 1>(g, s) : start<kFp16, kGroup, 2, 2>(g, s);
+// The rows of a tile that take the least time: whole rounds of the SMs' tiles, each as long
+// as its warps' chunks and about 0.6 chunks for its end.
+int warp_rows(const Int4Gemm &g) {
+  const int chunks = (g.K + kChunk - 1) / kChunk;
+  int best = 1;
+  double least = 0;
+  for (int wr = 1; wr <= kWarps; wr *= 2) {
+    const int tiles = (g.N + 16 * wr - 1) / (16 * wr);
+    const int rounds = (tiles + num_sms() - 1) / num_sms();
+    const int split = kWarps / wr;
+    const double us = (double)rounds * ((chunks + split - 1) / split + (split > 1 ? 0.6 : 0.2));
+    if (least == 0 || us < least) {
+      least = us;
+      best = wr;
+    }
+  }
+  return best;
 }
-template <bool kFp16>
+
+template <int kGroup, bool kStaged>
+cudaError_t by_rows(const Int4Gemm &g, cudaStream_t s) {
+  switch (warp_rows(g)) {
+    case 1: return start<kGroup, 1, kStaged>(g, s);
+    case 2: return start<kGroup, 2, kStaged>(g, s);
+    case 4: return start<kGroup, 4, kStaged>(g, s);
+    case 8: return start<kGroup, 8, kStaged>(g, s);
+    default: return start<kGroup, 16, kStaged>(g, s);
+  }
+}
+template <bool kStaged>
 cudaError_t by_group(const Int4Gemm &g, cudaStream_t s) {
-  if (g.group == 32) return by_rows<kFp16, 32>(g, s);
-  return g.group == 64 ? by_rows<kFp16, 64>(g, s) : by_rows<kFp16, 128>(g, s);
+  if (g.group == 32) return by_rows<32, kStaged>(g, s);
+  return g.group == 64 ? by_rows<64, kStaged>(g, s) : by_rows<128, kStaged>(g, s);
 }
 
 }  // namespace
 
+bool int4_staged(const Int4Gemm &g) {
+  return (size_t)g.T * staged_pitch((g.K + kChunk - 1) / kChunk) <= kStagedBytes;
+}
+
 cudaError_t launch_int4_small(const Int4Gemm &g, cudaStream_t s) {
-  return g.dtype == MOE_DTYPE_FP16 ? by_group<true>(g, s) : by_group<false>(g, s);
+  return int4_staged(g) ? by_group<true>(g, s) : by_group<false>(g, s);
 }
 
 }  // namespace moe

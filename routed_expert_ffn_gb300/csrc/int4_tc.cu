@@ -2,8 +2,7 @@
 // bias) + residual of one matrix, or y_p = W_e x_p for the rows p of each expert e.
 //
 // Bound: HBM for few rows, which reads half a byte for each weight.  To keep up an SM
-// turns 48 codes a clock into 16-bit numbers, a good half of what its schedulers issue
-// (13 instructions for a word of eight).  So every weight is unpacked once for all rows of
+// turns 48 codes a clock into 16-bit numbers, nine instructions for a word of eight.  So every weight is unpacked once for all rows of
 // a tile: 128 rows of W are the MMA's M, up to 64 rows of x its N, and the unpacked
 // numbers go to TMEM, where the MMA reads its A operand: through shared memory they would
 // be written and read once more, twice what it moves anyway.
@@ -13,15 +12,15 @@
 // group's scale (a lane is a row of W) and add in fp32 registers.  Neither codes nor scales
 // are rounded, and the tensor cores' truncating additions go over 128 products at most.
 //
-// Depth goes by units of 256 columns (a row's 128 bytes of codes), unpacked in steps of 64
-// (32 TMEM columns of 16-bit pairs) and accumulated in blocks of 128.  Tiles, and the depth
+// Depth goes by units of 256 columns (a row's 128 bytes of codes).  Tiles, and the depth
 // of those that do not fill a round of the SMs, are dealt out as in grouped_pair.cu.
 //
-// CTA = 14 warps, one CTA an SM:
-//   warps 0-3    scale and add the accumulators; the epilogue (32 TMEM lanes each)
-//   warps 4-11   unpack, two sets of four (32 TMEM lanes each), every other step
-//   warp 12      TMA: codes and rows of x
-//   warp 13      TMEM allocation; one thread issues the MMAs
+// CTA = 28 warps, one CTA an SM:
+//   warps 0-7    scale and add the accumulators; the epilogue (32 TMEM lanes each, and
+//                half of the rows of x)
+//   warps 8-23   unpack, four sets of four (32 TMEM lanes each)
+//   warp 24      TMA: codes and rows of x
+//   warp 25      TMEM allocation; one thread issues the MMAs (26 and 27 idle)
 // Every wait is bounded; on expiry the CTA latches the status bit and leaves its loops.
 #include <algorithm>
 
@@ -33,35 +32,39 @@ namespace moe {
 
 namespace {
 
-constexpr int kAddWarps = 4, kUnpackWarps = 8;
+constexpr int kAddWarps = 8, kUnpackWarps = 16;
 constexpr int kTmaWarp = kAddWarps + kUnpackWarps, kMmaWarp = kTmaWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kUnit = 256, kStep = 64, kSteps = kUnit / kStep;
+constexpr int kThreads = 28 * 32;  // (two warps idle: registers move by fours of warps)
+constexpr int kUnit = 256;
 constexpr uint32_t kCodeBytes = kBM * kUnit / 2;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kABufs = 8, kAColsStep = kStep / 2;  // operand: [0, 256)
-constexpr uint32_t kDCol = kABufs * kAColsStep;         // accumulators: [256, 512)
-constexpr int kMaxCtas = 160;  // (a GB300 has 152 SMs)
+constexpr uint32_t kDCol = 256;  // operands: TMEM columns [0, 256), accumulators: [256, 512)
+constexpr int kMaxCtas = 160;    // (a GB300 has 152 SMs)
 constexpr int kMaxParts = 16;
 
-// Rows of x of a tile at most, and where the accumulators of a block lie: one for each
-// group, kGroup columns apart.
+// Rows of x of a tile at most (kN), and how depth is handed from one group of warps to
+// the next: in blocks of `block` columns, unpacked into one of `bufs` operand buffers
+// and accumulated into one of as many, where each group of columns has kN columns.
+// A hand-over costs about 250 clocks whatever it hands over, and HBM brings 128 x 256
+// codes in 680: blocks are as large as TMEM holds twice.
 template <int kGroup, int kN>
 struct Shape {
-  static constexpr int x_step = kN * kStep * 2;  // bytes of x for one step
-  static constexpr uint32_t stage = kCodeBytes + kSteps * x_step;
+  static constexpr int x_box = kN * 128;  // bytes of 64 columns of x
+  static constexpr uint32_t stage = kCodeBytes + kUnit / 64 * x_box;
   static constexpr int stages = kN == 16 ? 8 : (kN == 32 ? 6 : 4);
-  static constexpr uint32_t d_cols = kGroup == 128 ? 64 : 128;  // of a block
-  static constexpr uint32_t d_bufs = (kTmemCols - kDCol) / d_cols;
-  static constexpr int groups = 128 / kGroup;  // of a block
-  static_assert(kN <= kGroup && kN <= 64, "accumulator columns");
+  static constexpr int block = 256 / kGroup * kN <= 128 ? 256 : 128;
+  static constexpr int blocks = kUnit / block;     // of a unit
+  static constexpr int groups = block / kGroup;    // of a block
+  static constexpr uint32_t a_cols = block / 2, d_cols = groups * kN;
+  static constexpr uint32_t bufs = d_cols <= 64 && a_cols <= 64 ? 4 : 2;
+  static_assert(bufs * a_cols <= kDCol && bufs * d_cols <= kTmemCols - kDCol, "TMEM columns");
 };
 template <int kGroup, int kN>
 constexpr size_t smem_bytes(int E) {
   typedef Shape<kGroup, kN> S;
-  return 1024 + (size_t)S::stages * S::stage + (2 * kMaxStages + 2 * kABufs + 2 * S::d_bufs + 1) * 8 +
-         32 + (size_t)2 * (E + 1) * 4;
+  return 1024 + (size_t)S::stages * S::stage + (2 * kMaxStages + 3 * S::bufs + 1) * 8 + 32 +
+         (size_t)2 * (E + 1) * 4;
 }
 static_assert(smem_bytes<128, 16>(kMaxE) <= 232448 && smem_bytes<128, 32>(kMaxE) <= 232448 &&
                   smem_bytes<128, 64>(kMaxE) <= 232448,
@@ -74,6 +77,8 @@ struct TcMaps {
 struct TcArgs {
   const int32_t *offsets;
   int T, E, N, K;
+  int first;  // row of x that is the first of the rows made
+  const float *factor;
   int mt, units, groups;
   int dtype, out_dtype, act;
   const uint16_t *scale;
@@ -85,59 +90,58 @@ struct TcArgs {
 };
 
 // D[tmem] (+)= A[tmem] B[smem]^T: A's rows in the TMEM lanes, two elements to a column.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "n"(kDescHiK), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+// 32 lanes x kCols consecutive columns; nothing is there before tmem_ld_wait.
+template <int kCols>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t *r) {
+  if constexpr (kCols == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  } else {
+    tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r));
+  }
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
-      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
-      " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[15])
       : "memory");
 }
 
-template <bool kFp16>
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  if (kFp16)
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  else
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+// Registers of a thread, of the 72 that each of the 7 x 128 has: the adding warps hold up to
+// 32 sums and 32 more on their way from TMEM.
+constexpr int kAddRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
+static_assert(2 * kAddRegs + 4 * kUnpackRegs + kOtherRegs <= 7 * 72, "more would be waited for without end");
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-// A word of eight codes as code - 8, pairs in the order of the columns: a pair is a byte,
-// its halves moved to the low bits of two 16-bit numbers, which the exponent of 128
-// (bf16) or 1024 (fp16) makes 128 + code; less 136 that is exact.
-template <bool kFp16>
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t *to) {
-  constexpr uint32_t kOne = kFp16 ? 0x64006400u : 0x43004300u;
-  constexpr uint32_t kZero = kFp16 ? 0x64086408u : 0x43084308u;
-  const uint32_t high = w >> 4;
-#pragma unroll
-  for (uint32_t b = 0; b < 4; ++b)
-    to[b] = sub2<kFp16>((__byte_perm(w, high, 0x4000u + (0x400u | b << 8) + b) & 0x000f000fu) | kOne,
-                        kZero);
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// `and` over the adding warps' 128 threads.
+// `and` over the adding warps' 256 threads.
 __device__ __forceinline__ bool add_all(bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred a, b;\n\t"
       "setp.ne.u32 a, %1, 0;\n\t"
-      "bar.red.and.pred b, 1, 128, a;\n\t"
+      "bar.red.and.pred b, 1, 256, a;\n\t"
       "selp.u32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)p)
@@ -145,56 +149,21 @@ __device__ __forceinline__ bool add_all(bool p) {
   return r != 0;
 }
 
-// A row's scales of one unit, as they lie.
-template <int kGroup>
-struct UnitScales {
-  static constexpr int count = kUnit / kGroup;  // 8, 4 or 2
-  uint32_t w[count / 2];
-  __device__ __forceinline__ void load(const uint16_t *row, int unit, int groups) {
-    const int g = unit * count;
-    const uint16_t *p = row + g;
-    if (groups % count == 0) {  // whole units, as aligned as they are long
-      if constexpr (kGroup == 32) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
-      } else if constexpr (kGroup == 64) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        w[0] = v.x;
-        w[1] = v.y;
-      } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < count; i += 2) {
-        const uint32_t lo = g + i < groups ? __ldg(p + i) : 0u;
-        const uint32_t hi = g + i + 1 < groups ? __ldg(p + i + 1) : 0u;
-        w[i / 2] = lo | hi << 16;
-      }
-    }
-  }
-};
-
-template <bool kFp16, int kGroup, int kN>
+template <int kGroup, int kN>
 __global__ void __launch_bounds__(kThreads, 1)
     int4_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a) {
   typedef Shape<kGroup, kN> S;
   typedef RowSchedule<kN, 16, kBM, kMaxParts, 1> Tiles;
   constexpr int kStages = S::stages;
-  constexpr int kDtype = kFp16 ? MOE_DTYPE_FP16 : MOE_DTYPE_BF16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint64_t *full = reinterpret_cast<uint64_t *>(ring + kStages * S::stage);
   uint64_t *empty = full + kMaxStages;
-  uint64_t *a_full = empty + kMaxStages;
-  uint64_t *a_empty = a_full + kABufs;
-  uint64_t *d_full = a_empty + kABufs;
-  uint64_t *d_empty = d_full + S::d_bufs;
-  uint64_t *fin = d_empty + S::d_bufs;
+  uint64_t *a_full = empty + kMaxStages;  // a block is unpacked
+  uint64_t *done = a_full + S::bufs;      // it is multiplied: its operands are free, its sums there
+  uint64_t *d_empty = done + S::bufs;     // they are read
+  uint64_t *fin = d_empty + S::bufs;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fin + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *last_flag = abort_flag + 1;
@@ -207,12 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kUnpackWarps + 1);
     }
-    for (uint32_t b = 0; b < kABufs; ++b) {
-      mbar_init(&a_full[b], 4);
-      mbar_init(&a_empty[b], 1);
-    }
-    for (uint32_t b = 0; b < S::d_bufs; ++b) {
-      mbar_init(&d_full[b], 1);
+    for (uint32_t b = 0; b < S::bufs; ++b) {
+      mbar_init(&a_full[b], kUnpackWarps);
+      mbar_init(&done[b], 1);
       mbar_init(&d_empty[b], kAddWarps);
     }
     mbar_init(fin, 1);
@@ -227,9 +193,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.x[0]);
   }
-  pdl_wait();
+  // The launch before this one made the rows of x, and waited for all before it: what
+  // else is read here is there.
   pdl_launch_dependents();
-  make_tables(a.offsets, a.E, a.T, seg, first, a.status,
+  make_tables(a.offsets, a.E, a.T, a.first, min(a.T, a.first + kInt4Rows), seg, first, a.status,
               [&](int m) { return Tiles::row_tiles(m) * a.mt; });
   tc_fence_before();
   __syncthreads();
@@ -244,28 +211,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   sch.cid = blockIdx.x;
   sch.ncl = gridDim.x;
   sch.start();
-  auto steps_of = [&](int unit) { return min(kSteps, (a.K - unit * kUnit + kStep - 1) / kStep); };
+  auto blocks_of = [&](int unit) {
+    return min(S::blocks, (a.K - unit * kUnit + S::block - 1) / S::block);
+  };
   Work w;
+  uint32_t st = 0, ph = 0;    // stages of codes and rows
+  uint32_t buf = 0, bph = 0;  // blocks
 
+  if (warp >= kTmaWarp) fewer_registers<kOtherRegs>();
   if (warp == kTmaWarp) {
     // ------------------------------------------------------ TMA producer --
-    uint32_t st = 0, ph = 0, issued = 0;
+    uint32_t issued = 0;
     bool ok = true;
+    auto copy_codes = [&](const Work &v, int u, uint32_t to) {
+      const uint32_t n16 = (uint32_t)(v.n + 15) & ~15u;
+      mbar_arrive_expect_tx(&full[to], kCodeBytes + kUnit / 64 * n16 * 128);
+      tma_load_3d(ring + to * S::stage, &maps.q, &full[to], u * (kUnit / 2), v.a0, v.e);
+    };
+    auto copy_rows = [&](const Work &v, int u, uint32_t to) {
+      const CUtensorMap *mx = &maps.x[((v.n + 15) >> 4) - 1];
+#pragma unroll
+      for (int s = 0; s < kUnit / 64; ++s)
+        tma_load_2d(ring + to * S::stage + kCodeBytes + s * S::x_box, mx, &full[to],
+                    u * kUnit + s * 64, v.b0 - a.first);
+    };
+    // the first round of codes does not wait for the rows
+    uint32_t early = 0;
+    for (int i = 0; early < (uint32_t)kStages && sch.at(i, &w); ++i)
+      for (int u = w.k0; u < w.k1 && early < (uint32_t)kStages; ++u, ++early)
+        if (elect_one()) copy_codes(w, u, early);
+    pdl_wait();
     for (int i = 0; ok && sch.at(i, &w); ++i) {
-      const int n16 = (w.n + 15) & ~15;
-      const CUtensorMap *mx = &maps.x[(n16 >> 4) - 1];
       for (int u = w.k0; u < w.k1; ++u) {
-        if (!mbar_wait_warp(&empty[st], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
+        if (issued >= early &&
+            !mbar_wait_warp(&empty[st], ph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
           ok = false;
           break;
         }
-        const int steps = steps_of(u);
         if (elect_one()) {
-          uint8_t *to = ring + st * S::stage;
-          mbar_arrive_expect_tx(&full[st], kCodeBytes + (uint32_t)(steps * n16 * kStep * 2));
-          tma_load_3d(to, &maps.q, &full[st], u * (kUnit / 2), w.a0, w.e);
-          for (int s = 0; s < steps; ++s)
-            tma_load_2d(to + kCodeBytes + s * S::x_step, mx, &full[st], u * kUnit + s * kStep, w.b0);
+          if (issued >= early) copy_codes(w, u, st);
+          copy_rows(w, u, st);
         }
         ++issued;
         if (++st == (uint32_t)kStages) {
@@ -284,49 +269,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- MMA issuer --
     const uint32_t b_lo = smem_u32(ring + kCodeBytes) >> 4 | kDescLoK;
-    uint32_t st = 0, ph = 0, ab = 0, aph = 0, db = 0, dph = 0;
     bool ok = true;
     for (int i = 0; ok && sch.at(i, &w); ++i) {
-      const uint32_t idesc = idesc_16(kDtype, false, false, kBM, (w.n + 15) & ~15);
+      const uint32_t idesc = idesc_16(MOE_DTYPE_FP16, false, false, kBM, (w.n + 15) & ~15);
       for (int u = w.k0; ok && u < w.k1; ++u) {
         if (!mbar_wait_warp(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
           ok = false;
           break;
         }
-        const int steps = steps_of(u);
-        for (int s = 0; s < steps; ++s) {
-          if ((s & 1) == 0 &&
-              !mbar_wait_warp(&d_empty[db], dph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait_warp(&a_full[ab], aph, abort_flag, a.status, kStatusTimeoutDense)) {
+        const int blocks = blocks_of(u);
+        for (int b = 0; b < blocks; ++b) {
+          if (!mbar_wait_warp(&d_empty[buf], bph ^ 1u, abort_flag, a.status, kStatusTimeoutDense) ||
+              !mbar_wait_warp(&a_full[buf], bph, abort_flag, a.status, kStatusTimeoutDense)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t d0 = tmem_base + kDCol + db * S::d_cols, a0 = tmem_base + ab * kAColsStep;
-            const uint32_t bd = b_lo + ((st * S::stage + (uint32_t)s * S::x_step) >> 4);
+            const uint32_t d0 = tmem_base + kDCol + buf * S::d_cols, a0 = tmem_base + buf * S::a_cols;
+            const uint32_t bd = b_lo + ((st * S::stage + (uint32_t)b * (S::block / 64) * S::x_box) >> 4);
 #pragma unroll
-            for (uint32_t q = 0; q < 4; ++q) {
-              const uint32_t k = (uint32_t)(s & 1) * kStep + q * 16;  // in the block
-              umma_ts(d0 + k / kGroup * kGroup, a0 + q * 8, (uint64_t)kDescHiK << 32 | (bd + 2 * q),
+            for (uint32_t q = 0; q < S::block / 16; ++q) {
+              const uint32_t k = q * 16;  // in the block
+              umma_ts(d0 + k / kGroup * kN, a0 + q * 8, bd + (k / 64 * S::x_box >> 4) + 2 * (q & 3),
                       idesc, k % kGroup != 0 ? 1u : 0u);
             }
-            umma_commit(&a_empty[ab]);
-            if ((s & 1) == 1 || s + 1 == steps) umma_commit(&d_full[db]);
-            if (s + 1 == steps) umma_commit(&empty[st]);
+            umma_commit(&done[buf]);
+            if (b + 1 == blocks) umma_commit(&empty[st]);
           }
-          if (++ab == kABufs) {
-            ab = 0;
-            aph ^= 1u;
-          }
-          if ((s & 1) == 1 || s + 1 == steps) {
-            if (++db == S::d_bufs) {
-              db = 0;
-              dph ^= 1u;
-            }
+          if (++buf == S::bufs) {
+            buf = 0;
+            bph ^= 1u;
           }
         }
         if (++st == (uint32_t)kStages) {
@@ -339,62 +312,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_wait_drain(fin, 0);
     __syncwarp();
+  } else if (warp > kMmaWarp) {
   } else if (warp >= kAddWarps) {
+    fewer_registers<kUnpackRegs>();
     // ---------------------------------------------------------- unpackers --
+    // Four sets of four warps, 32 rows to a warp; each set takes a quarter of a block's columns.
+    const Unpack unpack;
     const int quad = warp & 3, set = (warp - kAddWarps) >> 2;
     const int r = quad * 32 + lane;
-    const uint32_t to = tmem_base + ((uint32_t)(quad * 32) << 16);
-    uint32_t st = 0, ph = 0, ab = 0, aph = 0;
+    constexpr int kChunks = S::block / 128;  // of 32 columns, for a set: 2 or 1
+    const uint32_t to = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)set * (S::a_cols / 4);
     bool ok = true;
     for (int i = 0; ok && sch.at(i, &w); ++i) {
-      for (int u = w.k0; u < w.k1; ++u) {
+      for (int u = w.k0; ok && u < w.k1; ++u) {
         if (!mbar_wait_warp(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
           ok = false;
           break;
         }
-        // this set's two steps of the unit: 32 bytes of the row each
         const uint8_t *row = ring + st * S::stage + r * 128;
-        uint4 v[2][2];
+        uint4 v[S::blocks][kChunks];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int b = 0; b < S::blocks; ++b)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            v[h][c] = *reinterpret_cast<const uint4 *>(
-                row + (((4 * h + 2 * set + c) ^ (r & 7)) << 4));
+          for (int c = 0; c < kChunks; ++c)
+            v[b][c] = *reinterpret_cast<const uint4 *>(
+                row + ((((b * 4 + set) * kChunks + c) ^ (r & 7)) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
-        const int steps = steps_of(u);
+        const int blocks = blocks_of(u);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int s = 2 * h + set;
-          if (s < steps) {
-            const uint32_t at = ab + (uint32_t)s, b = at & (kABufs - 1);
-            const uint32_t p = aph ^ (at >= kABufs ? 1u : 0u);
-            uint32_t o[32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              unpack8<kFp16>(v[h][c].x, o + 16 * c);
-              unpack8<kFp16>(v[h][c].y, o + 16 * c + 4);
-              unpack8<kFp16>(v[h][c].z, o + 16 * c + 8);
-              unpack8<kFp16>(v[h][c].w, o + 16 * c + 12);
-            }
-            if (!mbar_wait_warp(&a_empty[b], p ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
+        for (int b = 0; b < S::blocks; ++b) {
+          if (b < blocks) {
+            // (the operands before these are multiplied)
+            if (!mbar_wait_warp(&done[buf], bph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            tmem_st32(to + b * kAColsStep, o);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              uint32_t o[16];
+              unpack(v[b][c].x, o);
+              unpack(v[b][c].y, o + 4);
+              unpack(v[b][c].z, o + 8);
+              unpack(v[b][c].w, o + 12);
+              tmem_st16(to + buf * S::a_cols + (uint32_t)c * 16, o);
+            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[b]);
+            if (lane == 0) mbar_arrive(&a_full[buf]);
+            if (++buf == S::bufs) {
+              buf = 0;
+              bph ^= 1u;
+            }
           }
-        }
-        if (!ok) break;
-        ab += (uint32_t)steps;
-        if (ab >= kABufs) {
-          ab -= kABufs;
-          aph ^= 1u;
         }
         if (++st == (uint32_t)kStages) {
           st = 0;
@@ -404,74 +376,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------- scaling, adding, epilogue --
-    const int quad = warp;
-    const uint32_t from = tmem_base + ((uint32_t)(quad * 32) << 16) + kDCol;
-    uint32_t db = 0, dph = 0;
+    more_registers<kAddRegs>();
+    pdl_wait();
+    // warps w and w + 4 share 32 TMEM lanes, each half of the rows of x
+    constexpr int kHalf = kN / 2;
+    const int quad = warp & 3, half = (warp >> 2) * kHalf;
+    const uint32_t from = tmem_base + ((uint32_t)(quad * 32) << 16) + kDCol + half;
     bool ok = true;
-    auto scales_of = [&](const Work &t) {
-      const int n = min(t.a0 + quad * 32 + lane, a.N - 1);
-      return a.scale + ((int64_t)t.e * a.N + n) * a.groups;
+    // A row's scales, two units ahead, of even and of odd units: what is done with a register
+    // that a load is still to fill waits for it, a move included.
+    UnitScales<kGroup, kUnit> even, odd;
+    Work w_ask = {};
+    int i_ask = 0, u_ask = 0;
+    bool is_odd = false;
+    const uint16_t *scale_row = nullptr;
+    auto aim = [&]() {
+      u_ask = sch.at(i_ask, &w_ask) ? w_ask.k0 : -1;
+      scale_row = a.scale + ((int64_t)w_ask.e * a.N + min(w_ask.a0 + quad * 32 + lane, a.N - 1)) * a.groups;
     };
-    UnitScales<kGroup> next;
-    Work w_next;
-    bool more = sch.at(0, &w_next);
-    if (more) next.load(scales_of(w_next), w_next.k0, a.groups);
-    for (int i = 0; more;) {
-      w = w_next;
-      more = sch.at(++i, &w_next);
-      float acc[kN];
+    auto ask = [&](UnitScales<kGroup, kUnit> &s) {
+      if (u_ask < 0) return;
+      s.load(scale_row, u_ask, a.groups);
+      if (++u_ask == w_ask.k1) {
+        ++i_ask;
+        aim();
+      }
+    };
+    aim();
+    ask(even);
+    ask(odd);
+    for (int i = 0; sch.at(i, &w); ++i) {
+      float acc[kHalf];
 #pragma unroll
-      for (int j = 0; j < kN; ++j) acc[j] = 0.f;
-      const uint16_t *row = scales_of(w);
-      for (int u = w.k0; u < w.k1; ++u) {
-        const UnitScales<kGroup> sc = next;
-        if (u + 1 < w.k1)
-          next.load(row, u + 1, a.groups);
-        else if (more)
-          next.load(scales_of(w_next), w_next.k0, a.groups);
-        const int blocks = (steps_of(u) + 1) >> 1;
+      for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
+      for (int u = w.k0; ok && u < w.k1; ++u) {
+        float scales[kUnit / kGroup];
+        auto take = [&](UnitScales<kGroup, kUnit> &s) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+          for (int g = 0; g < kUnit / kGroup; ++g) scales[g] = scale_half(a.dtype, s.w[g / 2], g & 1);
+          ask(s);
+        };
+        if (is_odd)
+          take(odd);
+        else
+          take(even);
+        is_odd = !is_odd;
+        const int blocks = blocks_of(u);
+#pragma unroll
+        for (int b = 0; b < S::blocks; ++b) {
           if (b < blocks) {
-            ok = mbar_wait_warp(&d_full[db], dph, abort_flag, a.status, kStatusTimeoutDense);
+            ok = mbar_wait_warp(&done[buf], bph, abort_flag, a.status, kStatusTimeoutDense);
             if (!ok) break;
             tc_fence_after();
+            // up to 32 columns on their way at a time: of several groups, or of one
+            constexpr int kLoad = kHalf < 16 ? 8 : 16;
+            constexpr int kLoads = S::groups * (kHalf / kLoad);  // of a block
+            constexpr int kOnce = kLoads < 32 / kLoad ? kLoads : 32 / kLoad;
 #pragma unroll
-            for (int g = 0; g < S::groups; ++g) {
-              const int at = b * S::groups + g;
-              if (u * UnitScales<kGroup>::count + at >= a.groups) break;  // never accumulated
-              const float f = unpack16(kDtype, at & 1 ? sc.w[at / 2] >> 16 : sc.w[at / 2]).x;
+            for (int l0 = 0; l0 < kLoads; l0 += kOnce) {
+              uint32_t v[kOnce * kLoad];
 #pragma unroll
-              for (int c = 0; c < kN; c += 16) {
-                float v[16];
-                tmem_ld16f(from + db * S::d_cols + (uint32_t)(g * kGroup + c), v);
+              for (int l = 0; l < kOnce; ++l)
+                tmem_ld_cols<kLoad>(from + buf * S::d_cols + (uint32_t)((l0 + l) / (kHalf / kLoad) * kN +
+                                                                        (l0 + l) % (kHalf / kLoad) * kLoad),
+                                    v + l * kLoad);
+              tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(f, v[j], acc[c + j]);
+              for (int k = 0; k < kOnce * kLoad; ++k) asm volatile("" : "+r"(v[k]));  // not before
+#pragma unroll
+              for (int l = 0; l < kOnce; ++l) {
+                const int g = b * S::groups + (l0 + l) / (kHalf / kLoad);
+                const int c = (l0 + l) % (kHalf / kLoad) * kLoad;
+#pragma unroll
+                for (int j = 0; j < kLoad; ++j)
+                  acc[c + j] = fmaf(scales[g], __uint_as_float(v[l * kLoad + j]), acc[c + j]);
               }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[db]);
-            if (++db == S::d_bufs) {
-              db = 0;
-              dph ^= 1u;
+            if (lane == 0) mbar_arrive(&d_empty[buf]);
+            if (++buf == S::bufs) {
+              buf = 0;
+              bph ^= 1u;
             }
           }
         }
-        if (!ok) break;
       }
       // warps meet at a split tile: all of them leave there, or none
-      if (i <= sch.pieces) ok = add_all(ok && !*abort_flag);
+      if (i < sch.pieces) ok = add_all(ok && !*abort_flag);
       if (!ok) break;
       bool last = true;
       if (w.parts > 1) {
         auto place = [&](int part) {
           const int s = sch.slot(sch.first_worker(w.tile) + part, w.tile);
-          return a.part + (size_t)s * (kBM * kN) + (quad * 32 + lane) * 4;
+          return a.part + (size_t)s * (kBM * kN) + (size_t)half * kBM + (quad * 32 + lane) * 4;
         };
         float *mine = place(w.part);
 #pragma unroll
-        for (int q = 0; q < kN / 4; ++q)
+        for (int q = 0; q < kHalf / 4; ++q)
           __stcg(reinterpret_cast<float4 *>(mine + q * (kBM * 4)),
                  make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
         __threadfence();
@@ -487,11 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence();
         if (last) {
 #pragma unroll
-          for (int j = 0; j < kN; ++j) acc[j] = 0.f;
+          for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
+          // several loads in flight, added in order
+#pragma unroll 4
           for (int part = 0; part < w.parts; ++part) {
             const float *p = place(part);
 #pragma unroll
-            for (int q = 0; q < kN / 4; ++q) {
+            for (int q = 0; q < kHalf / 4; ++q) {
               const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + q * (kBM * 4)));
               acc[4 * q] += v.x;
               acc[4 * q + 1] += v.y;
@@ -503,6 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int n = w.a0 + quad * 32 + lane;
       if (last && n < a.N) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j)
+          if (half + j < w.n) acc[j] *= a.factor[w.b0 - a.first + half + j];
         const bool wide = a.out_dtype == MOE_DTYPE_FP32;
         auto load = [&](const void *p, int64_t at) {
           return wide ? static_cast<const float *>(p)[at]
@@ -511,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.bias != nullptr) {
           const float b = load(a.bias, n);
 #pragma unroll
-          for (int j = 0; j < kN; ++j) acc[j] += b;
+          for (int j = 0; j < kHalf; ++j) acc[j] += b;
         }
         if (wide)
           activate_all<true>(a.act, acc);
@@ -519,20 +526,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           activate_all<false>(a.act, acc);
         if (a.residual != nullptr) {
 #pragma unroll
-          for (int j = 0; j < kN; ++j)
-            if (j < w.n) acc[j] += load(a.residual, (int64_t)(w.b0 + j) * a.ldr + n);
+          for (int j = 0; j < kHalf; ++j)
+            if (half + j < w.n) acc[j] += load(a.residual, (int64_t)(w.b0 + half + j) * a.ldr + n);
         }
-        const int64_t y0 = (int64_t)w.b0 * a.ldy + n;
+        const int64_t y0 = (int64_t)(w.b0 + half) * a.ldy + n;
         if (wide) {
           float *p = static_cast<float *>(a.y) + y0;
 #pragma unroll
-          for (int j = 0; j < kN; ++j)
-            if (j < w.n) p[j * a.ldy] = acc[j];
+          for (int j = 0; j < kHalf; ++j)
+            if (half + j < w.n) p[j * a.ldy] = acc[j];
         } else {
           uint16_t *p = static_cast<uint16_t *>(a.y) + y0;
 #pragma unroll
-          for (int j = 0; j < kN; ++j)
-            if (j < w.n) p[j * a.ldy] = (uint16_t)pack16(a.out_dtype, acc[j], 0.f);
+          for (int j = 0; j < kHalf; ++j)
+            if (half + j < w.n) p[j * a.ldy] = (uint16_t)pack16(a.out_dtype, acc[j], 0.f);
         }
       }
     }
@@ -546,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kFp16, int kGroup, int kN>
+template <int kGroup, int kN>
 cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
-  auto kern = int4_tc_kernel<kFp16, kGroup, kN>;
+  auto kern = int4_tc_kernel<kGroup, kN>;
   static std::atomic<bool> allowed[64];
   cudaError_t e = allow_smem(kern, smem_bytes<kGroup, kN>(kMaxE), allowed);
   if (e != cudaSuccess) return e;
@@ -558,6 +565,8 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
   a.E = g.E;
   a.N = g.N;
   a.K = g.K;
+  a.first = g.first;
+  a.factor = g.factor;
   a.mt = (g.N + kBM - 1) / kBM;
   a.units = (g.K + kUnit - 1) / kUnit;
   a.groups = (g.K + kGroup - 1) / kGroup;
@@ -573,6 +582,7 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
   a.part = g.part;
   a.counters = g.status + kSplitCounterWord;
   a.status = g.status;
+  const int rows = std::min(g.T - g.first, kInt4Rows);
   TcMaps maps = {};
   const cuuint64_t dims[3] = {(cuuint64_t)g.K / 2, (cuuint64_t)g.N, (cuuint64_t)g.E};
   const cuuint64_t strides[2] = {(cuuint64_t)g.K / 2, (cuuint64_t)g.N * (g.K / 2)};
@@ -580,39 +590,42 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
   bool ok = encode_map(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, g.q, 3,
                        dims, strides, box);
   for (int i = 0; i < kN / 16; ++i)
-    ok = ok && map_2d(&maps.x[i], g.dtype, CU_TENSOR_MAP_SWIZZLE_128B, g.x, g.T, g.K, g.ldx,
-                      16 * (i + 1), kStep);
+    ok = ok && map_2d(&maps.x[i], MOE_DTYPE_FP16, CU_TENSOR_MAP_SWIZZLE_128B, g.xr, rows, int4_pitch(g.K),
+                      int4_pitch(g.K), 16 * (i + 1), 64);
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = ((int64_t)std::min(g.E, g.T) + g.T / kN) * a.mt;
+  // (rows of a tile are chosen by what int4_part_bytes counts on)
+  if (g.part_bytes < (size_t)2 * kMaxCtas * kBM * kN * 4) return cudaErrorInvalidValue;
+  const int64_t tiles = ((int64_t)std::min(g.E, rows) + rows / kN) * a.mt;
   const int64_t most = std::min<int64_t>(tiles * std::min(kMaxParts, a.units),
                                          std::min(num_sms(), kMaxCtas));
   return launch_pdl(kern, dim3((unsigned)most), dim3(kThreads), smem_bytes<kGroup, kN>(g.E), s, maps,
                     a);
 }
 
-// Rows of a tile: as many as most experts have, if they are spread evenly.
-template <bool kFp16, int kGroup>
+// Rows of a tile: what one pass takes.  Experts' rows vary, so that half of the most that an
+// even spread gives 16 of would take two passes: 32 experts of 4096 x 7168 with 16 rows
+// on average take 179 us in tiles of up to 32, 215 in tiles of 16 and 252 in tiles of 64; a
+// matrix of 14336 x 4096 with 16 rows 20.9, 18.7 and 23.9.
+template <int kGroup>
 cudaError_t by_rows(const Int4Gemm &g, cudaStream_t s) {
   const int rows = (g.T + g.E - 1) / g.E;
-  if (rows <= 16) return start<kFp16, kGroup, 16>(g, s);
-  if (rows <= 32 || kGroup == 32) return start<kFp16, kGroup, 32>(g, s);
-  return start<kFp16, kGroup, kGroup == 32 ? 32 : 64>(g, s);
-}
-template <bool kFp16>
-cudaError_t by_group(const Int4Gemm &g, cudaStream_t s) {
-  if (g.group == 32) return by_rows<kFp16, 32>(g, s);
-  return g.group == 64 ? by_rows<kFp16, 64>(g, s) : by_rows<kFp16, 128>(g, s);
+  if (rows <= (g.E == 1 ? 16 : 8)) return start<kGroup, 16>(g, s);
+  if (rows <= 32 || kGroup == 32) return start<kGroup, 32>(g, s);
+  return start<kGroup, kGroup == 32 ? 32 : 64>(g, s);
 }
 
 }  // namespace
 
+// Two pieces to a CTA, 128 x (rows of a tile) fp32 each; of up to 8 rows over any experts a
+// tile has 16 rows, of up to 16 or of more than one expert's 32 at most.
 size_t int4_part_bytes(int T) {
-  const int rows = T <= 16 ? 16 : (T <= 32 ? 32 : 64);
+  const int rows = T <= 8 ? 16 : (T <= 32 ? 32 : 64);
   return (size_t)2 * kMaxCtas * kBM * rows * 4;
 }
 
 cudaError_t launch_int4_tc(const Int4Gemm &g, cudaStream_t s) {
-  return g.dtype == MOE_DTYPE_FP16 ? by_group<true>(g, s) : by_group<false>(g, s);
+  if (g.group == 32) return by_rows<32>(g, s);
+  return g.group == 64 ? by_rows<64>(g, s) : by_rows<128>(g, s);
 }
 
 }  // namespace moe

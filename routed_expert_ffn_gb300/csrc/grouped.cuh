@@ -150,6 +150,17 @@ struct RowSchedule {
   }
 };
 
+// One thread's arrival at a split tile's counter, after a barrier behind the writes of all whose
+// part it is: true for the last of `parts`, which then sees the others' (after another
+// barrier everybody behind it).
+__device__ __forceinline__ bool arrive_last(uint32_t *counter, int parts) {
+  uint32_t before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  if (before + 1 != (uint32_t)parts) return false;
+  *counter = 0;  // nobody else comes
+  return true;
+}
+
 cudaError_t launch_grouped_rows(const GroupedGemm &g, bool grad, cudaStream_t s);
 cudaError_t launch_grouped_weight_grad(const GroupedGemm &g, cudaStream_t s);
 

@@ -40,7 +40,13 @@ enum { kForward = 0, kRowGrad = 1, kWeightGrad = 2 };
 
 constexpr int kEpiWarps = 8;
 constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
+// kFine: its epilogue's threads hold 128 sums and 32 on their way, with registers that the
+// other four warps (two of them idle) leave them: 2 x 208 + 88 = 3 x 168, what each of
+// the three groups of 128 threads starts with.
+template <bool kFine>
+constexpr int kThreads = (kEpiWarps + (kFine ? 4 : 2)) * 32;
+constexpr int kFineEpiRegs = 208, kFineOtherRegs = 88;
+static_assert(2 * kFineEpiRegs + kFineOtherRegs <= 3 * 168, "more would be waited for without end");
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;  // the most accumulator columns
 constexpr uint32_t kABytes = kBM * kBK * 2;
@@ -54,6 +60,12 @@ struct Shape {
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxClusters = 80;  // (a GB300 has 76 pairs of SMs)
+constexpr int kChunks = kTileN / 64;  // of 32 accumulator columns, to an epilogue warp
+// The tensor cores' additions truncate, each by up to a step of the running sum, which adds
+// up: 2.4e-6 of the result over 2048 products, 8 times what fp32 rounding leaves.  For fp32
+// results (kFine) an accumulator takes 512 of depth and the epilogue's warps add them,
+// rounding to nearest.
+constexpr int kFineStages = 8;
 // Pieces of a split tile: at most this many, of at least this many stages.
 constexpr int kMaxParts = 8, kMinPart = 4;
 
@@ -155,8 +167,8 @@ __device__ __forceinline__ void store_rows(void *d, int64_t ld, int dtype, int64
   }
 }
 
-template <int kMode>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kMode, bool kFine>
+__global__ void __launch_bounds__(kThreads<kFine>, 1)
     grouped_pair_kernel(const __grid_constant__ GroupedMaps maps,
                         const __grid_constant__ GroupedArgs a) {
   constexpr bool kWeights = kMode == kWeightGrad;
@@ -232,7 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // accumulator columns of a tile, and those whose B a CTA holds
   auto columns = [&](const Work &w) { return kWeights ? a.bn : (w.n + 31) & ~31; };
 
-  if (warp == kTmaWarp) {
+  if (kFine && warp >= kEpiWarps) fewer_registers<kFineOtherRegs>();
+  if (kFine && warp > kMmaWarp) {
+    // (no work of its own)
+  } else if (warp == kTmaWarp) {
     // ------------------------------------------------------ TMA producer --
     const uint32_t full0 = cluster_addr(full, 0);
     uint32_t st = 0, ph = 0, issued = 0;
@@ -312,34 +327,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       Work w;
       for (int i = 0; ok && sch.at(i, &w); ++i) {
         if (w.k1 <= w.k0) continue;
-        const uint32_t buf = tl & 1u, use = tl >> 1;
-        ++tl;
-        if (!mbar_wait_warp(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense))
-          break;
-        tc_fence_after();
-        const uint32_t d0 = tmem_base + buf * kTileN;
         const uint32_t idesc = idesc_16(a.dtype, kAMn, kBMn, 2 * kBM, columns(w));
-        for (int kb = w.k0; kb < w.k1; ++kb) {
-          if (!mbar_wait_warp(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
+        for (int from = w.k0; ok && from < w.k1; from += kFine ? kFineStages : w.k1 - w.k0) {
+          const int to = kFine ? min(from + kFineStages, w.k1) : w.k1;
+          const uint32_t buf = tl & 1u, use = tl >> 1;
+          ++tl;
+          if (!mbar_wait_warp(&tempty[buf], (use & 1u) ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ad = a_lo + st * (kStageBytes >> 4), bd = b_lo + st * (kStageBytes >> 4);
-          if (elect_one()) {
+          const uint32_t d0 = tmem_base + buf * kTileN;
+          for (int kb = from; kb < to; ++kb) {
+            if (!mbar_wait_warp(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t ad = a_lo + st * (kStageBytes >> 4), bd = b_lo + st * (kStageBytes >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (uint32_t q = 0; q < 4; ++q)
-              umma_16_pair(d0, ad + q * kAStep, kAHi, bd + q * kBStep, kBHi, idesc,
-                           kb > w.k0 || q > 0 ? 1u : 0u);
-            umma_commit_pair(&empty[st], 3);
+              for (uint32_t q = 0; q < 4; ++q)
+                umma_16_pair(d0, ad + q * kAStep, kAHi, bd + q * kBStep, kBHi, idesc,
+                             kb > from || q > 0 ? 1u : 0u);
+              umma_commit_pair(&empty[st], 3);
+            }
+            if (++st == (uint32_t)kStages) {
+              st = 0;
+              ph ^= 1u;
+            }
           }
-          if (++st == (uint32_t)kStages) {
-            st = 0;
-            ph ^= 1u;
-          }
+          if (ok && elect_one()) umma_commit_pair(&tfull[buf], 3);
         }
-        if (!ok) break;
-        if (elect_one()) umma_commit_pair(&tfull[buf], 3);
       }
       if (elect_one()) umma_commit_pair(fin, 1);
       __syncwarp();
@@ -348,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue --
+    if (kFine) more_registers<kFineEpiRegs>();
     // warps w and w + 4 share 32 TMEM lanes and take every other 32 columns
     Slots<2> slot = {slots + warp * kOutBytes, 0, false};
     const int quad = warp & 3, turn = (warp >> 2) * 32;
@@ -355,28 +375,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     Work w;
     for (int i = 0; sch.at(i, &w); ++i) {
       const bool none = w.k1 <= w.k0;  // an expert without rows: zeros
-      const uint32_t buf = tl & 1u, use = tl >> 1;
+      const int m0 = w.a0 + (int)rank * kBM + quad * 32;
+      const int cend = m0 < a.M ? w.n : 0;
       bool ok = true;
-      if (!none) {
+      uint32_t tb = 0;
+      // the next accumulator
+      auto take = [&]() {
+        const uint32_t buf = tl & 1u, use = tl >> 1;
         ++tl;
+        tb = tmem_base + ((uint32_t)(quad * 32) << 16) + buf * kTileN;
         ok = mbar_wait_warp(&tfull[buf], use & 1u, abort_flag, a.status, kStatusTimeoutDense);
         tc_fence_after();
+      };
+      auto hand_back = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_relaxed(cluster_addr(&tempty[(tl - 1) & 1u], 0));
+      };
+      // kFine: the sums of all accumulators; else the one accumulator is read where it is used
+      float sums[kFine ? kChunks : 1][32];
+      if constexpr (kFine) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sums[i][j] = 0.f;
+        for (int from = w.k0; ok && from < w.k1; from += kFineStages) {
+          take();
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            if (turn + 64 * i < w.n) {
+              float v[32];
+              tmem_ld32(tb + turn + 64 * i, v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sums[i][j] += v[j];
+            }
+          }
+          hand_back();
+        }
+      } else if (!none) {
+        take();
       }
       // warps meet at a split tile: all of them leave there, or none
       if (!kWeights && i < sch.pieces) ok = epi_all(ok && !*abort_flag);
       if (!ok) break;
-      const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + buf * kTileN;
-      const int m0 = w.a0 + (int)rank * kBM + quad * 32;
+      // 32 columns of the accumulator, the warp's i-th
+      auto columns_of = [&](int i, float (&v)[32]) {
+        if constexpr (kFine) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = sums[i][j];
+        } else {
+          tmem_ld32(tb + turn + 64 * i, v);
+        }
+      };
       if constexpr (kWeights) {
         const bool wide = a.out_dtype == MOE_DTYPE_FP32;
-        const int cend = m0 < a.M ? w.n : 0;
-        for (int c = turn; c < cend; c += 64) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = turn + 64 * i;
+          if (c >= cend) break;
           float v[32];
           if (none) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
           } else {
-            tmem_ld32(tb + c, v);
+            columns_of(i, v);
           }
           Rows32 held;
           if (a.accumulate)
@@ -393,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const int col = m0 + lane;
-        float *mine = nullptr;
         bool last = true;
         auto place = [&](int part, int c) {
           const int s = sch.slot(sch.first_worker(w.tile) + part, w.tile);
@@ -401,36 +463,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                  quad * 1024 + lane * 4;
         };
         if (w.parts > 1) {
-          for (int c = turn; c < w.n; c += 64) {
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int c = turn + 64 * i;
+            if (c >= w.n) break;
             float v[32];
-            tmem_ld32(tb + c, v);
-            mine = place(w.part, c);
+            columns_of(i, v);
+            float *mine = place(w.part, c);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               __stcg(reinterpret_cast<float4 *>(mine + q * 128),
                      make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
           }
-          __threadfence();
           epi_all(true);
-          if (threadIdx.x == 0) {
-            uint32_t *counter = a.counters + 2 * w.tile + rank;
-            const uint32_t n = atomicAdd(counter, 1u) + 1;
-            if (n == (uint32_t)w.parts) *counter = 0;  // nobody else comes
-            __threadfence();
-            *last_flag = n == (uint32_t)w.parts;
-          }
+          if (threadIdx.x == 0) *last_flag = arrive_last(a.counters + 2 * w.tile + rank, w.parts);
           epi_all(true);
           last = *last_flag != 0;
-          __threadfence();
         }
         if (last) {
-          for (int c = turn; c < w.n; c += 64) {
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int c = turn + 64 * i;
+            if (c >= w.n) break;
             float v[32];
             if (w.parts == 1) {
-              tmem_ld32(tb + c, v);
+              columns_of(i, v);
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = 0.f;
+              // (two parts' loads at a time took longer: 24.7 us instead of 21.5 for eight
+              // experts of 4096 x 1536 with a row each)
               for (int part = 0; part < w.parts; ++part) {
                 const float *p = place(part, c);
 #pragma unroll
@@ -447,11 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!none) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_relaxed(cluster_addr(&tempty[buf], 0));
-      }
+      if (!kFine && !none) hand_back();
     }
     // the slots outlive the copies that read them
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -501,9 +559,9 @@ __global__ void grouped_maps_kernel(const __grid_constant__ MapTemplates t, cons
 }
 
 // Clusters that can run at once (per device, queried once).
-template <int kMode>
+template <int kMode, bool kFine>
 cudaError_t resident_clusters(int *out) {
-  auto kern = grouped_pair_kernel<kMode>;
+  auto kern = grouped_pair_kernel<kMode, kFine>;
   static std::atomic<int> resident[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -518,7 +576,7 @@ cudaError_t resident_clusters(int *out) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads<kFine>);
     cfg.dynamicSmemBytes = smem_bytes<kMode>(kMaxE);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -532,7 +590,7 @@ cudaError_t resident_clusters(int *out) {
   return cudaSuccess;
 }
 
-template <int kMode>
+template <int kMode, bool kFine>
 cudaError_t start(const GroupedMaps &maps, const GroupedArgs &a, int clusters, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -543,12 +601,12 @@ cudaError_t start(const GroupedMaps &maps, const GroupedArgs &a, int clusters, c
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(2 * clusters));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<kFine>);
   cfg.dynamicSmemBytes = smem_bytes<kMode>(a.E);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_pair_kernel<kMode>, maps, a);
+  return cudaLaunchKernelEx(&cfg, grouped_pair_kernel<kMode, kFine>, maps, a);
 }
 
 // [E][rows][cols], dense.
@@ -564,10 +622,10 @@ bool map_3d(CUtensorMap *m, int dtype, CUtensorMapSwizzle sw, const void *p, int
 // Accumulator columns of the largest tile of R rows.
 int part_cols(int R) { return std::min(kTileN, (R + 31) / 32 * 32); }
 
-template <int kMode>
+template <int kMode, bool kFine>
 cudaError_t rows_product(const GroupedGemm &g, cudaStream_t s) {
   int resident = 0;
-  cudaError_t e = resident_clusters<kMode>(&resident);
+  cudaError_t e = resident_clusters<kMode, kFine>(&resident);
   if (e != cudaSuccess) return e;
   const bool grad = kMode == kRowGrad;
   const int M = grad ? g.K : g.N, depth = grad ? g.N : g.K;
@@ -597,7 +655,7 @@ cudaError_t rows_product(const GroupedGemm &g, cudaStream_t s) {
   // at most this many tiles, each of which may be split
   const int64_t tiles = ((int64_t)std::min(g.E, g.R) + g.R / kTileN) * a.mt;
   const int64_t most = tiles * std::max(1, std::min(kMaxParts, a.nkb / kMinPart));
-  return start<kMode>(maps, a, (int)std::min<int64_t>(resident, most), s);
+  return start<kMode, kFine>(maps, a, (int)std::min<int64_t>(resident, most), s);
 }
 
 }  // namespace
@@ -608,12 +666,17 @@ size_t grouped_part_bytes(int R) {
 }
 
 cudaError_t launch_grouped_rows(const GroupedGemm &g, bool grad, cudaStream_t s) {
-  return grad ? rows_product<kRowGrad>(g, s) : rows_product<kForward>(g, s);
+  if (grad) return rows_product<kRowGrad, false>(g, s);
+  return g.out_dtype == MOE_DTYPE_FP32 ? rows_product<kForward, true>(g, s)
+                                       : rows_product<kForward, false>(g, s);
 }
 
-cudaError_t launch_grouped_weight_grad(const GroupedGemm &g, cudaStream_t s) {
+namespace {
+
+template <bool kFine>
+cudaError_t weight_grad(const GroupedGemm &g, cudaStream_t s) {
   int resident = 0;
-  cudaError_t e = resident_clusters<kWeightGrad>(&resident);
+  cudaError_t e = resident_clusters<kWeightGrad, kFine>(&resident);
   if (e != cudaSuccess) return e;
   const CUtensorMapSwizzle in = CU_TENSOR_MAP_SWIZZLE_128B;
   MapTemplates t;
@@ -645,7 +708,13 @@ cudaError_t launch_grouped_weight_grad(const GroupedGemm &g, cudaStream_t s) {
                  g.ldy * 2, static_cast<const uint8_t *>(g.x), g.ldx * 2, g.maps);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)g.E * a.mt * a.nt;
-  return start<kWeightGrad>(maps, a, (int)std::min<int64_t>(resident, tiles), s);
+  return start<kWeightGrad, kFine>(maps, a, (int)std::min<int64_t>(resident, tiles), s);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_weight_grad(const GroupedGemm &g, cudaStream_t s) {
+  return g.out_dtype == MOE_DTYPE_FP32 ? weight_grad<true>(g, s) : weight_grad<false>(g, s);
 }
 
 }  // namespace moe

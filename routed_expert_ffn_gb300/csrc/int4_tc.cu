@@ -126,15 +126,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 // 32 sums and 32 more on their way from TMEM.
 constexpr int kAddRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
 static_assert(2 * kAddRegs + 4 * kUnpackRegs + kOtherRegs <= 7 * 72, "more would be waited for without end");
-template <int kRegs>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 // `and` over the adding warps' 256 threads.
 __device__ __forceinline__ bool add_all(bool p) {
   uint32_t r;
@@ -476,17 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < kHalf / 4; ++q)
           __stcg(reinterpret_cast<float4 *>(mine + q * (kBM * 4)),
                  make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
-        __threadfence();
         add_all(true);
-        if (threadIdx.x == 0) {
-          const uint32_t n = atomicAdd(a.counters + w.tile, 1u) + 1;
-          if (n == (uint32_t)w.parts) a.counters[w.tile] = 0;  // nobody else comes
-          __threadfence();
-          *last_flag = n == (uint32_t)w.parts;
-        }
+        if (threadIdx.x == 0) *last_flag = arrive_last(a.counters + w.tile, w.parts);
         add_all(true);
         last = *last_flag != 0;
-        __threadfence();
         if (last) {
 #pragma unroll
           for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;

@@ -114,4 +114,15 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t *bar, uint16_t mask) {
       : "memory");
 }
 
+// Registers of a thread from here on, for the four warps of a warpgroup; those that are given
+// up by one go to another, never more than the block was launched with in all.
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 }  // namespace moe

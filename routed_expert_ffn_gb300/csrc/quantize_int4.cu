@@ -14,7 +14,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;
+constexpr int kAhead = 2;
 constexpr int kBlock = kThreads * kAhead;  // chunks of a block's stretch
 
 // round(f / s) + 8 as the low bits of a float's, for a quotient in [-7.5, 7.5].  With f
@@ -110,7 +110,7 @@ cudaError_t start(const void *w, int dtype, int64_t rows, int K, uint8_t *q, voi
   const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + per_row - 1) / per_row);
   const int64_t blocks = (total + kBlock - 1) / kBlock;
   auto kern = values != nullptr ? quantize_int4_kernel<kGroup, true> : quantize_int4_kernel<kGroup, false>;
-  return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)num_sms() * 16)),
+  return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(blocks, (int64_t)num_sms() * 64)),
                     dim3(kThreads), 0, s, static_cast<const uint4 *>(w), dtype, total, per_row, magic,
                     K / 8, reinterpret_cast<uint32_t *>(q), static_cast<uint16_t *>(scale),
                     static_cast<uint4 *>(values));

@@ -144,7 +144,99 @@ def test_infinities_stay_where_they_belong(T, group):
     assert bool(torch.isnan(y[2]).all())
 
 
-SEGMENTS = [[1], [0, 0, 3], [7, 0, 8, 9, 1], [0] * 40 + [1] * 8 + [0, 5] * 16, [40, 17, 0, 64, 130],
+def row_error(x, w):
+    """What rows of x as fp16, each times a power of two, add to the bound: numbers below 2^-28 of
+    the row's largest are off by half a step of fp16's smallest, 2^-25 where that is 2^14 or more."""
+    most = torch.where(torch.isfinite(x), x, torch.zeros_like(x)).abs().amax(1, keepdim=True)
+    return most * 2.0 ** -39 * w.abs().sum(1)
+
+
+@pytest.mark.parametrize("T,N,K", [(8, 264, 16384), (1, 40, 65536), (2500, 136, 160)])
+def test_deep_and_long(T, N, K):
+    """Rows that do not fit beside the codes, and more than are multiplied at a time."""
+    x = randn(91, T, K)
+    q, s = weights(92, N, K, group=64, dtype=BF16)
+    d = moe.linear_desc(T, N, K, moe.MOE_DTYPE_BF16, out_dtype=moe.MOE_DTYPE_FP32)
+    ws = moe.alloc_workspace(d)
+    y = torch.empty(T, N, device="cuda")
+    moe.moe_linear_int4(d, 64, x, q, s, None, None, y, ws)
+    status_ok(ws)
+    w = int4_ref.values(q, s, 64)
+    want, bound = forward_bound(x.double(), w, None, None, "none", FP32)
+    assert_within(y, want, bound + row_error(x.double(), w), "y")
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_rows_of_any_size(T):
+    """Rows from the smallest numbers to the largest, and rows with both."""
+    N, K, group = 136, 544, 128
+    x = randn(93, T, K).float()
+    x[0] *= 2.0 ** -126
+    x[1] *= 2.0 ** 110
+    x[2, ::2] *= 2.0 ** -60
+    x[2, 1::2] *= 2.0 ** 20
+    x = x.to(BF16)
+    if T > 3:
+        x[3] = 0.0
+        x[4] = 2.0 ** -133
+        x[5] = torch.finfo(BF16).max
+        x[5, ::2] = -torch.finfo(BF16).max
+    q, s = weights(94, N, K, group=group, dtype=BF16)
+    d = moe.linear_desc(T, N, K, moe.MOE_DTYPE_BF16, out_dtype=moe.MOE_DTYPE_FP32)
+    ws = moe.alloc_workspace(d)
+    y = torch.empty(T, N, device="cuda")
+    moe.moe_linear_int4(d, group, x, q, s, None, None, y, ws)
+    status_ok(ws)
+    w = int4_ref.values(q, s, group)
+    want, bound = forward_bound(x.double(), w, None, None, "none", FP32)
+    # (sums of the smallest numbers are subnormal: one step of those more for each group)
+    bound = bound + row_error(x.double(), w) + 2.0 ** -148
+    # the largest rows' sums reach 8 x 544 x 2^128 / 4 sqrt(544): what fp32 cannot hold (2^128 less
+    # half a step, and more) rounds to infinity
+    beyond = want.abs() - bound > torch.finfo(FP32).max
+    assert torch.equal(y[beyond], torch.sign(want[beyond]).float() * float("inf"))
+    near = (want.abs() + bound > torch.finfo(FP32).max) & ~beyond
+    y[beyond | near], want[beyond | near] = 0.0, 0.0
+    assert_within(y, want, bound, "y")
+
+
+def test_two_streams():
+    """Two calls at once, each with a workspace of its own."""
+    N, K, group = 1000, 2080, 32
+    q, s = weights(95, N, K, group=group, dtype=FP16)
+    w = int4_ref.values(q, s, group)
+    runs = []
+    for i, T in enumerate((5, 70)):
+        d = moe.linear_desc(T, N, K, moe.MOE_DTYPE_FP16)
+        runs.append((d, randn(96 + i, T, K, dtype=FP16), torch.empty(T, N, dtype=FP16, device="cuda"),
+                     moe.alloc_workspace(d), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for d, x, y, ws, stream in runs:
+            moe.moe_linear_int4(d, group, x, q, s, None, None, y, ws, stream=stream)
+    torch.cuda.synchronize()
+    for d, x, y, ws, _ in runs:
+        status_ok(ws)
+        want, bound = forward_bound(x.double(), w, None, None, "none", FP16)
+        assert_within(y, want, bound, "y")
+
+
+@pytest.mark.parametrize("T", [6, 33])
+def test_runs_give_the_same_bits(T):
+    N, K, group = 4096, 4096, 128
+    x = randn(97, T, K)
+    q, s = weights(98, N, K, group=group, dtype=BF16)
+    d = moe.linear_desc(T, N, K, moe.MOE_DTYPE_BF16, out_dtype=moe.MOE_DTYPE_FP32)
+    ws = moe.alloc_workspace(d)
+    y, again = torch.empty(T, N, device="cuda"), torch.empty(T, N, device="cuda")
+    moe.moe_linear_int4(d, group, x, q, s, None, None, y, ws)
+    for _ in range(5):
+        moe.moe_linear_int4(d, group, x, q, s, None, None, again, ws)
+        assert torch.equal(y, again)
+    status_ok(ws)
+
+
+SEGMENTS = [[700, 3, 0, 1500, 40], [1], [0, 0, 3], [7, 0, 8, 9, 1], [0] * 40 + [1] * 8 + [0, 5] * 16, [40, 17, 0, 64, 130],
             [0, 0, 0]]
 
 

@@ -69,8 +69,8 @@ GroupedGemm grouped_product(const moe_grouped_desc_t &d, const int32_t *offsets,
 bool ok_group(int32_t group) { return group == 32 || group == 64 || group == 128; }
 
 // `rows`: int4_rows_bytes of the workspace.  Up to eight rows of one matrix by the kernel
-// that multiplies where it unpacks, others by way of tcgen05: 14336 x 4096 with 8 rows 14.7
-// and 19.1 us, 114688 x 4096 53 and 74, 14336 x 4096 with 16 rows 25 and 18.7.
+// that multiplies where it unpacks, others by way of tcgen05: 14336 x 4096 with 8 rows 14.4
+// and 17.0 us, 114688 x 4096 51 and 70, 14336 x 4096 with 16 rows 25 and 17.2.
 cudaError_t launch_int4(Int4Gemm g, void *rows, cudaStream_t s) {
   const bool small = g.offsets == nullptr && g.T <= kInt4SmallRows;
   if (small && int4_staged(g)) return launch_int4_small(g, s);

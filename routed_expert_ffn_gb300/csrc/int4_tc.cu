@@ -2,10 +2,12 @@
 // bias) + residual of one matrix, or y_p = W_e x_p for the rows p of each expert e.
 //
 // Bound: HBM for few rows, which reads half a byte for each weight.  To keep up an SM
-// turns 48 codes a clock into 16-bit numbers, nine instructions for a word of eight.  So every weight is unpacked once for all rows of
-// a tile: 128 rows of W are the MMA's M, up to 64 rows of x its N, and the unpacked
-// numbers go to TMEM, where the MMA reads its A operand: through shared memory they would
-// be written and read once more, twice what it moves anyway.
+// turns 48 codes a clock into 16-bit numbers, nine instructions for a word of eight.  So
+// every weight is unpacked once for all rows of a tile: 128 rows of W are the MMA's M, up
+// to 64 rows of x its N, and the unpacked numbers go to TMEM, where the MMA reads its A
+// operand: through shared memory they would be written and read once more, twice what
+// it moves anyway.  What a block costs now is the hand-over between the groups of warps (the
+// MMAs of 256 x 128 codes by 64 rows take 670 clocks of about 1600).
 //
 // The numbers are code - 8, exact in 16 bits, not yet scaled: the sums of one group of
 // columns are an accumulator of their own, which the epilogue's warps multiply by the
@@ -15,12 +17,12 @@
 // Depth goes by units of 256 columns (a row's 128 bytes of codes).  Tiles, and the depth
 // of those that do not fill a round of the SMs, are dealt out as in grouped_pair.cu.
 //
-// CTA = 28 warps, one CTA an SM:
+// CTA, one an SM:
 //   warps 0-7    scale and add the accumulators; the epilogue (32 TMEM lanes each, and
 //                half of the rows of x)
-//   warps 8-23   unpack, four sets of four (32 TMEM lanes each)
-//   warp 24      TMA: codes and rows of x
-//   warp 25      TMEM allocation; one thread issues the MMAs (26 and 27 idle)
+//   then         one or two sets of four warps that unpack (32 TMEM lanes each)
+//   then         a warp for TMA (codes and rows of x), and one for TMEM's allocation, of
+//                which one thread issues the MMAs
 // Every wait is bounded; on expiry the CTA latches the status bit and leaves its loops.
 #include <algorithm>
 
@@ -32,9 +34,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kAddWarps = 8, kUnpackWarps = 16;
-constexpr int kTmaWarp = kAddWarps + kUnpackWarps, kMmaWarp = kTmaWarp + 1;
-constexpr int kThreads = 28 * 32;  // (two warps idle: registers move by fours of warps)
 constexpr int kUnit = 256;
 constexpr uint32_t kCodeBytes = kBM * kUnit / 2;
 constexpr int kMaxStages = 8;
@@ -50,6 +49,13 @@ constexpr int kMaxParts = 16;
 // codes in 680: blocks are as large as TMEM holds twice.
 template <int kGroup, int kN>
 struct Shape {
+  // Sets of four unpacking warps: one is enough where the adding warps have the most to do
+  // (203 rows of 7176 x 2080 in groups of 32: 54 us with two, 50 with one, 60 with four; 32
+  // experts of 4096 x 7168 with 16 rows in groups of 64: 156, 161 and 179).
+  static constexpr int sets = kN == 64 || (kN == 32 && kGroup == 32) ? 1 : 2;
+  static constexpr int add_warps = 8, unpack_warps = 4 * sets;
+  static constexpr int tma_warp = add_warps + unpack_warps, mma_warp = tma_warp + 1;
+  static constexpr int threads = (mma_warp + 1) * 32;
   static constexpr int x_box = kN * 128;  // bytes of 64 columns of x
   static constexpr uint32_t stage = kCodeBytes + kUnit / 64 * x_box;
   static constexpr int stages = kN == 16 ? 8 : (kN == 32 ? 6 : 4);
@@ -122,26 +128,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
-// Registers of a thread, of the 72 that each of the 7 x 128 has: the adding warps hold up to
-// 32 sums and 32 more on their way from TMEM.
-constexpr int kAddRegs = 104, kUnpackRegs = 64, kOtherRegs = 40;
-static_assert(2 * kAddRegs + 4 * kUnpackRegs + kOtherRegs <= 7 * 72, "more would be waited for without end");
 // `and` over the adding warps' 256 threads.
+template <int kCount>
 __device__ __forceinline__ bool add_all(bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred a, b;\n\t"
       "setp.ne.u32 a, %1, 0;\n\t"
-      "bar.red.and.pred b, 1, 256, a;\n\t"
+      "bar.red.and.pred b, 1, %2, a;\n\t"
       "selp.u32 %0, 1, 0, b;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p)
+      : "r"((uint32_t)p), "n"(kCount)
       : "memory");
   return r != 0;
 }
 
 template <int kGroup, int kN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<kGroup, kN>::threads, 1)
     int4_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs a) {
   typedef Shape<kGroup, kN> S;
   typedef RowSchedule<kN, 16, kBM, kMaxParts, 1> Tiles;
@@ -165,22 +168,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kUnpackWarps + 1);
+      mbar_init(&empty[s], S::unpack_warps + 1);
     }
     for (uint32_t b = 0; b < S::bufs; ++b) {
-      mbar_init(&a_full[b], kUnpackWarps);
+      mbar_init(&a_full[b], S::unpack_warps);
       mbar_init(&done[b], 1);
-      mbar_init(&d_empty[b], kAddWarps);
+      mbar_init(&d_empty[b], S::add_warps);
     }
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == S::mma_warp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kTmaWarp && lane == 0) {
+  if (warp == S::tma_warp && lane == 0) {
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.x[0]);
   }
@@ -209,8 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t st = 0, ph = 0;    // stages of codes and rows
   uint32_t buf = 0, bph = 0;  // blocks
 
-  if (warp >= kTmaWarp) fewer_registers<kOtherRegs>();
-  if (warp == kTmaWarp) {
+  if (warp == S::tma_warp) {
     // ------------------------------------------------------ TMA producer --
     uint32_t issued = 0;
     bool ok = true;
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(&full[st], ph);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == S::mma_warp) {
     // ------------------------------------------------------- MMA issuer --
     const uint32_t b_lo = smem_u32(ring + kCodeBytes) >> 4 | kDescLoK;
     bool ok = true;
@@ -277,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (elect_one()) {
+            // (with the TMEM addresses known at compile time blocks took as long)
             const uint32_t d0 = tmem_base + kDCol + buf * S::d_cols, a0 = tmem_base + buf * S::a_cols;
             const uint32_t bd = b_lo + ((st * S::stage + (uint32_t)b * (S::block / 64) * S::x_box) >> 4);
 #pragma unroll
@@ -303,16 +306,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_wait_drain(fin, 0);
     __syncwarp();
-  } else if (warp > kMmaWarp) {
-  } else if (warp >= kAddWarps) {
-    fewer_registers<kUnpackRegs>();
+  } else if (warp >= S::add_warps) {
     // ---------------------------------------------------------- unpackers --
-    // Four sets of four warps, 32 rows to a warp; each set takes a quarter of a block's columns.
+    // 32 rows to a warp; each set takes its share of a block's columns
     const Unpack unpack;
-    const int quad = warp & 3, set = (warp - kAddWarps) >> 2;
+    const int quad = warp & 3, set = (warp - S::add_warps) >> 2;
     const int r = quad * 32 + lane;
-    constexpr int kChunks = S::block / 128;  // of 32 columns, for a set: 2 or 1
-    const uint32_t to = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)set * (S::a_cols / 4);
+    constexpr int kChunks = S::block / 32 / S::sets;  // of 32 columns, for a set
+    const uint32_t to = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)set * (S::a_cols / S::sets);
     bool ok = true;
     for (int i = 0; ok && sch.at(i, &w); ++i) {
       for (int u = w.k0; ok && u < w.k1; ++u) {
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             v[b][c] = *reinterpret_cast<const uint4 *>(
-                row + ((((b * 4 + set) * kChunks + c) ^ (r & 7)) << 4));
+                row + ((((b * S::sets + set) * kChunks + c) ^ (r & 7)) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
         const int blocks = blocks_of(u);
@@ -367,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------- scaling, adding, epilogue --
-    more_registers<kAddRegs>();
     pdl_wait();
     // warps w and w + 4 share 32 TMEM lanes, each half of the rows of x
     constexpr int kHalf = kN / 2;
@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // up to 32 columns on their way at a time: of several groups, or of one
             constexpr int kLoad = kHalf < 16 ? 8 : 16;
+            static_assert(kHalf % kLoad == 0, "columns of a load");
             constexpr int kLoads = S::groups * (kHalf / kLoad);  // of a block
             constexpr int kOnce = kLoads < 32 / kLoad ? kLoads : 32 / kLoad;
 #pragma unroll
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // warps meet at a split tile: all of them leave there, or none
-      if (i < sch.pieces) ok = add_all(ok && !*abort_flag);
+      if (i < sch.pieces) ok = add_all<S::add_warps * 32>(ok && !*abort_flag);
       if (!ok) break;
       bool last = true;
       if (w.parts > 1) {
@@ -467,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < kHalf / 4; ++q)
           __stcg(reinterpret_cast<float4 *>(mine + q * (kBM * 4)),
                  make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
-        add_all(true);
+        add_all<S::add_warps * 32>(true);
         if (threadIdx.x == 0) *last_flag = arrive_last(a.counters + w.tile, w.parts);
-        add_all(true);
+        add_all<S::add_warps * 32>(true);
         last = *last_flag != 0;
         if (last) {
 #pragma unroll
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == S::mma_warp) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);
   }
@@ -582,7 +583,7 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
   const int64_t tiles = ((int64_t)std::min(g.E, rows) + rows / kN) * a.mt;
   const int64_t most = std::min<int64_t>(tiles * std::min(kMaxParts, a.units),
                                          std::min(num_sms(), kMaxCtas));
-  return launch_pdl(kern, dim3((unsigned)most), dim3(kThreads), smem_bytes<kGroup, kN>(g.E), s, maps,
+  return launch_pdl(kern, dim3((unsigned)most), dim3(Shape<kGroup, kN>::threads), smem_bytes<kGroup, kN>(g.E), s, maps,
                     a);
 }
 

@@ -768,7 +768,8 @@ size_t moe_grouped_linear_workspace_size(const moe_grouped_desc_t *d);
  *   x        [R,K] in
  *   offsets  [E+1] int32 in
  *   w        [E,N,K] in, dense
- *   y        [R,N] out; fp32 sums rounded once
+ *   y        [R,N] out; fp32 sums rounded once (fp32 results: sums of 512 products each, added
+ *            in fp32)
  * Limits: 0 <= R <= 2^24, 1 <= E <= 512, 8 <= N, K <= 2^18, both multiples of 8
  * (MOE_ERR_UNSUPPORTED_SHAPE).
  */
@@ -817,9 +818,13 @@ moe_status_t moe_quantize_int4(const void *w, int32_t dtype, int64_t rows, int32
 
 /*
  * moe_linear_int4 -- moe_linear, y = act(x w^T + bias) + residual, with w in 4 bits.
- *   d       as moe_linear's, dtype BF16 or FP16; the workspace too
+ *   d       as moe_linear's, dtype BF16 or FP16; the workspace too (moe_linear_workspace_size)
  *   scale   [N,ceil(K/group)] of type dtype
- * Other arguments as moe_linear.  Made for few rows: W is read once for each 16.
+ * Other arguments as moe_linear.  Made for few rows: W is read and unpacked once for each 64
+ * (groups of 32: 32).  Rows of x are multiplied as fp16, bf16 rows times a power of two
+ * that brings their largest number to 2^14 or more: numbers down to 2^-28 of it are exact,
+ * smaller ones off by 2^-39 of it at most.  Sums are formed under that factor: bf16 scales of
+ * 2^92 or more can overflow where the result would not.
  */
 moe_status_t moe_linear_int4(const moe_linear_desc_t *d, int32_t group, const void *x,
                              const void *q, const void *scale, const void *bias,
@@ -829,7 +834,7 @@ moe_status_t moe_linear_int4(const moe_linear_desc_t *d, int32_t group, const vo
 /*
  * moe_grouped_linear_int4 -- moe_grouped_linear with the experts' matrices in 4 bits.
  *   q       [E,N,K/2], scale [E,N,ceil(K/group)] of type dtype
- * Other arguments as moe_grouped_linear; R <= 2^20.
+ * Other arguments as moe_grouped_linear, rows of x as in moe_linear_int4; R <= 2^20.
  */
 moe_status_t moe_grouped_linear_int4(const moe_grouped_desc_t *d, int32_t group, const void *x,
                                      const int32_t *offsets, const void *q, const void *scale,

@@ -1,5 +1,5 @@
-// Shared by the products with 4-bit weights (int4_small.cu), the quantiser
-// (quantize_int4.cu) and their C ABI (api_grouped.cu).
+// Shared by the products with 4-bit weights (int4_small.cu, int4_tc.cu), the rows that they
+// take (int4_rows.cu), the quantiser (quantize_int4.cu) and their C ABI (api_grouped.cu).
 #pragma once
 
 #include "dense.cuh"
@@ -74,7 +74,7 @@ __device__ __forceinline__ float scale_half(int dtype, uint32_t two, int i) {
 // One shift, four LOP3 and four subtractions; bf16, with seven bits beside the exponent,
 // needs two shifts more, and the logic unit is what limits the unpacking.
 // The constants stay in registers (the compiler does not see what they are): as literals
-// they took two LOP3 and a move each, 25 instructions a word in all instead of %N%.
+// they took two LOP3 and moves, a third of all instructions more.
 struct Unpack {
   uint32_t one_low, one_high, zero_low, zero_high;
   __device__ __forceinline__ Unpack() {

@@ -269,14 +269,16 @@ __global__ void __launch_bounds__(Shape<kGroup, kN>::threads, 1)
     for (int i = 0; ok && sch.at(i, &w); ++i) {
       const uint32_t idesc = idesc_16(MOE_DTYPE_FP16, false, false, kBM, (w.n + 15) & ~15);
       for (int u = w.k0; ok && u < w.k1; ++u) {
-        if (!mbar_wait_warp(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
-          ok = false;
-          break;
-        }
+        const bool rows_there = mbar_test(&full[st], ph);
         const int blocks = blocks_of(u);
         for (int b = 0; b < blocks; ++b) {
-          if (!mbar_wait_warp(&d_empty[buf], bph ^ 1u, abort_flag, a.status, kStatusTimeoutDense) ||
-              !mbar_wait_warp(&a_full[buf], bph, abort_flag, a.status, kStatusTimeoutDense)) {
+          // (the other two have been there for long when the operands come)
+          const bool sums_free = mbar_test(&d_empty[buf], bph ^ 1u);
+          if (!mbar_wait_warp(&a_full[buf], bph, abort_flag, a.status, kStatusTimeoutDense) ||
+              (b == 0 && !mbar_wait_asked(rows_there, &full[st], ph, abort_flag, a.status,
+                                          kStatusTimeoutDense)) ||
+              !mbar_wait_asked(sums_free, &d_empty[buf], bph ^ 1u, abort_flag, a.status,
+                               kStatusTimeoutDense)) {
             ok = false;
             break;
           }
@@ -317,10 +319,10 @@ __global__ void __launch_bounds__(Shape<kGroup, kN>::threads, 1)
     const int r = quad * 32 + lane;
     constexpr int kChunks = S::block / 32 / S::sets;  // of 32 columns, for a set
     const uint32_t to = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)set * (S::a_cols / S::sets);
-    bool ok = true;
+    bool ok = true, codes_there = mbar_test(&full[st], ph), free = mbar_test(&done[buf], bph ^ 1u);
     for (int i = 0; ok && sch.at(i, &w); ++i) {
       for (int u = w.k0; ok && u < w.k1; ++u) {
-        if (!mbar_wait_warp(&full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
+        if (!mbar_wait_asked(codes_there, &full[st], ph, abort_flag, a.status, kStatusTimeoutDense)) {
           ok = false;
           break;
         }
@@ -334,12 +336,17 @@ __global__ void __launch_bounds__(Shape<kGroup, kN>::threads, 1)
                 row + ((((b * S::sets + set) * kChunks + c) ^ (r & 7)) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
+        if (++st == (uint32_t)kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+        codes_there = mbar_test(&full[st], ph);
         const int blocks = blocks_of(u);
 #pragma unroll
         for (int b = 0; b < S::blocks; ++b) {
           if (b < blocks) {
             // (the operands before these are multiplied)
-            if (!mbar_wait_warp(&done[buf], bph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
+            if (!mbar_wait_asked(free, &done[buf], bph ^ 1u, abort_flag, a.status, kStatusTimeoutDense)) {
               ok = false;
               break;
             }
@@ -353,19 +360,17 @@ __global__ void __launch_bounds__(Shape<kGroup, kN>::threads, 1)
               unpack(v[b][c].w, o + 12);
               tmem_st16(to + buf * S::a_cols + (uint32_t)c * 16, o);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[buf]);
+            const uint32_t mine = buf;
             if (++buf == S::bufs) {
               buf = 0;
               bph ^= 1u;
             }
+            free = mbar_test(&done[buf], bph ^ 1u);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&a_full[mine]);
           }
-        }
-        if (++st == (uint32_t)kStages) {
-          st = 0;
-          ph ^= 1u;
         }
       }
     }
@@ -403,6 +408,9 @@ __global__ void __launch_bounds__(Shape<kGroup, kN>::threads, 1)
       float acc[kHalf];
 #pragma unroll
       for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
+      // asked for now, used at the tile's end: lane j's is that of row j
+      const float factor =
+          lane < kHalf && half + lane < w.n ? a.factor[w.b0 - a.first + half + lane] : 1.f;
       for (int u = w.k0; ok && u < w.k1; ++u) {
         float scales[kUnit / kGroup];
         auto take = [&](UnitScales<kGroup, kUnit> &s) {
@@ -494,10 +502,9 @@ __global__ void __launch_bounds__(Shape<kGroup, kN>::threads, 1)
         }
       }
       const int n = w.a0 + quad * 32 + lane;
-      if (last && n < a.N) {
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j)
-          if (half + j < w.n) acc[j] *= a.factor[w.b0 - a.first + half + j];
+      for (int j = 0; j < kHalf; ++j) acc[j] *= __shfl_sync(0xffffffffu, factor, j);
+      if (last && n < a.N) {
         const bool wide = a.out_dtype == MOE_DTYPE_FP32;
         auto load = [&](const void *p, int64_t at) {
           return wide ? static_cast<const float *>(p)[at]

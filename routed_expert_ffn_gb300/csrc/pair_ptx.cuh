@@ -58,6 +58,25 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity,
                                                uint32_t code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, code));
 }
+// Whether phase `parity` is complete, not waiting for it.  Even an answer of yes takes some 100
+// clocks; one asked for early is there when mbar_wait_asked wants it.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait_warp, with mbar_test's answer.
+__device__ __forceinline__ bool mbar_wait_asked(bool there, uint64_t *bar, uint32_t parity,
+                                                volatile int *abort_flag, uint32_t *status,
+                                                uint32_t code) {
+  return __all_sync(0xffffffffu, there) || mbar_wait_warp(bar, parity, abort_flag, status, code);
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");

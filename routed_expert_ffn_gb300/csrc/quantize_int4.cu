@@ -26,9 +26,9 @@ constexpr float kFine = 192.f, kWhole = 12582912.f + 8.f - 192.f;  // 1.5 * 2^7,
 
 template <int kGroup, bool kValues>
 __global__ void __launch_bounds__(kThreads)
-    quantize_int4_kernel(const uint4 *__restrict__ w, int dtype, int64_t total, int per_row,
+    quantize_int4_kernel(const uint4 *w, int dtype, int64_t total, int per_row,
                          uint32_t magic, int in_row, uint32_t *__restrict__ q,
-                         uint16_t *__restrict__ scale, uint4 *__restrict__ values) {
+                         uint16_t *__restrict__ scale, uint4 *values) {  // (values may be w)
   constexpr int kLanes = kGroup / 8;
   pdl_wait();
   pdl_launch_dependents();

@@ -225,3 +225,17 @@ def test_one_workspace_for_all():
     want, bound = forward_bound(x.double(), int4_ref.values(q[3], s[3], group), None, None, "none", BF16)
     assert_within(ys[2], want, bound, "4 bits")
     assert_within(ys[3][o[3]:o[4]], want[o[3]:o[4]], bound[o[3]:o[4]], "4 bits, expert 3")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows,K", [(3, 96), (1000, 2080), (20000, 4096)])
+def test_values_in_place(rows, K, group, dtype):
+    """The values written over the weights: as beside them."""
+    w = randn(71, rows, K, std=K ** -0.5, dtype=dtype)
+    q = [torch.empty(rows, K // 2, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = [torch.empty(rows, -(-K // group), dtype=dtype, device="cuda") for _ in range(2)]
+    v = torch.empty_like(w)
+    moe.moe_quantize_int4(w, rows, K, group, q[0], s[0], v)
+    moe.moe_quantize_int4(w, rows, K, group, q[1], s[1], w)
+    assert torch.equal(q[0], q[1]) and torch.equal(s[0], s[1]) and torch.equal(v, w)

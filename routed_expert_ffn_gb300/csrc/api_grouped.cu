@@ -72,6 +72,7 @@ bool ok_group(int32_t group) { return group == 32 || group == 64 || group == 128
 // that multiplies where it unpacks, others by way of tcgen05: 14336 x 4096 with 8 rows 14.4
 // and 17.0 us, 114688 x 4096 51 and 70, 14336 x 4096 with 16 rows 25 and 17.2.
 cudaError_t launch_int4(Int4Gemm g, void *rows, cudaStream_t s) {
+  if (g.offsets != nullptr && int4_few(g)) return launch_int4_small(g, s);
   const bool small = g.offsets == nullptr && g.T <= kInt4SmallRows;
   if (small && int4_staged(g)) return launch_int4_small(g, s);
   float *factor = reinterpret_cast<float *>(at(rows, (size_t)std::min(g.T, kInt4Rows) * int4_pitch(g.K) * 2));

@@ -165,6 +165,7 @@ constexpr int kInt4Rows = 1024;
 // Up to eight rows of one matrix (int4_small.cu); more, or an expert's (int4_tc.cu).
 constexpr int kInt4SmallRows = 8;
 cudaError_t launch_int4_small(const Int4Gemm &g, cudaStream_t s);
+bool int4_few(const Int4Gemm &g);     // whether launch_int4_small is to take the experts' rows
 bool int4_staged(const Int4Gemm &g);  // whether launch_int4_small makes the rows itself
 cudaError_t launch_int4_tc(const Int4Gemm &g, cudaStream_t s);
 // Bytes of `part`, and of rows and their factors.

@@ -26,6 +26,7 @@
 // (4.8 TB/s).
 #include <algorithm>
 
+#include "grouped.cuh"
 #include "int4.cuh"
 
 namespace moe {
@@ -52,6 +53,10 @@ struct SmallArgs {
   const void *bias, *residual;
   void *y;
   int64_t ldx, ldr, ldy;
+  // experts: T is the most rows of a pass, `tiles` those of a matrix
+  const int32_t *offsets;
+  int R, E;
+  uint32_t *status;
 };
 
 __device__ __forceinline__ void copy_codes(uint32_t to, const uint8_t *from) {
@@ -74,15 +79,15 @@ __device__ __forceinline__ int k_of(int t, int i) {
 // and 64 more, so that two rows' pieces lie in different banks.
 __host__ __device__ constexpr int staged_pitch(int chunks) { return chunks * 256 + 64; }
 
-// The T rows of x to shared memory as launch_int4_rows makes them, in that order; their
+// `rows` rows of x from row `first_row` on to shared memory as launch_int4_rows makes them, in that order; their
 // factors to `factor`.  The warps share the rows evenly.
 template <int kGroup>
-__device__ __forceinline__ void stage_rows(const SmallArgs &a, uint8_t *to, float *factor,
-                                           float *most) {
-  const int per = a.T == 1 ? kWarps : (a.T == 2 ? kWarps / 2 : (a.T <= 4 ? kWarps / 4 : kWarps / 8));
+__device__ __forceinline__ void stage_rows(const SmallArgs &a, int64_t first_row, int rows,
+                                           uint8_t *to, float *factor, float *most) {
+  const int per = rows == 1 ? kWarps : (rows == 2 ? kWarps / 2 : (rows <= 4 ? kWarps / 4 : kWarps / 8));
   const int warp = threadIdx.x >> 5, r = warp / per, first = warp % per * 32 + (threadIdx.x & 31);
-  const bool mine = r < a.T;
-  const uint4 *row = reinterpret_cast<const uint4 *>(a.x + (int64_t)(mine ? r : 0) * a.ldx * 2);
+  const bool mine = r < rows;
+  const uint4 *row = reinterpret_cast<const uint4 *>(a.x + (first_row + (mine ? r : 0)) * a.ldx * 2);
   float up = 1.f;
   if (a.dtype == MOE_DTYPE_BF16) {
     float m = 0.f;
@@ -131,20 +136,25 @@ __device__ __forceinline__ void store(const SmallArgs &a, float v, int n, int64_
 // rounding, by `threads` threads; a function of its own, as it is not worth a copy in each
 // place.
 template <int kWarpRows>
-__device__ __noinline__ void finish(const SmallArgs &a, int n0, const float *red,
-                                    const float *factors, int from, int cols, int thread,
-                                    int threads) {
+__device__ __noinline__ void finish(const SmallArgs &a, int n0, int64_t first_row, int rows,
+                                    const float *red, const float *factors, int from, int cols,
+                                    int thread, int threads) {
   constexpr int kCols = 16 * kWarpRows, kSplit = kWarps / kWarpRows;
-  for (int j = thread; j < cols * a.T; j += threads) {
+  for (int j = thread; j < cols * rows; j += threads) {
     const int c = from + j % cols, r = j / cols, n = n0 + c;
     float v = 0.f;
 #pragma unroll
     for (int s = 0; s < kSplit; ++s) v += red[(s * kRows + r) * (kCols + 1) + c];
-    if (n < a.N) store(a, v * factors[r], n, r);
+    if (n < a.N) store(a, v * factors[r], n, first_row + r);
   }
 }
 
-template <int kGroup, int kWarpRows, bool kStaged>
+// Passes over an expert's matrix: up to `most` of its rows each.
+__host__ __device__ __forceinline__ int passes(int rows, int most) { return (rows + most - 1) / most; }
+
+// kExperts: tiles of every pass of every expert in turn, a stretch of them to each CTA, which
+// stages an expert's rows (kStaged) when it comes to them.
+template <int kGroup, int kWarpRows, bool kStaged, bool kExperts>
 __global__ void __launch_bounds__(kThreads, 1)
     int4_small_kernel(const __grid_constant__ SmallArgs a) {
   constexpr int kCols = 16 * kWarpRows, kSplit = kWarps / kWarpRows;
@@ -159,6 +169,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   // it, so that the codes are there
   if (kStaged) pdl_wait();
   pdl_launch_dependents();
+  const int32_t *seg = reinterpret_cast<const int32_t *>(staged + a.T * staged_pitch(a.chunks));
+  const int32_t *first = seg + a.E + 1;
+  int tile = blockIdx.x, end = a.tiles, step = gridDim.x;
+  if constexpr (kExperts) {
+    make_tables(a.offsets, a.E, a.R, 0, a.R, const_cast<int32_t *>(seg), const_cast<int32_t *>(first),
+                a.status, [&](int m) { return passes(m, a.T) * a.tiles; });
+    __syncthreads();
+    const int64_t total = first[a.E];
+    tile = (int)(total * blockIdx.x / gridDim.x);
+    end = (int)(total * (blockIdx.x + 1) / gridDim.x);
+    step = 1;
+    if (tile == end) return;
+  }
+  // The expert of a tile, from that of one before it on, and the tile's first row of W.
+  auto expert_at = [&](int tile, int e) {
+    if (kExperts)
+      while (first[e + 1] <= tile) ++e;
+    return e;
+  };
+  auto n_of = [&](int tile, int e) {
+    return (kExperts ? (tile - first[e]) % a.tiles : tile) * kCols;
+  };
+  const int e0 = kExperts ? expert_of(first, a.E, tile) : 0;
 
   // this warp's chunks of a tile, [c0, c0 + count)
   const int per = (a.chunks + kSplit - 1) / kSplit, c0 = part * per;
@@ -170,18 +203,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A lane's 16 bytes lie in the ring where a quad's words can be read without bank conflicts.
   const uint32_t ring = smem_u32(dyn) + warp * (kAhead * 1024);
   const uint32_t put = ring + (g * 4 + (t ^ ((g >> 1) & 3))) * 16;
-  int ask_tile = blockIdx.x, to_ask = 0;
+  int ask_tile = tile, ask_e = e0, to_ask = 0;
   uint32_t ask_slot = 0;
   const uint8_t *q = nullptr;
   int down = 0;
   auto ask = [&]() {
-    if (to_ask == 0 && count > 0 && ask_tile < a.tiles) {
-      const int n = ask_tile * kCols + 16 * wr + g;
+    if (to_ask == 0 && count > 0 && ask_tile < end) {
+      ask_e = expert_at(ask_tile, ask_e);
+      const int n = n_of(ask_tile, ask_e) + 16 * wr + g;
       const int n0 = min(n, a.N - 1), n1 = min(n + 8, a.N - 1);
-      q = a.q + (int64_t)n0 * (a.K >> 1) + c0 * (kChunk / 2) + 16 * t;
+      q = a.q + ((int64_t)ask_e * a.N + n0) * (a.K >> 1) + c0 * (kChunk / 2) + 16 * t;
       down = (n1 - n0) * (a.K >> 1);
       to_ask = count;
-      ask_tile += gridDim.x;
+      ask_tile += step;
     }
     if (to_ask > 0) {
       if (to_ask > 1 || !skips) {
@@ -199,15 +233,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Scales, eight groups at a time, one such block ahead: lane l holds four of row l / 2.
   constexpr int kBlock = 8 * kGroup / kChunk;  // chunks: 8, 4 or 2
-  int scale_tile = blockIdx.x, scale_at = 0;   // group of the warp's range
+  int scale_tile = tile, scale_e = e0, scale_at = 0;  // group of the warp's range
   const int range = count > 0 ? min(count * (kChunk / kGroup), a.groups - c0 * (kChunk / kGroup)) : 0;
   const uint16_t *sc = nullptr;
   uint32_t next[4] = {};  // (as they come: whatever is done with them waits for them)
   auto ask_scales = [&]() {
-    if (scale_tile >= a.tiles || range == 0) return;
-    if (scale_at == 0)
-      sc = a.scale + (int64_t)min(scale_tile * kCols + 16 * wr + (lane >> 1), a.N - 1) * a.groups +
-           c0 * (kChunk / kGroup) + (lane & 1) * 4;
+    if (scale_tile >= end || range == 0) return;
+    if (scale_at == 0) {
+      scale_e = expert_at(scale_tile, scale_e);
+      const int n = min(n_of(scale_tile, scale_e) + 16 * wr + (lane >> 1), a.N - 1);
+      sc = a.scale + ((int64_t)scale_e * a.N + n) * a.groups + c0 * (kChunk / kGroup) + (lane & 1) * 4;
+    }
     const int have = range - scale_at - (lane & 1) * 4;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -218,13 +254,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     scale_at += 8;
     if (scale_at >= range) {
       scale_at = 0;
-      scale_tile += gridDim.x;
+      scale_tile += step;
     }
   };
   ask_scales();
 
-  if (kStaged) {
-    stage_rows<kGroup>(a, staged, factors, most);
+  // the rows at hand: row `g` is this lane's; past the last one the sums are not used, and row 0
+  // will do
+  int64_t row0 = 0;
+  int rows = a.T;
+  if (kExperts) {
+    // (see below)
+  } else if (kStaged) {
+    stage_rows<kGroup>(a, 0, rows, staged, factors, most);
   } else {
     pdl_wait();
     if (threadIdx.x < a.T) factors[threadIdx.x] = a.factor[threadIdx.x];
@@ -233,14 +275,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const Unpack unpack;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  int tile = blockIdx.x, i = 0;
+  int i = 0, e = e0, n0 = 0, staged_to = -1;
   uint32_t turn = 0, slot = 0;
-  // this lane's row of x, from this warp's first chunk on; past the last row the sums are not
-  // used: row 0 will do
-  const int row = g < a.T ? g : 0;
-  const uint8_t *const x0 = kStaged ? staged + row * staged_pitch(a.chunks) + t * 16 + c0 * 256
-                                    : a.x + ((int64_t)row * a.pitch + c0 * kChunk) * 2;
-  const uint8_t *xp = x0;
+  auto row_of_lane = [&]() {
+    const int row = g < rows ? g : 0;
+    return kStaged ? staged + row * staged_pitch(a.chunks) + t * 16 + c0 * 256
+                   : a.x + ((int64_t)row * a.pitch + c0 * kChunk) * 2;
+  };
+  const uint8_t *x0 = row_of_lane(), *xp = x0;  // from this warp's first chunk on
+  // By all threads, before a tile: its first row of W, and its rows of x.
+  auto open = [&]() {
+    e = expert_at(tile, e);
+    n0 = n_of(tile, e);
+    if (kExperts && tile >= staged_to) {
+      const int pass = (tile - first[e]) / a.tiles;
+      staged_to = first[e] + (pass + 1) * a.tiles;
+      row0 = seg[e] + (int64_t)pass * a.T;
+      rows = min(a.T, seg[e + 1] - (int)row0);
+      __syncthreads();  // (everybody is done with the rows before)
+      stage_rows<kGroup>(a, row0, rows, staged, factors, most);
+      __syncthreads();
+      x0 = row_of_lane();
+    }
+    xp = x0;
+  };
 
   // The tile's sums: of this warp alone, or of all that share its rows.
   auto close = [&]() {
@@ -252,21 +310,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kSplit == 1) {
       __syncwarp();
-      finish<kWarpRows>(a, tile * kCols, red[turn], factors, 16 * wr, 16, lane, 32);
+      finish<kWarpRows>(a, n0, row0, rows, red[turn], factors, 16 * wr, 16, lane, 32);
     } else {
       __syncthreads();
-      finish<kWarpRows>(a, tile * kCols, red[turn], factors, 0, kCols, threadIdx.x, kThreads);
+      finish<kWarpRows>(a, n0, row0, rows, red[turn], factors, 0, kCols, threadIdx.x, kThreads);
     }
     turn ^= 1u;  // the other buffer was read before everybody arrived here
-    tile += gridDim.x;
-    xp = x0;
+    tile += step;
   };
 
   if (count == 0) {
-    while (tile < a.tiles) close();
+    while (tile < end) {
+      open();
+      close();
+    }
     return;
   }
-  while (tile < a.tiles) {
+  while (tile < end) {
+    if (i == 0) open();
     float scales[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) scales[k] = unpack16(a.dtype, next[k]).x;
@@ -354,20 +415,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <int kGroup, int kWarpRows, bool kStaged>
+// Experts' rows of a pass: as many as are staged.
+int pass_rows(const Int4Gemm &g) {
+  const int fit = (int)(kStagedBytes / staged_pitch((g.K + kChunk - 1) / kChunk));
+  return std::min(std::min(g.T, kRows), fit);
+}
+
+template <int kGroup, int kWarpRows, bool kStaged, bool kExperts>
 cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
-  auto kern = int4_small_kernel<kGroup, kWarpRows, kStaged>;
+  auto kern = int4_small_kernel<kGroup, kWarpRows, kStaged, kExperts>;
   static std::atomic<bool> allowed[64];
-  const cudaError_t e = allow_smem(kern, kRingBytes + kStagedBytes, allowed);
+  const size_t tables = kExperts ? (size_t)2 * (g.E + 1) * 4 : 0;
+  const cudaError_t e = allow_smem(kern, kRingBytes + kStagedBytes + 2 * (kMaxE + 1) * 4, allowed);
   if (e != cudaSuccess) return e;
   SmallArgs a = {};
-  a.T = g.T;
+  a.T = kExperts ? pass_rows(g) : g.T;
   a.N = g.N;
   a.K = g.K;
   a.tiles = (g.N + 16 * kWarpRows - 1) / (16 * kWarpRows);
   a.chunks = (g.K + kChunk - 1) / kChunk;
   a.groups = (g.K + kGroup - 1) / kGroup;
   a.pitch = int4_pitch(g.K);
+  a.offsets = g.offsets;
+  a.R = g.T;
+  a.E = g.E;
+  a.status = g.status;
   a.dtype = g.dtype;
   a.out_dtype = g.out_dtype;
   a.act = g.act;
@@ -381,8 +453,9 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
   a.ldx = g.ldx;
   a.ldr = g.ldr;
   a.ldy = g.ldy;
-  const size_t smem = kRingBytes + (kStaged ? (size_t)g.T * staged_pitch(a.chunks) : 0);
-  return launch_pdl(kern, dim3((unsigned)std::min(a.tiles, num_sms())), dim3(kThreads), smem, s, a);
+  const size_t smem = kRingBytes + (kStaged ? (size_t)a.T * staged_pitch(a.chunks) : 0) + tables;
+  const int64_t tiles = kExperts ? ((int64_t)std::min(g.E, g.T) + g.T / a.T) * a.tiles : a.tiles;
+  return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(tiles, num_sms())), dim3(kThreads), smem, s, a);
 }
 
 // The rows of a tile that take the least time: whole rounds of the SMs' tiles, each as long
@@ -391,9 +464,9 @@ int warp_rows(const Int4Gemm &g) {
   const int chunks = (g.K + kChunk - 1) / kChunk;
   int best = 1;
   double least = 0;
-  for (int wr = 1; wr <= kWarps; wr *= 2) {
-    const int tiles = (g.N + 16 * wr - 1) / (16 * wr);
-    const int rounds = (tiles + num_sms() - 1) / num_sms();
+  for (int wr = g.offsets != nullptr ? 4 : 1; wr <= kWarps; wr *= 2) {
+    const int64_t tiles = (int64_t)((g.N + 16 * wr - 1) / (16 * wr)) * std::min(g.E, g.T);
+    const int rounds = (int)((tiles + num_sms() - 1) / num_sms());
     const int split = kWarps / wr;
     const double us = (double)rounds * ((chunks + split - 1) / split + (split > 1 ? 0.6 : 0.2));
     if (least == 0 || us < least) {
@@ -404,20 +477,21 @@ int warp_rows(const Int4Gemm &g) {
   return best;
 }
 
-template <int kGroup, bool kStaged>
+template <int kGroup, bool kStaged, bool kExperts>
 cudaError_t by_rows(const Int4Gemm &g, cudaStream_t s) {
-  switch (warp_rows(g)) {
-    case 1: return start<kGroup, 1, kStaged>(g, s);
-    case 2: return start<kGroup, 2, kStaged>(g, s);
-    case 4: return start<kGroup, 4, kStaged>(g, s);
-    case 8: return start<kGroup, 8, kStaged>(g, s);
-    default: return start<kGroup, 16, kStaged>(g, s);
+  const int wr = warp_rows(g);
+  if constexpr (!kExperts) {
+    if (wr == 1) return start<kGroup, 1, kStaged, false>(g, s);
+    if (wr == 2) return start<kGroup, 2, kStaged, false>(g, s);
   }
+  if (wr == 4) return start<kGroup, 4, kStaged, kExperts>(g, s);
+  if (wr == 8) return start<kGroup, 8, kStaged, kExperts>(g, s);
+  return start<kGroup, 16, kStaged, kExperts>(g, s);
 }
-template <bool kStaged>
+template <bool kStaged, bool kExperts>
 cudaError_t by_group(const Int4Gemm &g, cudaStream_t s) {
-  if (g.group == 32) return by_rows<32, kStaged>(g, s);
-  return g.group == 64 ? by_rows<64, kStaged>(g, s) : by_rows<128, kStaged>(g, s);
+  if (g.group == 32) return by_rows<32, kStaged, kExperts>(g, s);
+  return g.group == 64 ? by_rows<64, kStaged, kExperts>(g, s) : by_rows<128, kStaged, kExperts>(g, s);
 }
 
 }  // namespace
@@ -426,8 +500,14 @@ bool int4_staged(const Int4Gemm &g) {
   return (size_t)g.T * staged_pitch((g.K + kChunk - 1) / kChunk) <= kStagedBytes;
 }
 
+bool int4_few(const Int4Gemm &g) {
+  const int most = pass_rows(g);
+  return g.T <= most || (g.T + g.E - 1) / g.E <= most / 2;
+}
+
 cudaError_t launch_int4_small(const Int4Gemm &g, cudaStream_t s) {
-  return int4_staged(g) ? by_group<true>(g, s) : by_group<false>(g, s);
+  if (g.offsets != nullptr) return by_group<true, true>(g, s);
+  return int4_staged(g) ? by_group<true, false>(g, s) : by_group<false, false>(g, s);
 }
 
 }  // namespace moe

@@ -69,8 +69,8 @@ GroupedGemm grouped_product(const moe_grouped_desc_t &d, const int32_t *offsets,
 bool ok_group(int32_t group) { return group == 32 || group == 64 || group == 128; }
 
 // `rows`: int4_rows_bytes of the workspace.  Up to eight rows of one matrix by the kernel
-// that multiplies where it unpacks, others by way of tcgen05: 14336 x 4096 with 8 rows 14.4
-// and 17.0 us, 114688 x 4096 51 and 70, 14336 x 4096 with 16 rows 25 and 17.2.
+// that multiplies where it unpacks (experts': int4_few), others by way of tcgen05: 14336 x 4096
+// with 8 rows 13.5 and 16.9 us, 114688 x 4096 51 and 68; groups of 32 16.7 and 18.1, 81 and 75.
 cudaError_t launch_int4(Int4Gemm g, void *rows, cudaStream_t s) {
   if (g.offsets != nullptr && int4_few(g)) return launch_int4_small(g, s);
   const bool small = g.offsets == nullptr && g.T <= kInt4SmallRows;

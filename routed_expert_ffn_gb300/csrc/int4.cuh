@@ -162,7 +162,7 @@ __device__ __forceinline__ uint4 row_piece(uint4 v, int dtype, float up) {
 // At most this many rows at a time: the workspace holds them.
 constexpr int kInt4Rows = 1024;
 
-// Up to eight rows of one matrix (int4_small.cu); more, or an expert's (int4_tc.cu).
+// Up to eight rows of one matrix, or few rows of experts (int4_small.cu); others (int4_tc.cu).
 constexpr int kInt4SmallRows = 8;
 cudaError_t launch_int4_small(const Int4Gemm &g, cudaStream_t s);
 bool int4_few(const Int4Gemm &g);     // whether launch_int4_small is to take the experts' rows

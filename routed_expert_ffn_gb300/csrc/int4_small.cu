@@ -1,4 +1,5 @@
-// Products with 4-bit weights and up to eight rows (decode): y = act(x W^T + bias) + residual.
+// Products with 4-bit weights and few rows (decode): y = act(x W^T + bias) + residual of up to
+// eight rows, or y_p = W_e x_p where experts have few rows each.
 //
 // Bound: HBM, which reads half a byte for each weight; next to it the instructions that
 // unpack the codes, nine for a word of eight (int4.cuh).  Every weight is unpacked once
@@ -22,8 +23,15 @@
 // fit, kStaged, every CTA makes them for itself while its first codes are under way, which
 // saves a launch.
 //
+// Experts: a pass takes up to eight of an expert's rows (as many as are staged); each CTA
+// works through a stretch of all passes' tiles, which lie in the order of the experts, and stages
+// rows when it comes to the next pass.
+//
 // Measured: 4096 x 4096 with one row 5.9 us, 14336 x 4096 with eight 14.3, 114688 x 4096 51
-// (4.8 TB/s).
+// (4.8 TB/s); 32 rows over 29 experts of 4096 x 1536 33.4 (2.9 TB/s: launch, offsets and first
+// codes take 7, the fullest CTA's tiles a seventh more than the average's).  Scales twice as far
+// ahead (groups of 64 and 32) and tiles finished one tile later, so that nobody waits for the
+// slowest warp, gave nothing.
 #include <algorithm>
 
 #include "grouped.cuh"
@@ -263,10 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // will do
   int64_t row0 = 0;
   int rows = a.T;
-  if (kExperts) {
-    // (see below)
-  } else if (kStaged) {
-    stage_rows<kGroup>(a, 0, rows, staged, factors, most);
+  if (kStaged) {
+    if (!kExperts) stage_rows<kGroup>(a, 0, rows, staged, factors, most);  // (else as they come)
   } else {
     pdl_wait();
     if (threadIdx.x < a.T) factors[threadIdx.x] = a.factor[threadIdx.x];
@@ -459,7 +465,9 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
 }
 
 // The rows of a tile that take the least time: whole rounds of the SMs' tiles, each as long
-// as its warps' chunks and about 0.6 chunks for its end.
+// as its warps' chunks and about 0.6 chunks for its end.  Experts': as if all had rows; 29 of 128
+// experts of 4096 x 1536 take 39.6 us in tiles of 64 rows, 33.4 of 128 and 34.8 of 256 (51 of 32,
+// which are left out).
 int warp_rows(const Int4Gemm &g) {
   const int chunks = (g.K + kChunk - 1) / kChunk;
   int best = 1;
@@ -490,7 +498,9 @@ cudaError_t by_rows(const Int4Gemm &g, cudaStream_t s) {
 }
 template <bool kStaged, bool kExperts>
 cudaError_t by_group(const Int4Gemm &g, cudaStream_t s) {
-  if (g.group == 32) return by_rows<32, kStaged, kExperts>(g, s);
+  if constexpr (!kExperts) {
+    if (g.group == 32) return by_rows<32, kStaged, false>(g, s);
+  }
   return g.group == 64 ? by_rows<64, kStaged, kExperts>(g, s) : by_rows<128, kStaged, kExperts>(g, s);
 }
 
@@ -500,7 +510,14 @@ bool int4_staged(const Int4Gemm &g) {
   return (size_t)g.T * staged_pitch((g.K + kChunk - 1) / kChunk) <= kStagedBytes;
 }
 
+// Experts' rows: here, or by way of tcgen05, which takes up to 32 rows in a pass.  128 experts of
+// 4096 x 1536, groups of 128: 8 rows over all of them 12.4 and 18.6 us, 32 rows 30.1 and 35.2, 128
+// rows 70.6 and 89.3, 512 rows 115 and 136.  32 experts of 4096 x 7168, where five rows fit a pass,
+// groups of 64: 64 rows 108 and 118 us, 128 rows 145 and 129.  Groups of 32 have four times
+// the scales to bring to their lanes: 64 experts of 1536 x 4096 with 8 rows 19.7 and 18.2 us, with 64
+// rows 60 and 46.
 bool int4_few(const Int4Gemm &g) {
+  if (g.group == 32) return false;
   const int most = pass_rows(g);
   return g.T <= most || (g.T + g.E - 1) / g.E <= most / 2;
 }

@@ -24,9 +24,11 @@
 //   then         a warp for TMA (codes and rows of x), and one for TMEM's allocation, of
 //                which one thread issues the MMAs
 // Every wait is bounded; on expiry the CTA latches the status bit and leaves its loops.
+// A wait takes some 100 clocks even when what it waits for is there, and each role of a block
+// has two or three in a row: those that can be are asked for ahead (mbar_test).
 //
-// Measured: 14336 x 4096 with 16 rows 17 us, with 64 23, with 256 49; 29 experts of 4096 x 1536
-// with a row each 38 us, 32 experts of 4096 x 7168 with 16 rows 152 to 156 (3.3 TB/s).
+// Measured: 14336 x 4096 with 16 rows 17 us, with 64 22, with 256 44; 32 experts of 4096 x 7168
+// with 16 rows on average 149 us (3.4 TB/s).
 #include <algorithm>
 
 #include "grouped.cuh"
@@ -53,8 +55,8 @@ constexpr int kMaxParts = 16;
 template <int kGroup, int kN>
 struct Shape {
   // Sets of four unpacking warps: one is enough where the adding warps have the most to do
-  // (203 rows of 7176 x 2080 in groups of 32: 54 us with two, 50 with one, 60 with four; 32
-  // experts of 4096 x 7168 with 16 rows in groups of 64: 156, 161 and 179).
+  // (203 rows of 7176 x 2080 in groups of 32: 53 us with two, 50 with one, 57 with four; 32
+  // experts of 4096 x 7168 with 16 rows in groups of 64: 150, 158 and 190).
   static constexpr int sets = kN == 64 || (kN == 32 && kGroup == 32) ? 1 : 2;
   static constexpr int add_warps = 8, unpack_warps = 4 * sets;
   static constexpr int tma_warp = add_warps + unpack_warps, mma_warp = tma_warp + 1;
@@ -599,8 +601,8 @@ cudaError_t start(const Int4Gemm &g, cudaStream_t s) {
 
 // Rows of a tile: what one pass takes.  Experts' rows vary, so that half of the most that an
 // even spread gives 16 of would take two passes: 32 experts of 4096 x 7168 with 16 rows
-// on average take 179 us in tiles of up to 32, 215 in tiles of 16 and 252 in tiles of 64; a
-// matrix of 14336 x 4096 with 16 rows 20.9, 18.7 and 23.9.
+// on average take 149 us in tiles of up to 32, 190 in tiles of 16 and 202 in tiles of 64; a
+// matrix of 14336 x 4096 with 16 rows 17.8 and 16.7 us in tiles of 32 and 16.
 template <int kGroup>
 cudaError_t by_rows(const Int4Gemm &g, cudaStream_t s) {
   const int rows = (g.T + g.E - 1) / g.E;

@@ -239,3 +239,41 @@ def test_values_in_place(rows, K, group, dtype):
     moe.moe_quantize_int4(w, rows, K, group, q[0], s[0], v)
     moe.moe_quantize_int4(w, rows, K, group, q[1], s[1], w)
     assert torch.equal(q[0], q[1]) and torch.equal(s[0], s[1]) and torch.equal(v, w)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (FP16, FP32)])
+@pytest.mark.parametrize("group", [64, 128])
+@pytest.mark.parametrize("E,N,K", [(64, 264, 544), (40, 1000, 7168), (64, 136, 17952), (512, 40, 32)])
+def test_few_rows_and_all_of_one(E, N, K, group, dtype, out):
+    """Few rows on average, all of them or most with one expert: several passes over its matrix."""
+    wide = torch.full((E + 9, K + 8), float("nan"), dtype=dtype, device="cuda")
+    wide[3:3 + E, :K] = randn(81, E, K, dtype=dtype)
+    x = wide[:, :K]
+    q, s = weights(82, E, N, K, group=group, dtype=dtype)
+    d = moe.grouped_desc(E + 9, E, N, K, moe.dtype_of(wide), out_dtype=moe.MOE_DTYPE_FP32 if out == FP32 else None,
+                         x_stride=K + 8, y_stride=N + 16)
+    ws = moe.alloc_workspace(d)
+    for counts in ([0] * (E // 2) + [E] + [0] * (E - E // 2 - 1), [1] + [0] * (E - 2) + [E - 1],
+                   [E - 12] + [11, 1] + [0] * (E - 3), [1] * E):
+        off, o = offsets_of(counts, 3)
+        yw = torch.full((E + 9, N + 16), 3.0, dtype=out, device="cuda")
+        y = yw[:, :N]
+        moe.moe_grouped_linear_int4(d, group, x, off, q, s, y, ws)
+        status_ok(ws)
+        for e in [e for e in range(E) if counts[e]][:6]:
+            rows = slice(o[e], o[e + 1])
+            want, bound = forward_bound(x[rows].double(), int4_ref.values(q[e], s[e], group), None, None,
+                                        "none", out)
+            assert_within(y[rows], want, bound, f"expert {e}")
+        assert bool((yw[:3] == 3).all()) and bool((yw[3 + E:] == 3).all()) and bool((yw[:, N:] == 3).all())
+    y0 = y.clone()
+    for bad in ([-1] + [4] * E, [0, 9] + [8] * (E - 1), [0] * E + [E + 10]):
+        y.fill_(5.0)
+        moe.moe_workspace_init(ws)
+        moe.moe_grouped_linear_int4(d, group, x, torch.tensor(bad, dtype=torch.int32, device="cuda"), q, s, y, ws)
+        st, _ = moe.moe_get_device_status(ws)
+        assert st != moe.MOE_OK and bool((y == 5).all())
+    moe.moe_workspace_init(ws)
+    moe.moe_grouped_linear_int4(d, group, x, off, q, s, y, ws)
+    status_ok(ws)
+    assert torch.equal(y[3:3 + E], y0[3:3 + E])

@@ -48,9 +48,10 @@ __device__ __forceinline__ int expert_of(const int32_t *first, int E, int tile) 
   return l;
 }
 
-// The offsets (null: all T rows of one matrix), as far as they lie in rows [low, high), to seg [E+1], and the prefix sums of
-// tiles(rows of an expert) to first [E+1], in shared memory; by all threads of the
-// block, which meet afterwards.  Offsets that do not hold make no tiles, and a status bit.
+// The offsets (null: all T rows of one matrix), as far as they lie in rows [low, high), to
+// seg [E+1], and the prefix sums of tiles(rows of an expert) to first [E+1], in shared
+// memory; by all threads of the block, which meet afterwards.  Offsets that do not hold make
+// no tiles, and a status bit.
 template <typename Tiles>
 __device__ __forceinline__ void make_tables(const int32_t *offsets, int E, int T, int low, int high,
                                             int32_t *seg, int32_t *first, uint32_t *status,
